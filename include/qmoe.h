@@ -79,6 +79,19 @@ typedef enum {
     QMOE_Q6_K = 5
 } qmoe_qtype;
 
+/* Element types beside F32: activations, outputs and unblocked weights, and
+ * e4m3 (8-bit float: 4 exponent and 3 significand bits, largest value 448, one
+ * NaN code, no infinity), whose scales lie in a separate array:
+ *   of rows (activations)  [rows][ceil(cols/128)] f32, one per row and 128
+ *                          columns
+ *   of a matrix (weights)  [ceil(rows/128)][ceil(cols/128)] f32, one per
+ *                          128 x 128 block; a stack holds its matrices' scales
+ *                          one after another
+ * An element's value is its e4m3 value times its scale. */
+#define QMOE_BF16 32
+#define QMOE_F16 33
+#define QMOE_E4M3 34
+
 typedef enum {
     QMOE_OK = 0,
     QMOE_ERR_INVALID_ARGUMENT = 1, /* null pointer, bad size, misalignment, small workspace */
@@ -291,12 +304,110 @@ qmoe_status moe_ffn_noalloc(const float* router_W, const void* gate_stack, const
                             const void* down_stack, const qmoe_moe_shape* shape, const float* x,
                             float* residual, int32_t* topk_idx, float* topk_w, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Products of e4m3, bf16 and f16 weights, and the experts of an MoE layer in
+ * e4m3.  The pages have no counterpart of these calls: they are additions of
+ * this library for checkpoints whose weights are not GGUF blocks.  Unlike the
+ * calls above, they order every operand by the stream, weights included (they
+ * may be the output of an earlier call on the stream), and a call with no
+ * rows returns QMOE_OK without touching anything.  They run on the current
+ * device, need no workspace unless one is named, and may be captured into a
+ * graph.  Same inputs, same bits: no sum depends on timing. */
+
+/* Rows to e4m3 with one scale per 128 columns:
+ *   s = the smallest 2^k, k >= -126, with max|x| <= 448 * 2^k over the block's
+ *       finite elements (1 if they are all 0);  q = x / s, rounded to nearest
+ *       even (the division is exact)
+ * A NaN or an infinity becomes the NaN code and leaves its block's scale to the
+ * finite elements.
+ *   xtype   QMOE_F32, QMOE_BF16 or QMOE_F16
+ *   x       [rows][cols], rows ldx elements apart (ldx >= cols), aligned to its
+ *           element (16-byte aligned rows and cols % 8 == 0 run fastest)
+ *   q       [rows][cols] e4m3, contiguous;  scale  [rows][ceil(cols/128)] f32
+ *   rows    >= 0;  cols  1..2^20
+ * q and scale must not overlap x.
+ * Errors: INVALID_ARGUMENT (null, sizes, alignment), UNSUPPORTED (xtype, too
+ * large, device), CUDA. */
+qmoe_status f8_quantize(int xtype, const void* x, int64_t rows, int64_t cols, int64_t ldx, void* q,
+                        float* scale, void* stream);
+
+/* y[t][i] = sum_j W[i][j] x[t][j] with e4m3 operands and block scales:
+ *   sum_b x_scale[t][b] w_scale[i/128][b] * (sum over the 128 columns of block
+ *   b of the codes' products)
+ * The inner sums run on the tensor cores, products exact and sums in f32; the
+ * outer sum is f32, and y is rounded once.  The product of two scales is
+ * formed in f32 first, so it has to be finite there.  For
+ * a few tokens the CTAs of a cluster share a row tile's K range and their
+ * parts are added in a fixed order.
+ *   W        [rows][cols] e4m3, contiguous, 16-byte aligned;  w_scale f32
+ *   rows     1..2^31-257;  cols  1..2^20, a multiple of 16 (else UNSUPPORTED)
+ *   x        [n_tokens][cols] e4m3, rows ldx apart (ldx >= cols, a multiple of
+ *            16), 16-byte aligned;  x_scale [n_tokens][ceil(cols/128)] f32
+ *   ytype    QMOE_F32, QMOE_BF16 or QMOE_F16
+ *   y        [n_tokens][rows], rows ldy elements apart (ldy >= rows); elements
+ *            between rows are left as they were
+ * y must not overlap an input.
+ * Errors as f8_quantize; QMOE_ERR_TIMEOUT from qmoe_device_status if a device
+ * wait ran out. */
+qmoe_status f8_mm(const void* W, const float* w_scale, int64_t rows, int64_t cols, const void* x,
+                  const float* x_scale, int64_t n_tokens, int64_t ldx, int ytype, void* y,
+                  int64_t ldy, void* stream);
+
+/* y[r] = W_g x[r] for the rows r of group g, offsets[g] <= r < offsets[g+1].
+ *   wtype    type of W and x: QMOE_E4M3 (as f8_mm), QMOE_BF16 or QMOE_F16
+ *            (products exact, sums in f32; w_scale and x_scale null)
+ *   W        [num_groups][rows][cols], contiguous;  num_groups 1..1024
+ *   cols     a multiple of 16 bytes, as is ldx
+ *   n_rows   rows of x and y
+ *   offsets  [num_groups + 1] int32 on the device, not decreasing, within
+ *            [0, n_rows]; groups may be empty, and rows of y before offsets[0]
+ *            or from offsets[num_groups] on are left as they were.  Offsets
+ *            that break this are clamped (no access leaves the arrays), and
+ *            qmoe_device_status reports INVALID_ARGUMENT.
+ * Other arguments, rules and errors as f8_mm. */
+qmoe_status mm_grouped(int wtype, const void* W, const float* w_scale, int32_t num_groups,
+                       int64_t rows, int64_t cols, const void* x, const float* x_scale,
+                       int64_t n_rows, int64_t ldx, const int32_t* offsets, int ytype, void* y,
+                       int64_t ldy, void* stream);
+
+/* Bytes of workspace moe_experts_f8 needs; 0 (with a message) for a shape it
+ * refuses. */
+size_t moe_experts_f8_workspace_size(const qmoe_moe_shape* shape);
+
+/* The experts of an MoE layer with e4m3 stacks, for given routes:
+ *   xq = f8_quantize(x_t);  for each slot s with e = topk_idx[t][s] in [0, E):
+ *   a = silu(G_e xq) * (U_e xq) in f32,  aq = f8_quantize(a),
+ *   out_t = residual_t + sum_s topk_w[t][s] * (D_e aq)
+ * with sums in f32 and one rounding into out.  topk_idx and topk_w are as
+ * moe_ffn returns them; any other routing rule may supply them.
+ *   gate_stack, up_stack  [E][F][H] e4m3;  scales [E][F/128][H/128]
+ *   down_stack            [E][H][F] e4m3;  scales [E][H/128][F/128]
+ *   shape       hidden and expert_dim multiples of 128, num_experts <= 256,
+ *               top_k <= 16 (it may exceed num_experts), n_tokens >= 0, the three
+ *               qtypes QMOE_E4M3, route_flags 0
+ *   xtype       type of x, residual and out: QMOE_F32, QMOE_BF16 or QMOE_F16
+ *   x           [T][H], contiguous
+ *   topk_idx    [T][k] int32; a slot outside [0, E) adds nothing (padding); an
+ *               expert may appear twice
+ *   topk_w      [T][k] f32, used as given
+ *   residual    [T][H], or NULL for zeros;  out [T][H], may be residual itself
+ *   ws          >= moe_experts_f8_workspace_size bytes, scratch; calls that
+ *               overlap on the GPU must not share one (nor may two graphs that
+ *               are replayed at the same time)
+ * Stacks, x, residual, out and ws 16-byte aligned.  Errors as f8_mm. */
+qmoe_status moe_experts_f8(const void* gate_stack, const float* gate_scale, const void* up_stack,
+                           const float* up_scale, const void* down_stack, const float* down_scale,
+                           const qmoe_moe_shape* shape, int xtype, const void* x,
+                           const int32_t* topk_idx, const float* topk_w, const void* residual,
+                           void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word: QMOE_ERR_TIMEOUT if a bounded device wait expired since the last
  * read (a pipeline stage, or a grid barrier that not every CTA reached);
  * QMOE_ERR_UNSUPPORTED if the many-token MoE path met a decoded gate/up
  * weight outside f16 range, or a quantized product met an activation of
- * magnitude 2^106 or more (the output is then not valid); QMOE_ERR_CUDA if
+ * magnitude 2^106 or more (the output is then not valid);
+ * QMOE_ERR_INVALID_ARGUMENT if mm_grouped met bad offsets; QMOE_ERR_CUDA if
  * the stream reported an error, or if an internal invariant of the routing
  * failed (an expert index outside [0, E) was clamped to 0); else QMOE_OK. */
 qmoe_status qmoe_device_status(void* stream);

@@ -27,6 +27,9 @@ QTYPES = {"F32": F32, "Q8_0": Q8_0, "Q4_0": Q4_0, "Q4_K": Q4_K, "Q5_K": Q5_K, "Q
 BLOCK_ELEMS = {F32: 1, Q8_0: 32, Q4_0: 32, Q4_K: 256, Q5_K: 256, Q6_K: 256}
 BLOCK_BYTES = {F32: 4, Q8_0: 34, Q4_0: 18, Q4_K: 144, Q5_K: 176, Q6_K: 210}
 
+# element types beside F32
+BF16, F16, E4M3 = 32, 33, 34
+
 # qmoe_status
 OK, ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT = 0, 1, 2, 3, 4
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARGUMENT", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT"}
@@ -34,7 +37,7 @@ STATUS_NAMES = {0: "OK", 1: "INVALID_ARGUMENT", 2: "UNSUPPORTED", 3: "CUDA", 4: 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-ftz=false",
               "-std=c++17", "-Xcompiler", "-fPIC"]
 # Translation units of libqmoe.so, compiled in parallel and linked together.
-UNITS = ("qmoe.cu", "batch.cu")
+UNITS = ("qmoe.cu", "batch.cu", "f8.cu")
 
 
 class QmoeError(RuntimeError):
@@ -114,6 +117,13 @@ SIGNATURES = {
     "moe_ffn_rmsnorm_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(_Shape)]),
     "moe_ffn_rmsnorm": (ctypes.c_int, [_P, _P, _P, _P, ctypes.POINTER(_Shape), _P, ctypes.c_float,
                                        _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "f8_quantize": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, _P, _P, _P]),
+    "f8_mm": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _I64, ctypes.c_int, _P, _I64, _P]),
+    "mm_grouped": (ctypes.c_int, [ctypes.c_int, _P, _P, ctypes.c_int32, _I64, _I64, _P, _P, _I64,
+                                  _I64, _P, ctypes.c_int, _P, _I64, _P]),
+    "moe_experts_f8_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(_Shape)]),
+    "moe_experts_f8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.POINTER(_Shape),
+                                      ctypes.c_int, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "qmoe_device_status": (ctypes.c_int, [_P]),
     "qmoe_set_exec_mode": (ctypes.c_int, [ctypes.c_int]),
     "qmoe_set_fault_injection": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_int]),
@@ -253,6 +263,112 @@ def moe_ffn_noalloc(router_W, gate_stack, up_stack, down_stack, shape: _Shape, x
     _check(lib().moe_ffn_noalloc(_ptr(router_W), _ptr(gate_stack), _ptr(up_stack),
                                  _ptr(down_stack), ctypes.byref(shape), _ptr(x), _ptr(residual),
                                  _ptr(topk_idx), _ptr(topk_w), _stream(stream)))
+
+
+# ------------------------------- e4m3 / bf16 / f16 products (include/qmoe.h)
+_DTYPES = {}
+
+
+def _arg(fn: str, name: str, t, kind: int, need: int):
+    """Address of a device array of at least `need` elements of type `kind`.
+
+    Integers (addresses) and None pass through unchecked; a tensor must live
+    on the current CUDA device, have the element type the call names (one-byte
+    types for E4M3) and reach `need` elements from its first one."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if not _DTYPES:
+        _DTYPES.update({F32: (torch.float32,), BF16: (torch.bfloat16,), F16: (torch.float16,),
+                        E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8),
+                        "i32": (torch.int32,)})
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise QmoeError(ERR_INVALID_ARGUMENT,
+                        f"{fn}: {name} is on {t.device}, not on the current CUDA device")
+    want = _DTYPES.get(kind)
+    if want is not None and t.dtype not in want:
+        raise QmoeError(ERR_INVALID_ARGUMENT, f"{fn}: {name} has dtype {t.dtype}, not {want[0]}")
+    have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if have < need:
+        raise QmoeError(ERR_INVALID_ARGUMENT,
+                        f"{fn}: {name} holds {have} elements, {need} are needed")
+    return t.data_ptr()
+
+
+def _span(rows: int, cols: int, ld: int) -> int:
+    return (rows - 1) * ld + cols if rows > 0 else 0
+
+
+def f8_blocks(n: int) -> int:
+    """Blocks of 128 that cover n elements (scales per row, or per column)."""
+    return -(-n // 128)
+
+
+def f8_quantize(xtype: int, x, rows: int, cols: int, q, scale, ldx=None, stream=None) -> None:
+    """q, scale = e4m3 rows of x with one scale per 128 columns (see include/qmoe.h)."""
+    fn, ldx = "f8_quantize", cols if ldx is None else ldx
+    _check(lib().f8_quantize(xtype, _arg(fn, "x", x, xtype, _span(rows, cols, ldx)), rows, cols,
+                             ldx, _arg(fn, "q", q, E4M3, rows * cols),
+                             _arg(fn, "scale", scale, F32, rows * f8_blocks(cols)),
+                             _stream(stream)))
+
+
+def f8_mm(W, w_scale, rows: int, cols: int, x, x_scale, n_tokens: int, ytype: int, y, ldx=None,
+          ldy=None, stream=None) -> None:
+    """y = x W^T with e4m3 operands and block scales (see include/qmoe.h)."""
+    fn, kb = "f8_mm", f8_blocks(cols)
+    ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
+    _check(lib().f8_mm(_arg(fn, "W", W, E4M3, rows * cols),
+                       _arg(fn, "w_scale", w_scale, F32, f8_blocks(rows) * kb), rows, cols,
+                       _arg(fn, "x", x, E4M3, _span(n_tokens, cols, ldx)),
+                       _arg(fn, "x_scale", x_scale, F32, n_tokens * kb), n_tokens, ldx, ytype,
+                       _arg(fn, "y", y, ytype, _span(n_tokens, rows, ldy)), ldy,
+                       _stream(stream)))
+
+
+def mm_grouped(wtype: int, W, w_scale, num_groups: int, rows: int, cols: int, x, x_scale,
+               n_rows: int, offsets, ytype: int, y, ldx=None, ldy=None, stream=None) -> None:
+    """y[r] = W_g x[r] for the rows of every group (see include/qmoe.h)."""
+    fn, kb = "mm_grouped", f8_blocks(cols)
+    ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
+    _check(lib().mm_grouped(wtype, _arg(fn, "W", W, wtype, num_groups * rows * cols),
+                            _arg(fn, "w_scale", w_scale, F32, num_groups * f8_blocks(rows) * kb),
+                            num_groups, rows, cols,
+                            _arg(fn, "x", x, wtype, _span(n_rows, cols, ldx)),
+                            _arg(fn, "x_scale", x_scale, F32, n_rows * kb), n_rows, ldx,
+                            _arg(fn, "offsets", offsets, "i32", num_groups + 1), ytype,
+                            _arg(fn, "y", y, ytype, _span(n_rows, rows, ldy)), ldy,
+                            _stream(stream)))
+
+
+def moe_experts_f8_workspace_size(shape: _Shape) -> int:
+    n = int(lib().moe_experts_f8_workspace_size(ctypes.byref(shape)))
+    if n == 0:
+        raise QmoeError(ERR_INVALID_ARGUMENT, last_error())
+    return n
+
+
+def moe_experts_f8(gate_stack, gate_scale, up_stack, up_scale, down_stack, down_scale,
+                   shape: _Shape, xtype: int, x, topk_idx, topk_w, residual, out, ws,
+                   ws_bytes=None, stream=None) -> None:
+    """out = residual + the routed experts' weighted outputs (see include/qmoe.h)."""
+    fn = "moe_experts_f8"
+    H, F, E = shape.hidden, shape.expert_dim, shape.num_experts
+    T, P = shape.n_tokens, shape.n_tokens * shape.top_k
+    blocks = E * f8_blocks(F) * f8_blocks(H)
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size()
+    _check(lib().moe_experts_f8(
+        _arg(fn, "gate_stack", gate_stack, E4M3, E * F * H),
+        _arg(fn, "gate_scale", gate_scale, F32, blocks),
+        _arg(fn, "up_stack", up_stack, E4M3, E * F * H),
+        _arg(fn, "up_scale", up_scale, F32, blocks),
+        _arg(fn, "down_stack", down_stack, E4M3, E * H * F),
+        _arg(fn, "down_scale", down_scale, F32, blocks), ctypes.byref(shape), xtype,
+        _arg(fn, "x", x, xtype, T * H), _arg(fn, "topk_idx", topk_idx, "i32", P),
+        _arg(fn, "topk_w", topk_w, F32, P), _arg(fn, "residual", residual, xtype, T * H),
+        _arg(fn, "out", out, xtype, T * H), _arg(fn, "ws", ws, None, 0), ws_bytes,
+        _stream(stream)))
 
 
 # qmoe_set_exec_mode

@@ -1,0 +1,533 @@
+// gmm.cuh — matrix products grouped by expert on the 5th-generation tensor
+// cores: y[r] = x[r] W_e^T for the rows r of group e, W an [E][N][K] stack of
+// row-major matrices, in f16, bf16, or e4m3 with f32 scales (x: one per row
+// and 128 columns; W: one per 128 x 128 block).  One matrix is the case of
+// one group.
+//
+// Orientation: the weight rows are the MMA's M side (128 of them = the 128
+// TMEM lanes), the token rows its N side.  A group of n rows then costs
+// about n / 16 of an N side in steps of 16, down to one token, with the
+// weights streamed once per token tile; and the epilogue's stores run along
+// a row of y.
+//
+// Scales.  With sx[r][b] and sw[e][n/128][b] for k-block b,
+//   y[r][n] = sum_b sx sw sum_{k in b} xq Wq.
+// The tensor core forms the inner sum of one k-block exactly as products
+// and in f32 as sums; the epilogue warps then add (sx sw) * partial to f32
+// registers while the tensor core works on the next block (two TMEM
+// buffers).  f16/bf16 products accumulate in TMEM over the whole of K.
+//
+// Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs,
+// warps 2-3 stage the scale products, warps 4-11 are the epilogue: warp w
+// reads TMEM lanes 32 (w % 4) .. +31, and the two groups of four warps take
+// alternate runs of columns.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "f8.cuh"
+#include "gmm_tiles.cuh"
+#include "ptx.cuh"
+#include "umma.cuh"
+
+namespace qmoe {
+namespace gmm {
+
+constexpr int TILE_W = 128;    // weight rows per tile
+constexpr int KBLK = 128;      // bytes of K per stage and operand row
+constexpr int THREADS = 384;
+constexpr int EPI_WARPS = 8;
+constexpr int SC_BLK = 4;      // k-blocks of scales staged at a time
+constexpr int SC_RING = 3;     // such stages
+
+enum OutType : int { OUT_F32 = 0, OUT_BF16 = 1, OUT_F16 = 2 };
+
+struct Params {
+    const int32_t* offsets;  // [E+1] rows of each group, or null: one group of all rows
+    const float* xs;         // [M][kb] scales of x (e4m3)
+    const float* ws;         // [E][nb][kb] scales of W (gate)
+    const float* ws2;        // [E][nb][kb] scales of the second matrix (up)
+    void* y;                 // [M][ldy]
+    uint8_t* aq;             // SwiGLU form: [M][N] e4m3 activations
+    float* as;               //              [M][nb] their scales
+    int64_t ldy;
+    int M, N, E;
+    int kb;                  // 128-byte blocks of K
+    int nb;                  // 128-row tiles of W
+    int out;                 // OutType
+    uint32_t idesc;          // instruction descriptor without N
+    DevCtl* err;
+};
+
+// Configuration of one instantiation.
+//   F8     e4m3 operands with scales (else 16-bit)
+//   NT     largest token tile (columns)
+//   NST    pipeline stages
+//   GU     two weight stacks (gate, up) and the SwiGLU + e4m3 epilogue
+//   SPLIT  the CTAs of a cluster share a tile's K range and add their parts
+template <bool F8_, int NT_, int NST_, bool GU_, bool SPLIT_>
+struct Cfg {
+    static constexpr bool F8 = F8_, GU = GU_, SPLIT = SPLIT_;
+    static constexpr int NT = NT_, NST = NST_;
+    static constexpr int NA = GU ? 2 : 1;
+    static constexpr int BOX = NT < 64 ? NT : 64;  // token rows per TMA box
+    static constexpr int A_BYTES = TILE_W * KBLK;
+    static constexpr int B_BYTES = NT * KBLK;
+    static constexpr int STAGE = NA * A_BYTES + B_BYTES;
+    static constexpr int CH = NT >= 64 ? 32 : 16;  // columns per TMEM load
+    static constexpr int NCH = NT / CH / 2;        // such runs per epilogue warp
+    static constexpr int TM_BUF = NA * NT;         // TMEM columns per buffer
+    static constexpr int TM_COLS = 2 * TM_BUF < 32 ? 32 : 2 * TM_BUF;
+    static constexpr int SC_STAGE = SC_BLK * NA * NT;  // floats
+    // byte offsets in shared memory
+    static constexpr int O_SC = NST * STAGE;
+    static constexpr int O_PART = O_SC + (F8 ? SC_RING * SC_STAGE * 4 : 0);
+    static constexpr int O_AMAX = O_PART + (SPLIT ? NT * TILE_W * 4 : 0);
+    static constexpr int O_BAR = O_AMAX + (GU ? 2 * 4 * NT * 4 : 0);
+    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 4 + 1;
+    static constexpr int O_TAB = O_BAR + (N_BAR + 1) * 8;
+    // tables: first row, end row and first tile of each group, total last
+    static constexpr int smem(int E) { return 1024 + O_TAB + (3 * E + 4) * 4; }
+    static_assert(NT % (2 * CH) == 0 && NT <= 256 && TM_COLS <= 512, "tile shape");
+    static_assert((TM_COLS & (TM_COLS - 1)) == 0, "TMEM columns: a power of two");
+};
+
+// acc += v * s on pairs (one packed FMA).
+__device__ __forceinline__ void fma2(float& a0, float& a1, float v0, float v1, float s0,
+                                     float s1) {
+    asm("{\n\t.reg .b64 a, v, s;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\t"
+        "fma.rn.f32x2 a, v, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(v0), "f"(v1), "f"(s0), "f"(s1));
+}
+
+template <class C>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[C::CH]) {
+    if constexpr (C::CH == 32)
+        umma::ld_32x32b_x32(addr, r);
+    else
+        umma::ld_32x32b_x16(addr, r);
+}
+
+__device__ __forceinline__ void store_out(void* y, int64_t i, int type, float v) {
+    if (type == OUT_BF16)
+        static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
+    else if (type == OUT_F16)
+        static_cast<__half*>(y)[i] = __float2half_rn(v);
+    else
+        static_cast<float*>(y)[i] = v;
+}
+
+template <class C>
+__global__ void __launch_bounds__(THREADS, 1)
+    gmm_kernel(const Params p, const __grid_constant__ CUtensorMap tm_w,
+               const __grid_constant__ CUtensorMap tm_w2,
+               const __grid_constant__ CUtensorMap tm_x) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* ring = reinterpret_cast<float*>(base + C::O_SC);
+    float* part = reinterpret_cast<float*>(base + C::O_PART);
+    uint32_t* amax = reinterpret_cast<uint32_t*>(base + C::O_AMAX);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::O_BAR);
+    uint64_t* full = bars;
+    uint64_t* empty = full + C::NST;
+    uint64_t* sc_full = empty + C::NST;
+    uint64_t* sc_empty = sc_full + SC_RING;
+    uint64_t* acc_full = sc_empty + SC_RING;  // [2]
+    uint64_t* acc_empty = acc_full + 2;       // [2]
+    uint64_t* mma_done = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BAR);
+    int* t_lo = reinterpret_cast<int*>(base + C::O_TAB);
+    int* t_hi = t_lo + p.E;
+    int* t_pre = t_hi + p.E;  // [E+1]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == 1) umma::tmem_alloc(tmem_slot, C::TM_COLS);
+    if (tid == 0) {
+        for (int i = 0; i < C::NST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < SC_RING; ++i) {
+            mbar_init(&sc_full[i], 2);
+            mbar_init(&sc_empty[i], EPI_WARPS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], EPI_WARPS);
+        }
+        mbar_init(mma_done, 1);
+        fence_barrier_init();
+    }
+    // Every operand may be an earlier launch's output (weights quantised on
+    // this stream too), so nothing is read before the dependency wait.
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) {
+        // group tables; offsets are clamped into [0, M], so that no value of
+        // theirs forms an address outside x or y
+        int total = 0;
+        bool bad = false;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            int lo = 0, hi = 0;
+            if (e < p.E) {
+                if (p.offsets) {
+                    bad |= !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M,
+                                       &lo, &hi);
+                } else {
+                    hi = p.M;
+                }
+            }
+            const int n = group_tiles(hi - lo, C::NT, p.nb);
+            int s = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += v;
+            }
+            if (e < p.E) {
+                t_lo[e] = lo;
+                t_hi[e] = hi;
+                t_pre[e] = total + s - n;
+            }
+            total += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) t_pre[p.E] = total;
+        if (bad) record_error(p.err, DEV_GMM_OFFSETS);
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const int tiles = t_pre[p.E];
+
+    // tiles first, first + step, ...; with SPLIT a cluster has one tile and
+    // each of its CTAs a share of K
+    int first = blockIdx.x, step = gridDim.x, kbeg = 0, kend = p.kb;
+    uint32_t rank = 0, ranks = 1;
+    if constexpr (C::SPLIT) {
+        rank = cluster_rank();
+        ranks = cluster_size();
+        first = blockIdx.x / ranks;
+        step = tiles > 0 ? tiles : 1;
+        kbeg = static_cast<int>(rank * p.kb / ranks);
+        kend = static_cast<int>((rank + 1) * p.kb / ranks);
+    }
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- loads
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += step) {
+                const Tile w = tile_at(t, C::NT, t_lo, t_hi, t_pre, p.E);
+                const int boxes = (w.np + C::BOX - 1) / C::BOX;
+                for (int kb = kbeg; kb < kend; ++kb, ++it) {
+                    const int s = it % C::NST, round = it / C::NST;
+                    if (round > 0 &&
+                        !mbar_wait_bounded(&empty[s], (round - 1) & 1, p.err, DEV_GMM_TIMEOUT)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = base + s * C::STAGE;
+                    mbar_arrive_expect_tx(&full[s],
+                                          C::NA * C::A_BYTES + boxes * C::BOX * KBLK);
+                    // x coordinates are multiples of 128 bytes; rows past the
+                    // matrix or past x arrive as zeros
+                    const int kx = C::F8 ? kb * KBLK : kb * (KBLK / 2);
+                    tma_load_3d(st, &tm_w, kx, w.nbi * TILE_W, w.e, &full[s]);
+                    if constexpr (C::GU)
+                        tma_load_3d(st + C::A_BYTES, &tm_w2, kx, w.nbi * TILE_W, w.e, &full[s]);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(st + C::NA * C::A_BYTES + b * C::BOX * KBLK, &tm_x, kx,
+                                    w.row0 + b * C::BOX, &full[s]);
+                }
+            }
+            // never leave with copies in flight
+            for (int k = max(it - C::NST, 0); k < it; ++k)
+                mbar_wait_bounded(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        if (lane == 0) {
+            int it = 0, ab = 0;  // stage and accumulator-buffer counters
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += step) {
+                const Tile w = tile_at(t, C::NT, t_lo, t_hi, t_pre, p.E);
+                const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
+                for (int kb = kbeg; kb < kend; ++kb, ++it) {
+                    const bool fresh = C::F8 || kb == kbeg;  // a new accumulator buffer
+                    if (fresh && ab >= 2 &&
+                        !mbar_wait_bounded(&acc_empty[ab & 1], ((ab >> 1) - 1) & 1, p.err,
+                                           DEV_GMM_TIMEOUT)) {
+                        ok = false;
+                        break;
+                    }
+                    const int s = it % C::NST;
+                    if (!mbar_wait_bounded(&full[s], (it / C::NST) & 1, p.err, DEV_GMM_TIMEOUT)) {
+                        ok = false;
+                        break;
+                    }
+                    umma::fence_after_sync();
+                    const uint32_t st = smem_u32(base + s * C::STAGE);
+                    const uint32_t d = tmem + (ab & 1) * C::TM_BUF;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint64_t db = umma::desc_sw128(st + C::NA * C::A_BYTES + 32 * j);
+                        const uint32_t acc = (!fresh || j > 0) ? 1u : 0u;
+#pragma unroll
+                        for (int a = 0; a < C::NA; ++a) {
+                            const uint64_t da = umma::desc_sw128(st + a * C::A_BYTES + 32 * j);
+                            if constexpr (C::F8)
+                                umma::mma_f8(d + a * C::NT, da, db, idesc, acc);
+                            else
+                                umma::mma_f16(d + a * C::NT, da, db, idesc, acc);
+                        }
+                    }
+                    umma::commit(&empty[s]);
+                    if (C::F8 || kb == kend - 1) {
+                        umma::commit(&acc_full[ab & 1]);
+                        ++ab;
+                    }
+                }
+            }
+            // every MMA has finished before TMEM and the stages are given up
+            umma::commit(mma_done);
+            mbar_wait_bounded(mma_done, 0, p.err, DEV_GMM_TIMEOUT);
+        }
+    } else if (warp < 4) {
+        // --------------------------------------------------------- scales
+        if constexpr (C::F8) {
+            const int lt = tid - 64;  // 0..63: token rows lt, lt + 64, ...
+            constexpr int RPT = (C::NT + 63) / 64;
+            // rows of scales are read four at a time where they are aligned
+            const bool vec = (p.kb & 3) == 0 && (kbeg & 3) == 0 &&
+                             (reinterpret_cast<uintptr_t>(p.xs) & 15) == 0;
+            int ch = 0;
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += step) {
+                const Tile w = tile_at(t, C::NT, t_lo, t_hi, t_pre, p.E);
+                const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + w.nbi) * p.kb;
+                for (int k0 = kbeg; k0 < kend; k0 += SC_BLK, ++ch) {
+                    float v[RPT][SC_BLK], g[C::NA][SC_BLK];
+#pragma unroll
+                    for (int b = 0; b < SC_BLK; ++b) {
+                        g[0][b] = k0 + b < kend ? __ldg(p.ws + wo + k0 + b) : 0.f;
+                        if constexpr (C::GU)
+                            g[1][b] = k0 + b < kend ? __ldg(p.ws2 + wo + k0 + b) : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < RPT; ++i) {
+                        const int j = lt + 64 * i;
+                        const float* src = p.xs + static_cast<int64_t>(w.row0 + j) * p.kb + k0;
+                        if (vec && j < w.nv && k0 + SC_BLK <= kend) {
+                            const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
+                            v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < SC_BLK; ++b)
+                                v[i][b] = j < w.nv && k0 + b < kend ? __ldcg(src + b) : 0.f;
+                        }
+                    }
+                    const int s = ch % SC_RING, round = ch / SC_RING;
+                    if (round > 0 && !mbar_wait_bounded(&sc_empty[s], (round - 1) & 1, p.err,
+                                                        DEV_GMM_TIMEOUT)) {
+                        ok = false;
+                        break;
+                    }
+                    float* dst = ring + s * C::SC_STAGE;
+#pragma unroll
+                    for (int i = 0; i < RPT; ++i) {
+                        const int j = lt + 64 * i;
+                        if (j < C::NT)
+#pragma unroll
+                            for (int b = 0; b < SC_BLK; ++b)
+#pragma unroll
+                                for (int a = 0; a < C::NA; ++a)
+                                    dst[(b * C::NA + a) * C::NT + j] = v[i][b] * g[a][b];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[s]);
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------- epilogue
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t tm_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        int ab = 0, ch = 0, par = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step, par ^= 1) {
+            const Tile w = tile_at(t, C::NT, t_lo, t_hi, t_pre, p.E);
+            float acc[C::NA][C::NCH][C::CH];
+#pragma unroll
+            for (int a = 0; a < C::NA; ++a)
+#pragma unroll
+                for (int i = 0; i < C::NCH; ++i)
+#pragma unroll
+                    for (int c = 0; c < C::CH; ++c) acc[a][i][c] = 0.f;
+            const int periods = C::F8 ? kend - kbeg : 1;
+            for (int k = 0; k < periods; ++k, ++ab) {
+                const float* sc = nullptr;
+                if constexpr (C::F8) {
+                    const int s = ch % SC_RING;
+                    if ((k % SC_BLK) == 0 && !mbar_wait_bounded(&sc_full[s], (ch / SC_RING) & 1,
+                                                                p.err, DEV_GMM_TIMEOUT)) {
+                        ok = false;
+                        break;
+                    }
+                    sc = ring + s * C::SC_STAGE + (k % SC_BLK) * C::NA * C::NT;
+                }
+                if (!mbar_wait_bounded(&acc_full[ab & 1], (ab >> 1) & 1, p.err,
+                                       DEV_GMM_TIMEOUT)) {
+                    ok = false;
+                    break;
+                }
+                umma::fence_after_sync();
+#pragma unroll
+                for (int a = 0; a < C::NA; ++a)
+#pragma unroll
+                    for (int i = 0; i < C::NCH; ++i) {
+                        const int col = (2 * i + half) * C::CH;
+                        if (col < w.np) {
+                            uint32_t r[C::CH];
+                            tmem_ld<C>(tm_lane + (ab & 1) * C::TM_BUF + a * C::NT + col, r);
+                            umma::wait_ld(r);
+                            if constexpr (C::F8) {
+                                const float4* s4 =
+                                    reinterpret_cast<const float4*>(sc + a * C::NT + col);
+#pragma unroll
+                                for (int c = 0; c < C::CH; c += 4) {
+                                    const float4 s = s4[c / 4];
+                                    fma2(acc[a][i][c], acc[a][i][c + 1], __uint_as_float(r[c]),
+                                         __uint_as_float(r[c + 1]), s.x, s.y);
+                                    fma2(acc[a][i][c + 2], acc[a][i][c + 3],
+                                         __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]),
+                                         s.z, s.w);
+                                }
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < C::CH; ++c)
+                                    acc[a][i][c] = __uint_as_float(r[c]);
+                            }
+                        }
+                    }
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&acc_empty[ab & 1]);
+                    if (C::F8 && ((k % SC_BLK) == SC_BLK - 1 || k == periods - 1))
+                        mbar_arrive(&sc_empty[ch % SC_RING]);
+                }
+                if (C::F8 && ((k % SC_BLK) == SC_BLK - 1 || k == periods - 1)) ++ch;
+            }
+            if (!ok) {
+                // the cluster's sum must not pass for a result
+                if constexpr (C::SPLIT)
+                    for (int j = half; j < w.nv; j += 2)
+                        part[j * TILE_W + quad * 32 + lane] = __int_as_float(0x7FC00000);
+                break;
+            }
+            const int nr = w.nbi * TILE_W + quad * 32 + lane;  // this thread's weight row
+            if constexpr (C::GU) {
+                // a = silu(g) u; a tile's 128 rows are one scale block of the
+                // activations, so the maximum over lanes and warps is the
+                // block's
+                uint32_t* am = amax + par * 4 * C::NT;
+#pragma unroll
+                for (int i = 0; i < C::NCH; ++i) {
+                    const int col = (2 * i + half) * C::CH;
+                    if (col >= w.np) continue;
+                    uint32_t mine = 0;
+#pragma unroll
+                    for (int c = 0; c < C::CH; ++c) {
+                        const float g = acc[0][i][c], u = acc[C::NA - 1][i][c];
+                        const float v = __fdividef(g, 1.0f + __expf(-g)) * u;
+                        acc[0][i][c] = v;
+                        const uint32_t m = __reduce_max_sync(0xffffffffu, finite_abs_bits(v));
+                        if (lane == c) mine = m;
+                    }
+                    if (lane < C::CH) am[quad * C::NT + col + lane] = mine;
+                }
+                named_bar(1 + half, 128);
+#pragma unroll
+                for (int i = 0; i < C::NCH; ++i) {
+                    const int col = (2 * i + half) * C::CH;
+                    if (col >= w.np) continue;
+                    float s = 1.f, inv = 1.f;
+                    if (lane < C::CH) {
+                        const int j = col + lane;
+                        const uint32_t m = max(max(am[j], am[C::NT + j]),
+                                               max(am[2 * C::NT + j], am[3 * C::NT + j]));
+                        f8_scale(m, &s, &inv);
+                        if (quad == 0 && j < w.nv)
+                            p.as[static_cast<int64_t>(w.row0 + j) * p.nb + w.nbi] = s;
+                    }
+#pragma unroll
+                    for (int c = 0; c < C::CH; c += 2) {
+                        const float i0 = __shfl_sync(0xffffffffu, inv, c);
+                        const float i1 = __shfl_sync(0xffffffffu, inv, c + 1);
+                        const uint32_t q = f8_pack2(acc[0][i][c] * i0, acc[0][i][c + 1] * i1);
+                        const int64_t o = static_cast<int64_t>(w.row0 + col + c) * p.N + nr;
+                        if (col + c < w.nv) p.aq[o] = static_cast<uint8_t>(q & 0xFF);
+                        if (col + c + 1 < w.nv) p.aq[o + p.N] = static_cast<uint8_t>(q >> 8);
+                    }
+                }
+            } else if constexpr (C::SPLIT) {
+#pragma unroll
+                for (int i = 0; i < C::NCH; ++i) {
+                    const int col = (2 * i + half) * C::CH;
+#pragma unroll
+                    for (int c = 0; c < C::CH; ++c)
+                        if (col + c < w.nv)
+                            part[(col + c) * TILE_W + quad * 32 + lane] = acc[0][i][c];
+                }
+            } else {
+                if (nr < p.N) {
+#pragma unroll
+                    for (int i = 0; i < C::NCH; ++i) {
+                        const int col = (2 * i + half) * C::CH;
+#pragma unroll
+                        for (int c = 0; c < C::CH; ++c)
+                            if (col + c < w.nv)
+                                store_out(p.y,
+                                          static_cast<int64_t>(w.row0 + col + c) * p.ldy + nr,
+                                          p.out, acc[0][i][c]);
+                    }
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    if constexpr (C::SPLIT) {
+        // add the ranks' parts in rank order; rank r takes columns r, r + ranks, ...
+        cluster_sync();
+        if (warp >= 4 && first < tiles) {
+            const Tile w = tile_at(first, C::NT, t_lo, t_hi, t_pre, p.E);
+            const int et = tid - 128, r = et & 127;
+            const int nr = w.nbi * TILE_W + r;
+            if (nr < p.N)
+                for (int j = static_cast<int>(rank) + static_cast<int>(ranks) * (et >> 7);
+                     j < w.nv; j += 2 * static_cast<int>(ranks)) {
+                    float v = 0.f;
+                    for (uint32_t q = 0; q < ranks; ++q)
+                        v += cluster_ld_f32(part + j * TILE_W + r, q);
+                    store_out(p.y, static_cast<int64_t>(w.row0 + j) * p.ldy + nr, p.out, v);
+                }
+        }
+        __syncwarp();
+        cluster_sync();
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    if (warp == 1) umma::tmem_dealloc(tmem, C::TM_COLS);
+}
+
+}  // namespace gmm
+}  // namespace qmoe

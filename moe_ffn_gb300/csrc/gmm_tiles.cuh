@@ -1,0 +1,65 @@
+// gmm_tiles.cuh — how the grouped products cut their work into tiles.
+// Compiled for the host as well, so the cutting can be checked on a CPU.
+#pragma once
+#include <cstdint>
+
+#include "route.cuh"  // QMOE_HD
+
+namespace qmoe {
+namespace gmm {
+
+// One tile: group e, weight tile nbi, token rows row0 .. row0 + nv - 1.
+struct Tile {
+    int e, nbi, row0, nv, np;  // np: nv rounded up to the MMA's step of 16
+};
+
+// A group's rows [*lo, *hi) from its two offsets, clamped so that
+// 0 <= *lo <= *hi <= M whatever they hold; true if they were in order.
+QMOE_HD bool group_rows(int lo, int hi, int M, int* lo_out, int* hi_out) {
+    const bool ok = lo >= 0 && hi >= lo && hi <= M;
+    lo = lo < 0 ? 0 : lo > M ? M : lo;
+    hi = hi < lo ? lo : hi > M ? M : hi;
+    *lo_out = lo;
+    *hi_out = hi;
+    return ok;
+}
+
+// Tiles of a group of `rows` rows: token tiles of at most nt rows times nb
+// weight tiles.
+QMOE_HD int group_tiles(int rows, int nt, int nb) {
+    return static_cast<int>((static_cast<int64_t>(rows) + nt - 1) / nt) * nb;
+}
+
+// Tile t, 0 <= t < pre[E]: lo, hi the groups' rows, pre[e] the tiles of the
+// groups before e.  A group is cut into ceil(rows / nt) token tiles of nearly
+// equal size (multiples of 16, nt one of them); the token tiles of one weight
+// tile are consecutive, so CTAs at work at the same time share the weight
+// tile in L2.
+QMOE_HD Tile tile_at(int t, int nt, const int* lo, const int* hi, const int* pre, int E) {
+    int a = 0, b = E;  // pre[a] <= t < pre[b]
+    while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (pre[m] <= t) a = m; else b = m;
+    }
+    Tile r;
+    r.e = a;
+    const int rows = hi[a] - lo[a];
+    const int c = (rows - 1) / nt + 1;
+    const int local = t - pre[a];
+    r.nbi = local / c;
+    const int ts = ((rows - 1) / c + 1 + 15) & ~15;
+    r.row0 = lo[a] + (local - r.nbi * c) * ts;
+    r.nv = hi[a] - r.row0 < ts ? hi[a] - r.row0 : ts;
+    r.np = (r.nv + 15) & ~15;
+    return r;
+}
+
+// Most tiles that M rows in E groups can make: every started token tile of
+// every group that has rows.
+QMOE_HD int64_t max_tiles(int64_t M, int E, int nt, int nb) {
+    const int64_t groups = M < E ? M : E;
+    return (M / nt + groups) * nb;
+}
+
+}  // namespace gmm
+}  // namespace qmoe

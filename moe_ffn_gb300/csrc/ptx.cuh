@@ -13,7 +13,9 @@ enum : unsigned {
     DEV_TIMEOUT_FULL = 1,
     DEV_TIMEOUT_EMPTY = 2,
     DEV_ROUTE_RANGE = 5,  // an expert index was clamped (internal invariant)
-    DEV_X_RANGE = 6       // an activation of magnitude >= 2^106
+    DEV_X_RANGE = 6,      // an activation of magnitude >= 2^106
+    DEV_GMM_TIMEOUT = 24, // a wait of the grouped products' pipeline
+    DEV_GMM_OFFSETS = 25  // group offsets that decrease or leave x's rows
 };
 
 // The device control block, one per device (a global of the library): the
@@ -170,6 +172,49 @@ __device__ __forceinline__ bool named_bar_and(int id, int nthreads, bool v) {
 // Arrive on a named barrier without waiting for it to complete.
 __device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// Tiled TMA loads without an L2 hint: 2-D box at (x, y), 3-D box at (x, y, z).
+__device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, int y,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Thread-block clusters: rank in the cluster, barrier over all its threads
+// (writes before it are visible to the whole cluster after it), and a load
+// from another CTA's shared memory at the address `p` has in this CTA.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_ld_f32(const float* p, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
 }
 
 }  // namespace qmoe

@@ -16,6 +16,7 @@
 
 #include "../../include/qmoe.h"
 #include "formats.cuh"
+#include "host.cuh"
 #include "ptx.cuh"
 #include "stream.cuh"
 #include "fused.cuh"
@@ -27,7 +28,7 @@ namespace qmoe {
 // ----------------------------------------------------------------- errors
 static thread_local std::string g_last_error;
 
-static qmoe_status fail(qmoe_status st, const char* fmt, ...) {
+qmoe_status fail(qmoe_status st, const char* fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -37,7 +38,9 @@ static qmoe_status fail(qmoe_status st, const char* fmt, ...) {
     return st;
 }
 
-static qmoe_status cuda_fail(cudaError_t e, const char* what) {
+void clear_error() { g_last_error.clear(); }
+
+qmoe_status cuda_fail(cudaError_t e, const char* what) {
     return fail(QMOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
@@ -81,27 +84,16 @@ static const char* qname(int qt) {
     default: return "unknown";
     }
 }
-static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 constexpr int64_t MAX_K = 32768;
 // Every workspace starts with the fused kernel's grid-barrier counters,
 // which each call leaves at zero; the other regions follow.
 constexpr size_t WS_SYNC_BYTES = 256;
 
 // ------------------------------------------------------------ device info
-struct DevInfo {
-    bool init = false;
-    bool supported = false;
-    int sms = 0;
-    int smem_optin = 0;
-    int smem_pair = 0;  // dynamic shared memory per CTA that lets two CTAs share an SM
-    DevCtl* err = nullptr;
-    int cc_major = 0, cc_minor = 0;
-};
 static DevInfo g_dev[64];
 static std::mutex g_dev_mu;
 
-static qmoe_status device_info(DevInfo** out) {
+qmoe_status device_info(DevInfo** out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -112,6 +104,7 @@ static qmoe_status device_info(DevInfo** out) {
         cudaDeviceProp prop;
         e = cudaGetDeviceProperties(&prop, dev);
         if (e != cudaSuccess) return cuda_fail(e, "cudaGetDeviceProperties");
+        d.dev = dev;
         d.cc_major = prop.major;
         d.cc_minor = prop.minor;
         d.sms = prop.multiProcessorCount;
@@ -136,23 +129,7 @@ static qmoe_status device_info(DevInfo** out) {
     return QMOE_OK;
 }
 
-// ------------------------------------------------------------ launching
-template <typename Kern, typename... Args>
-static cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                              Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
+// ------------------------------------------------------------ planning
 // Plan chunking and pipeline depth for a streamed GEMV; false if it cannot
 // fit in shared memory.
 template <class Fmt, int MODE>
@@ -447,6 +424,20 @@ static qmoe_status run_rmsnorm(const float* h, const float* w, int64_t rows, int
     return QMOE_OK;
 }
 
+EncodeTiledFn encode_tiled() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
 }  // namespace qmoe
 
 using namespace qmoe;
@@ -684,26 +675,6 @@ size_t moe_ffn_workspace_size(const qmoe_moe_shape* s) {
         return pf > decode ? pf : decode;
     }
     return decode;
-}
-
-// cuTensorMapEncodeTiled, looked up once through the runtime (no link
-// against the driver library).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-static EncodeTiledFn encode_tiled() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    });
-    return fn;
 }
 
 // A [rows][row_bytes] byte matrix as a 2-D tensor map with boxes of
@@ -1166,6 +1137,10 @@ qmoe_status qmoe_device_status(void* stream) {
             return fail(QMOE_ERR_CUDA,
                         "internal error: the routing produced an expert index outside [0, E) "
                         "(code %u); it was clamped, and the layer's output is not valid", v);
+        if (v == DEV_GMM_OFFSETS)
+            return fail(QMOE_ERR_INVALID_ARGUMENT,
+                        "mm_grouped: group offsets decrease or lie outside [0, n_rows] (code %u); "
+                        "they were clamped, and the output is not valid", v);
         return fail(QMOE_ERR_TIMEOUT, "a bounded device wait expired (code %u: %s)", v,
                     v == DEV_TIMEOUT_FULL    ? "stage never filled"
                     : v == DEV_TIMEOUT_EMPTY ? "stage never released"
