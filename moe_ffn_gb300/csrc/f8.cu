@@ -11,6 +11,7 @@
 #include "../../include/qmoe.h"
 #include "host.cuh"
 #include "gmm.cuh"
+#include "gmm_pair.cuh"
 #include "f8moe.cuh"
 
 namespace qmoe {
@@ -68,10 +69,12 @@ struct Gmm {
     gmm::Params p;
 };
 
-template <class C>
-static qmoe_status launch_gmm(const Gmm& g, int ranks, int clusters, const DevInfo& d,
-                              cudaStream_t st) {
-    auto kern = gmm::gmm_kernel<C>;
+// Launches kernel `kern` of configuration C; SPLIT: clusters of `ranks` CTAs
+// (the pair kernel has its cluster shape in its code).
+template <class C, class Kern>
+static qmoe_status launch_gmm(Kern kern, int threads, bool split, const Gmm& g, int ranks,
+                              int clusters, const DevInfo& d, cudaStream_t st) {
+    static_assert(C::smem(MAX_GROUPS) <= 232448, "shared memory of one CTA");
     const int smem = C::smem(g.p.E);
     static std::atomic<int> configured[64];
     if (smem > configured[d.dev].load()) {
@@ -93,7 +96,7 @@ static qmoe_status launch_gmm(const Gmm& g, int ranks, int clusters, const DevIn
     if (qmoe_status s = operand_map(&tx, g.x, size, bf16, g.K, g.p.M, 0, g.ldx, C::BOX)) return s;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
-    cfg.blockDim = dim3(gmm::THREADS);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -104,26 +107,38 @@ static qmoe_status launch_gmm(const Gmm& g, int ranks, int clusters, const DevIn
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = C::SPLIT ? 2 : 1;
+    cfg.numAttrs = split ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g.p, tw, tw2, tx);
     if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
     return QMOE_OK;
 }
 
+template <class C>
+static qmoe_status launch_split(const Gmm& g, int ranks, int tiles, const DevInfo& d,
+                                cudaStream_t st) {
+    return launch_gmm<C>(gmm::gmm_kernel<C>, gmm::THREADS, true, g, ranks, tiles, d, st);
+}
+// One CTA pair per two SMs, or as many as there can be tiles.
+template <class C>
+static qmoe_status launch_pairs(const Gmm& g, const DevInfo& d, cudaStream_t st) {
+    const int64_t tiles = gmm::max_tiles(g.p.M, g.p.E, C::NT, (g.p.nb + 1) / 2);
+    const int pairs = static_cast<int>(tiles < d.sms / 2 ? tiles : d.sms / 2);
+    return launch_gmm<C>(gmm::gmm_pair_kernel<C>, gmm::P_THREADS, false, g, 2, pairs, d, st);
+}
+
 template <bool F8>
-static qmoe_status run_gmm_kind(const Gmm& g, const DevInfo& d, cudaStream_t st) {
+static qmoe_status run_gmm_kind(Gmm& g, const DevInfo& d, cudaStream_t st) {
     const gmm::Params& p = g.p;
     if (p.M <= 32LL * (p.offsets ? p.E : 1) && p.M <= 512) {
         const int64_t tiles = gmm::max_tiles(p.M, p.E, 32, p.nb);
         int ranks = 1;
         while (ranks < 8 && tiles * ranks * 2 <= 2 * d.sms && p.kb >= ranks * 4) ranks *= 2;
         if (tiles <= 65536)
-            return launch_gmm<gmm::Cfg<F8, 32, 6, false, true>>(g, ranks,
-                                                                static_cast<int>(tiles), d, st);
+            return launch_split<gmm::Cfg<F8, 32, 6, false, true>>(g, ranks,
+                                                                  static_cast<int>(tiles), d, st);
     }
-    const int64_t tiles = gmm::max_tiles(p.M, p.E, 256, p.nb);
-    const int grid = static_cast<int>(tiles < d.sms ? tiles : d.sms);
-    return launch_gmm<gmm::Cfg<F8, 256, 4, false, false>>(g, 1, grid, d, st);
+    g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
+    return launch_pairs<gmm::PairCfg<F8, 192, 6, false>>(g, d, st);
 }
 
 static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
@@ -131,6 +146,7 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
     g.p.kb = static_cast<int>((g.K * size + gmm::KBLK - 1) / gmm::KBLK);
     g.p.nb = (g.p.N + gmm::TILE_W - 1) / gmm::TILE_W;
     g.p.err = d.err;
+    g.p.vec_out = g.p.out != gmm::OUT_F32 && aligned(g.p.y, 16) && g.p.ldy % 8 == 0;
     // D f32 (bit 4); 16-bit operands: 0 f16, 1 bf16 (bits 7-9 and 10-12);
     // 8-bit operands: 0 e4m3; M / 16 from bit 24
     const uint32_t fmt = g.type == QMOE_BF16 ? 1u : 0u;
@@ -138,9 +154,8 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
                 (static_cast<uint32_t>(gmm::TILE_W >> 4) << 24);
     if (g.type == QMOE_E4M3) {
         if (g.W2) {
-            const int64_t tiles = gmm::max_tiles(g.p.M, g.p.E, 128, g.p.nb);
-            const int grid = static_cast<int>(tiles < d.sms ? tiles : d.sms);
-            return launch_gmm<gmm::Cfg<true, 128, 4, true, false>>(g, 1, grid, d, st);
+            g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
+            return launch_pairs<gmm::PairCfg<true, 96, 5, true>>(g, d, st);
         }
         return run_gmm_kind<true>(g, d, st);
     }

@@ -56,6 +56,7 @@ struct Params {
     int kb;                  // 128-byte blocks of K
     int nb;                  // 128-row tiles of W
     int out;                 // OutType
+    int vec_out;             // y is 16-bit with 16-byte aligned rows
     uint32_t idesc;          // instruction descriptor without N
     DevCtl* err;
 };
@@ -120,6 +121,50 @@ __device__ __forceinline__ void store_out(void* y, int64_t i, int type, float v)
         static_cast<float*>(y)[i] = v;
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The groups' tables, by one warp: rows [lo, hi) of each group and the tiles
+// before it, the total last.  Offsets are clamped into [0, M], so that no
+// value of theirs forms an address outside x or y.
+__device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, int lane, int* t_lo,
+                                             int* t_hi, int* t_pre) {
+    int total = 0;
+    bool bad = false;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < p.E) {
+            if (p.offsets)
+                bad |= !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M, &lo,
+                                   &hi);
+            else
+                hi = p.M;
+        }
+        const int n = group_tiles(hi - lo, nt, nb);
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += v;
+        }
+        if (e < p.E) {
+            t_lo[e] = lo;
+            t_hi[e] = hi;
+            t_pre[e] = total + s - n;
+        }
+        total += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) t_pre[p.E] = total;
+    if (bad) record_error(p.err, DEV_GMM_OFFSETS);
+}
+
 template <class C>
 __global__ void __launch_bounds__(THREADS, 1)
     gmm_kernel(const Params p, const __grid_constant__ CUtensorMap tm_w,
@@ -144,7 +189,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     int* t_hi = t_lo + p.E;
     int* t_pre = t_hi + p.E;  // [E+1]
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (warp == 1) umma::tmem_alloc(tmem_slot, C::TM_COLS);
     if (tid == 0) {
         for (int i = 0; i < C::NST; ++i) {
@@ -166,39 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // this stream too), so nothing is read before the dependency wait.
     pdl_wait();
     pdl_trigger();
-    if (warp == 0) {
-        // group tables; offsets are clamped into [0, M], so that no value of
-        // theirs forms an address outside x or y
-        int total = 0;
-        bool bad = false;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            int lo = 0, hi = 0;
-            if (e < p.E) {
-                if (p.offsets) {
-                    bad |= !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M,
-                                       &lo, &hi);
-                } else {
-                    hi = p.M;
-                }
-            }
-            const int n = group_tiles(hi - lo, C::NT, p.nb);
-            int s = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += v;
-            }
-            if (e < p.E) {
-                t_lo[e] = lo;
-                t_hi[e] = hi;
-                t_pre[e] = total + s - n;
-            }
-            total += __shfl_sync(0xffffffffu, s, 31);
-        }
-        if (lane == 0) t_pre[p.E] = total;
-        if (bad) record_error(p.err, DEV_GMM_OFFSETS);
-    }
+    if (warp == 0) build_tables(p, C::NT, p.nb, lane, t_lo, t_hi, t_pre);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -220,19 +234,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------- loads
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int t = first; t < tiles && ok; t += step) {
-                const Tile w = tile_at(t, C::NT, t_lo, t_hi, t_pre, p.E);
-                const int boxes = (w.np + C::BOX - 1) / C::BOX;
-                for (int kb = kbeg; kb < kend; ++kb, ++it) {
-                    const int s = it % C::NST, round = it / C::NST;
-                    if (round > 0 &&
-                        !mbar_wait_bounded(&empty[s], (round - 1) & 1, p.err, DEV_GMM_TIMEOUT)) {
-                        ok = false;
-                        break;
-                    }
+        int it = 0, s = 0;
+        uint32_t ph = 1;  // parity of the wait for a free stage
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
+            const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const int boxes = (w.np + C::BOX - 1) / C::BOX;
+            for (int kb = kbeg; kb < kend; ++kb, ++it) {
+                // (before any use of a stage the wait passes at once)
+                if (!mbar_wait_spin(&empty[s], ph, p.err, DEV_GMM_TIMEOUT)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
                     uint8_t* st = base + s * C::STAGE;
                     mbar_arrive_expect_tx(&full[s],
                                           C::NA * C::A_BYTES + boxes * C::BOX * KBLK);
@@ -242,63 +256,75 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tma_load_3d(st, &tm_w, kx, w.nbi * TILE_W, w.e, &full[s]);
                     if constexpr (C::GU)
                         tma_load_3d(st + C::A_BYTES, &tm_w2, kx, w.nbi * TILE_W, w.e, &full[s]);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(st + C::NA * C::A_BYTES + b * C::BOX * KBLK, &tm_x, kx,
-                                    w.row0 + b * C::BOX, &full[s]);
+#pragma unroll
+                    for (int b = 0; b < C::NT / C::BOX; ++b)
+                        if (b < boxes)
+                            tma_load_2d(st + C::NA * C::A_BYTES + b * C::BOX * KBLK, &tm_x, kx,
+                                        w.row0 + b * C::BOX, &full[s]);
+                }
+                __syncwarp();
+                if (++s == C::NST) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
-            // never leave with copies in flight
-            for (int k = max(it - C::NST, 0); k < it; ++k)
-                mbar_wait_bounded(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
         }
+        // never leave with copies in flight
+        for (int k = max(it - C::NST, 0); k < it; ++k)
+            mbar_wait_spin(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            int it = 0, ab = 0;  // stage and accumulator-buffer counters
-            bool ok = true;
-            for (int t = first; t < tiles && ok; t += step) {
-                const Tile w = tile_at(t, C::NT, t_lo, t_hi, t_pre, p.E);
-                const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
-                for (int kb = kbeg; kb < kend; ++kb, ++it) {
-                    const bool fresh = C::F8 || kb == kbeg;  // a new accumulator buffer
-                    if (fresh && ab >= 2 &&
-                        !mbar_wait_bounded(&acc_empty[ab & 1], ((ab >> 1) - 1) & 1, p.err,
-                                           DEV_GMM_TIMEOUT)) {
-                        ok = false;
-                        break;
-                    }
-                    const int s = it % C::NST;
-                    if (!mbar_wait_bounded(&full[s], (it / C::NST) & 1, p.err, DEV_GMM_TIMEOUT)) {
-                        ok = false;
-                        break;
-                    }
-                    umma::fence_after_sync();
-                    const uint32_t st = smem_u32(base + s * C::STAGE);
-                    const uint32_t d = tmem + (ab & 1) * C::TM_BUF;
+        int s = 0;
+        uint32_t ph = 0, ab = 0, aph = 1;  // stage and accumulator phases
+        bool ok = true;
+        const uint64_t da0 = umma::desc_sw128(smem_u32(base));
+        const uint64_t db0 = umma::desc_sw128(smem_u32(base) + C::NA * C::A_BYTES);
+        for (int t = first; t < tiles && ok; t += step) {
+            const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
+            for (int kb = kbeg; kb < kend; ++kb) {
+                const bool fresh = C::F8 || kb == kbeg;  // a new accumulator buffer
+                if (fresh && !mbar_wait_spin(&acc_empty[ab], aph, p.err, DEV_GMM_TIMEOUT)) {
+                    ok = false;
+                    break;
+                }
+                if (!mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT)) {
+                    ok = false;
+                    break;
+                }
+                umma::fence_after_sync();
+                const bool last = C::F8 || kb == kend - 1;
+                if (elect_one()) {
+                    // 32 bytes of K further: the descriptors' address field + 2
+                    const uint64_t da = da0 + s * (C::STAGE >> 4);
+                    const uint64_t db = db0 + s * (C::STAGE >> 4);
+                    const uint32_t d = tmem + ab * C::TM_BUF;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint64_t db = umma::desc_sw128(st + C::NA * C::A_BYTES + 32 * j);
-                        const uint32_t acc = (!fresh || j > 0) ? 1u : 0u;
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int a = 0; a < C::NA; ++a) {
-                            const uint64_t da = umma::desc_sw128(st + a * C::A_BYTES + 32 * j);
+                            const uint32_t acc = (!fresh || j > 0) ? 1u : 0u;
+                            const uint64_t daj = da + a * (C::A_BYTES >> 4) + 2 * j;
                             if constexpr (C::F8)
-                                umma::mma_f8(d + a * C::NT, da, db, idesc, acc);
+                                umma::mma_f8(d + a * C::NT, daj, db + 2 * j, idesc, acc);
                             else
-                                umma::mma_f16(d + a * C::NT, da, db, idesc, acc);
+                                umma::mma_f16(d + a * C::NT, daj, db + 2 * j, idesc, acc);
                         }
-                    }
                     umma::commit(&empty[s]);
-                    if (C::F8 || kb == kend - 1) {
-                        umma::commit(&acc_full[ab & 1]);
-                        ++ab;
-                    }
+                    if (last) umma::commit(&acc_full[ab]);
+                }
+                __syncwarp();
+                if (last && (ab ^= 1) == 0) aph ^= 1;
+                if (++s == C::NST) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
-            // every MMA has finished before TMEM and the stages are given up
-            umma::commit(mma_done);
-            mbar_wait_bounded(mma_done, 0, p.err, DEV_GMM_TIMEOUT);
         }
+        // every MMA has finished before TMEM and the stages are given up
+        if (elect_one()) umma::commit(mma_done);
+        __syncwarp();
+        mbar_wait_spin(mma_done, 0, p.err, DEV_GMM_TIMEOUT);
     } else if (warp < 4) {
         // --------------------------------------------------------- scales
         if constexpr (C::F8) {
@@ -310,7 +336,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int ch = 0;
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
-                const Tile w = tile_at(t, C::NT, t_lo, t_hi, t_pre, p.E);
+                const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + w.nbi) * p.kb;
                 for (int k0 = kbeg; k0 < kend; k0 += SC_BLK, ++ch) {
                     float v[RPT][SC_BLK], g[C::NA][SC_BLK];
@@ -334,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                     const int s = ch % SC_RING, round = ch / SC_RING;
-                    if (round > 0 && !mbar_wait_bounded(&sc_empty[s], (round - 1) & 1, p.err,
+                    if (round > 0 && !mbar_wait_spin(&sc_empty[s], (round - 1) & 1, p.err,
                                                         DEV_GMM_TIMEOUT)) {
                         ok = false;
                         break;
@@ -362,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int ab = 0, ch = 0, par = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step, par ^= 1) {
-            const Tile w = tile_at(t, C::NT, t_lo, t_hi, t_pre, p.E);
+            const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             float acc[C::NA][C::NCH][C::CH];
 #pragma unroll
             for (int a = 0; a < C::NA; ++a)
@@ -375,14 +401,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float* sc = nullptr;
                 if constexpr (C::F8) {
                     const int s = ch % SC_RING;
-                    if ((k % SC_BLK) == 0 && !mbar_wait_bounded(&sc_full[s], (ch / SC_RING) & 1,
+                    if ((k % SC_BLK) == 0 && !mbar_wait_spin(&sc_full[s], (ch / SC_RING) & 1,
                                                                 p.err, DEV_GMM_TIMEOUT)) {
                         ok = false;
                         break;
                     }
                     sc = ring + s * C::SC_STAGE + (k % SC_BLK) * C::NA * C::NT;
                 }
-                if (!mbar_wait_bounded(&acc_full[ab & 1], (ab >> 1) & 1, p.err,
+                if (!mbar_wait_spin(&acc_full[ab & 1], (ab >> 1) & 1, p.err,
                                        DEV_GMM_TIMEOUT)) {
                     ok = false;
                     break;
@@ -508,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // add the ranks' parts in rank order; rank r takes columns r, r + ranks, ...
         cluster_sync();
         if (warp >= 4 && first < tiles) {
-            const Tile w = tile_at(first, C::NT, t_lo, t_hi, t_pre, p.E);
+            const Tile w = tile_at(first, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             const int et = tid - 128, r = et & 127;
             const int nr = w.nbi * TILE_W + r;
             if (nr < p.N)

@@ -10,7 +10,7 @@ namespace gmm {
 
 // One tile: group e, weight tile nbi, token rows row0 .. row0 + nv - 1.
 struct Tile {
-    int e, nbi, row0, nv, np;  // np: nv rounded up to the MMA's step of 16
+    int e, nbi, row0, nv, np;  // np: nv rounded up to `step`
 };
 
 // A group's rows [*lo, *hi) from its two offsets, clamped so that
@@ -32,10 +32,11 @@ QMOE_HD int group_tiles(int rows, int nt, int nb) {
 
 // Tile t, 0 <= t < pre[E]: lo, hi the groups' rows, pre[e] the tiles of the
 // groups before e.  A group is cut into ceil(rows / nt) token tiles of nearly
-// equal size (multiples of 16, nt one of them); the token tiles of one weight
+// equal size (multiples of `step`, a power of two that divides nt; the MMA's
+// N step: 16, or 32 for a CTA pair); the token tiles of one weight
 // tile are consecutive, so CTAs at work at the same time share the weight
 // tile in L2.
-QMOE_HD Tile tile_at(int t, int nt, const int* lo, const int* hi, const int* pre, int E) {
+QMOE_HD Tile tile_at(int t, int nt, int step, const int* lo, const int* hi, const int* pre, int E) {
     int a = 0, b = E;  // pre[a] <= t < pre[b]
     while (b - a > 1) {
         const int m = (a + b) >> 1;
@@ -47,10 +48,10 @@ QMOE_HD Tile tile_at(int t, int nt, const int* lo, const int* hi, const int* pre
     const int c = (rows - 1) / nt + 1;
     const int local = t - pre[a];
     r.nbi = local / c;
-    const int ts = ((rows - 1) / c + 1 + 15) & ~15;
+    const int ts = ((rows - 1) / c + step) & ~(step - 1);
     r.row0 = lo[a] + (local - r.nbi * c) * ts;
     r.nv = hi[a] - r.row0 < ts ? hi[a] - r.row0 : ts;
-    r.np = (r.nv + 15) & ~15;
+    r.np = (r.nv + step - 1) & ~(step - 1);
     return r;
 }
 

@@ -99,6 +99,18 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     }
 }
 
+// The same for pipelines that wait every few hundred clocks: the clock and
+// the limit are read only once 256 tries have failed (a try itself suspends
+// the thread for a while).  Reading the global timer at the start of every
+// wait cost more than the wait.
+__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, DevCtl* err,
+                                               unsigned code) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, err, code);
+}
+
 // L2 policy for streamed weights: evict first, so activations and
 // re-read operands keep their L2 lines.
 __device__ __forceinline__ uint64_t policy_evict_first() {
@@ -169,6 +181,20 @@ __device__ __forceinline__ bool named_bar_and(int id, int nthreads, bool v) {
     return r != 0;
 }
 
+// True in one lane of a converged warp.  Loops that feed the tensor core or
+// the copy engine run in the whole warp, with only the instructions
+// themselves under this predicate: operands then stay in uniform registers.
+// In a one-lane branch each such instruction took 80-130 clocks to issue.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Arrive on a named barrier without waiting for it to complete.
 __device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
@@ -215,6 +241,77 @@ __device__ __forceinline__ float cluster_ld_f32(const float* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
+}
+
+// The address in shared::cluster space that `p` has in CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+// Arrive on a barrier of the cluster (address from cluster_addr).  Relaxed: it
+// hands back tensor memory, whose reads tcgen05.wait::ld has completed, and no
+// ordinary memory; a release at cluster scope put a fence of 2,000-3,000
+// clocks in front of every arrival.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+                 : "memory");
+}
+
+// Tiled TMA loads of a CTA pair: into this CTA's shared memory, completing
+// transaction bytes on the barrier at cluster address `bar` (either CTA's).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, int x, int y,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* tmap, int x, int y, int z,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// 4-byte asynchronous copy global -> shared; zeros instead if !valid (the
+// source must be readable all the same).  cp_async_arrive arrives on `bar`
+// once this thread's earlier copies have landed.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_drain() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Register share of a warpgroup (every warp of it executes this).
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Four 8x8 tiles of 16-bit values to shared memory, transposed: thread T
+// holds row T / 4, columns 2 (T % 4) and + 1 of each; lane 8 m + j gives the
+// address of column j of tile m.
+__device__ __forceinline__ void stmatrix_x4_trans(void* dst, uint32_t a, uint32_t b, uint32_t c,
+                                                  uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     smem_u32(dst)),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
 
 }  // namespace qmoe

@@ -10,7 +10,7 @@ extern "C" {
 // Cuts the groups of `offsets` (E + 1 values) as the kernel does; writes up to
 // cap tiles of five ints each and returns their count (-1 if over cap).
 // *ok: the offsets were in order; *bound: max_tiles of the sizes.
-int gmm_tiles_host(const int* offsets, int E, int M, int nt, int nb, int* out, int cap, int* ok,
+int gmm_tiles_host(const int* offsets, int E, int M, int nt, int step, int nb, int* out, int cap, int* ok,
                    long long* bound) {
     using namespace qmoe::gmm;
     std::vector<int> lo(E), hi(E), pre(E + 1);
@@ -25,7 +25,7 @@ int gmm_tiles_host(const int* offsets, int E, int M, int nt, int nb, int* out, i
     *bound = max_tiles(M, E, nt, nb);
     if (total > cap) return -1;
     for (int t = 0; t < total; ++t) {
-        const Tile w = tile_at(t, nt, lo.data(), hi.data(), pre.data(), E);
+        const Tile w = tile_at(t, nt, step, lo.data(), hi.data(), pre.data(), E);
         const int v[5] = {w.e, w.nbi, w.row0, w.nv, w.np};
         for (int i = 0; i < 5; ++i) out[5 * t + i] = v[i];
     }

@@ -21,12 +21,12 @@ def cut():
                     os.path.join(HERE, "host", "gmm_tiles.cpp")], check=True)
     lib = ctypes.CDLL(so)
 
-    def f(offsets, M, nt, nb):
+    def f(offsets, M, nt, nb, step=16):
         E = len(offsets) - 1
         cap = 200000
         out = (ctypes.c_int * (5 * cap))()
         ok, bound = ctypes.c_int(), ctypes.c_longlong()
-        n = lib.gmm_tiles_host((ctypes.c_int * (E + 1))(*offsets), E, M, nt, nb, out, cap,
+        n = lib.gmm_tiles_host((ctypes.c_int * (E + 1))(*offsets), E, M, nt, step, nb, out, cap,
                                ctypes.byref(ok), ctypes.byref(bound))
         assert n >= 0
         return [tuple(out[5 * t:5 * t + 5]) for t in range(n)], bool(ok.value), bound.value
@@ -40,9 +40,9 @@ def offsets_of(sizes, start=0):
     return o
 
 
-@pytest.mark.parametrize("nt", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("nt,step", [(16, 16), (32, 16), (64, 16), (128, 16), (256, 16), (128, 32), (256, 32)])
 @pytest.mark.parametrize("seed", range(6))
-def test_tiles_cover_groups_once(cut, nt, seed):
+def test_tiles_cover_groups_once(cut, nt, step, seed):
     g = random.Random(seed)
     E = [1, 2, 7, 40, 130, 1024][seed]
     sizes = [g.choice([0, 0, 1, 2, 15, 16, 17, 31, 32, 33, 100, 255, 256, 257, 300])
@@ -53,11 +53,11 @@ def test_tiles_cover_groups_once(cut, nt, seed):
     nb = g.choice([1, 3])
     if M == 0:
         return
-    tiles, ok, bound = cut(off, M, nt, nb)
+    tiles, ok, bound = cut(off, M, nt, nb, step)
     assert ok and len(tiles) <= bound
     seen = set()
     for e, nbi, row0, nv, np_ in tiles:
-        assert 0 < nv <= np_ <= nt and np_ % 16 == 0 and np_ - nv < 16
+        assert 0 < nv <= np_ <= nt and np_ % step == 0 and np_ - nv < step
         assert off[e] <= row0 and row0 + nv <= off[e + 1] and 0 <= nbi < nb
         for r in range(row0, row0 + nv):
             assert (r, nbi) not in seen
