@@ -32,6 +32,8 @@ static int out_type(int t) {
 constexpr int64_t MAX_COLS = 1 << 20;    // K of a product, columns of a quantised row
 constexpr int64_t MAX_ROWS = 0x7fffff00; // token rows and weight rows
 constexpr int MAX_GROUPS = 1024;
+constexpr int MAX_F8_EXPERTS = 256;
+constexpr int MAX_F8_TOPK = 16;
 
 // ------------------------------------------------------------ tensor maps
 // [outer][rows][inner] elements of `size` bytes, 128-byte swizzled boxes of
@@ -74,14 +76,15 @@ struct Gmm {
 template <class C, class Kern>
 static qmoe_status launch_gmm(Kern kern, int threads, bool split, const Gmm& g, int ranks,
                               int clusters, const DevInfo& d, cudaStream_t st) {
-    static_assert(C::smem(MAX_GROUPS) <= 232448, "shared memory of one CTA");
     const int smem = C::smem(g.p.E);
+    constexpr int most = C::smem(C::GU ? MAX_F8_EXPERTS : MAX_GROUPS);
+    static_assert(most <= 232448, "shared memory of one CTA");
     static std::atomic<int> configured[64];
     if (smem > configured[d.dev].load()) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::smem(MAX_GROUPS));
+                                             most);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(grouped product)");
-        configured[d.dev].store(C::smem(MAX_GROUPS));
+        configured[d.dev].store(most);
     }
     const int size = type_size(g.type);
     const bool bf16 = g.type == QMOE_BF16;
@@ -138,7 +141,7 @@ static qmoe_status run_gmm_kind(Gmm& g, const DevInfo& d, cudaStream_t st) {
                                                                   static_cast<int>(tiles), d, st);
     }
     g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
-    return launch_pairs<gmm::PairCfg<F8, 192, 6, false>>(g, d, st);
+    return launch_pairs<gmm::PairCfg<F8, F8 ? 128 : 256, F8 ? 7 : 5, false>>(g, d, st);
 }
 
 static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
@@ -155,7 +158,7 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
     if (g.type == QMOE_E4M3) {
         if (g.W2) {
             g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
-            return launch_pairs<gmm::PairCfg<true, 96, 5, true>>(g, d, st);
+            return launch_pairs<gmm::PairCfg<true, 64, 5, true>>(g, d, st);
         }
         return run_gmm_kind<true>(g, d, st);
     }
@@ -202,9 +205,6 @@ static MoeWs moe_f8_layout(const qmoe_moe_shape& s) {
     w.total = o;
     return w;
 }
-
-constexpr int MAX_F8_EXPERTS = 256;
-constexpr int MAX_F8_TOPK = 16;
 
 // Shape rules of moe_experts_f8 (also behind its workspace size).
 static qmoe_status moe_f8_shape(const qmoe_moe_shape* s) {

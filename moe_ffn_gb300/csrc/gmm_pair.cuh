@@ -1,60 +1,146 @@
 // gmm_pair.cuh — the grouped products' kernel for many rows: a pair of CTAs
-// (a cluster of two) computes 256 weight rows x up to 192 token rows with
-// tcgen05.mma cta_group::2.
+// (a cluster of two) computes 256 weight rows by up to 256 token rows (16-bit)
+// or 128 (e4m3) with tcgen05.mma cta_group::2.
 //
 // Why pairs: each CTA loads its own 128 weight rows and half of the token
-// rows, so a stage of 128 bytes of K brings 32 KB per CTA for
-// 128 x 256 x 128 multiply-adds.  One CTA alone would load 48 KB for the same
-// work, and was bound by the 64 bytes an SM takes from L2 per clock.
+// rows.  A stage of 128 bytes of K is then 32 KB per CTA for
+// 128 x 256 x 64 16-bit multiply-adds; one CTA alone would load 48 KB for the
+// same work, and was bound by the bytes an SM takes from L2 per clock.
 //
 // Scales (e4m3).  The weight rows lie along TMEM lanes and the token rows
 // along its columns, so every column of a partial product has its own scale.
-// The epilogue reads TMEM in 16x256b fragments, in which a thread has two of
-// every eight columns of four rows: a quarter of the scale loads that
-// whole-row fragments need (those took 1024 clocks of shared-memory bandwidth
-// per k-block of 512 clocks).
+// The epilogue reads TMEM in 16x128b fragments, in which a thread has one of
+// every four columns of four rows: a quarter of the scale loads that whole-row
+// fragments need (those took 1024 clocks of shared-memory bandwidth per
+// 256-column k-block of 512 clocks).  Measured over 12 warps: 32x32b 439,
+// 16x128b 431, 16x256b 255 bytes per clock.
 //
-// Roles (512 threads): warp 0 loads, warp 1 (of the first CTA) issues the
-// MMAs, warps 2-3 copy scales, warps 4-15 are the epilogue: warp w reads
-// lanes 32 (w % 4) .. + 31 and every third run of 32 columns.  A warp hands a
-// TMEM buffer back once its values are in registers, before it adds them.
+// What bounds the e4m3 form is not a rate but the round trip of an
+// accumulator buffer, once per k-block: issue, MMA, commit, the sixteen warps
+// of two CTAs reading it, their arrivals at the issuing CTA - about 2,300
+// clocks with two buffers of 192 columns, whatever the instruction count.  So
+// the buffers are four of 128 columns, a warp reads one fragment of each, and
+// hands the buffer back before it adds the values.
+//
+// Roles (640 threads): warp 0 loads, warp 1 (of the first CTA) issues the
+// MMAs, warps 2-3 copy scales, warps 4-19 are the epilogue: warp w reads
+// lanes 32 (w % 4) .. + 31 and every fourth run of 32 columns (SwiGLU form:
+// run w / 4 % 2 of gate, w < 12, or of up).
 #pragma once
 #include "gmm.cuh"
 
 namespace qmoe {
 namespace gmm {
 
-constexpr int P_CG = 3;            // runs of columns in flight, one per four warps
+constexpr int P_CG = 4;            // runs of columns in flight, one per four warps
 constexpr int P_EPI = 4 * P_CG;    // epilogue warps
 constexpr int P_THREADS = 128 + 32 * P_EPI;
 constexpr int P_CH = 32;           // columns per run
-// registers per thread: 128 x 56 + 384 x 152 = 65,536, the launch's 512 x 128
-constexpr int P_REGS_LOAD = 56, P_REGS_EPI = 152;
+// registers per thread: 128 x 64 + 512 x 104 = 61,440, the launch's 640 x 96
+constexpr int P_REGS_LOAD = 64, P_REGS_EPI = 104;
 
 template <bool F8_, int NT_, int NST_, bool GU_>
 struct PairCfg {
     static constexpr bool F8 = F8_, GU = GU_;
     static constexpr int NT = NT_, NST = NST_;
     static constexpr int NA = GU ? 2 : 1;
-    static constexpr int BOX = GU ? 16 : 32;  // token rows per TMA box; divides NT / 2
+    static constexpr int BOX = 32;  // token rows per TMA box; divides NT / 2
     static constexpr int A_BYTES = TILE_W * KBLK;
     static constexpr int STAGE = NA * A_BYTES + NT / 2 * KBLK;
-    static constexpr int PARTS = NA * NT / P_CH / P_CG;  // runs per epilogue warp
     static constexpr int TM_BUF = NA * NT;
     static constexpr int TM_COLS = 512;
+    static constexpr int NBUF = TM_COLS / TM_BUF;      // accumulator buffers
+    static constexpr int RUNS = TM_BUF / P_CH / P_CG;  // runs per epilogue warp and buffer
     static constexpr int SC_ROW = NT + 4;  // scales of x, then of W (gate, up)
     static constexpr int SC_STAGE = SC_BLK * SC_ROW;  // floats
-    static constexpr int OUT_BYTES = GU ? 1024 : 2048;  // staging per epilogue warp
+    // staging per epilogue warp: 32 tokens of 32 16-bit values; SwiGLU form:
+    // per pair of warps, up's 32 x 32 f32 values on their way to gate's warp
+    static constexpr int OUT_BYTES = 2048;
     static constexpr int O_SC = NST * STAGE;
     static constexpr int O_OUT = O_SC + (F8 ? SC_RING * SC_STAGE * 4 : 0);
     static constexpr int O_AMAX = O_OUT + P_EPI * OUT_BYTES;
     static constexpr int O_BAR = O_AMAX + (GU ? 2 * 4 * NT * 4 : 0);
-    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 4 + 1;
+    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1 + (GU ? P_EPI : 0);
     static constexpr int O_TAB = O_BAR + (N_BAR + 1) * 8;
     static constexpr int smem(int E) { return 1024 + O_TAB + (3 * E + 4) * 4; }
-    static_assert(PARTS == 2 && 2 * TM_BUF <= TM_COLS && STAGE % 1024 == 0, "tile shape");
+    static_assert(TM_BUF * NBUF == TM_COLS && STAGE % 1024 == 0, "tile shape");
     static_assert((NT / 2) % BOX == 0, "boxes fill a stage exactly");
+    static_assert(RUNS == (F8 ? 1 : 2), "e4m3: one run per warp; 16-bit: two");
 };
+
+// Where token j's scale lies in a row of the ring: a thread's eight columns of
+// a run (4 i + lane % 4) are consecutive.
+__device__ __forceinline__ int sc_slot(int j) {
+    return (j & ~31) | ((j & 3) << 3) | ((j >> 2) & 7);
+}
+
+// A run of 32 columns of this warp's 32 weight rows.
+struct Frag {
+    uint32_t lo[16], hi[16];  // row halves
+};
+__device__ __forceinline__ void frag_load(uint32_t src, Frag& f) {
+    umma::ld_16x128b_x8(src, f.lo);
+    umma::ld_16x128b_x8(src + (16u << 16), f.hi);
+}
+__device__ __forceinline__ void frag_wait(Frag& f) {
+    umma::wait_ld(f.lo);
+    umma::wait_ld(f.hi);
+}
+
+// 16-bit y of one run (v[row half][2 i + j]: row 16 half + 8 j + lane / 4,
+// column 4 i + lane % 4), transposed through shared memory: a word holds rows r
+// and r + 8 of a token; token c's 64 bytes lie at 64 c, the halves swapped
+// where c has bit 1 (four tokens' words then fall in distinct banks).
+__device__ __forceinline__ void store_run16(uint8_t* stage, const float (&v)[2][16], bool bf16,
+                                            int lane, uint16_t* y, int64_t ldy, int nv) {
+    const int lr = lane >> 2, lc = lane & 3;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int tok = 4 * k + lc;
+            *reinterpret_cast<uint32_t*>(stage + tok * 64 +
+                                         ((32 * h + 4 * lr) ^ ((tok & 2) << 4))) =
+                bf16 ? pack_bf16(v[h][2 * k], v[h][2 * k + 1])
+                     : pack_f16(v[h][2 * k], v[h][2 * k + 1]);
+        }
+    __syncwarp();
+    // two lanes per token, 16 rows each: 32-byte runs of y's rows
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int tok = 16 * k + (lane >> 1), h = lane & 1;
+        const uint8_t* src = stage + tok * 64 + ((32 * h) ^ ((tok & 2) << 4));
+        const uint4 a = *reinterpret_cast<const uint4*>(src);
+        const uint4 b = *reinterpret_cast<const uint4*>(src + 16);
+        if (tok < nv) {
+            uint4* dst = reinterpret_cast<uint4*>(y + tok * ldy + 16 * h);
+            dst[0] = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+            dst[1] = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+        }
+    }
+    __syncwarp();
+}
+
+// One run of y: nv tokens from y's element `first`, weight rows n0 .. n0 + 31.
+__device__ __forceinline__ void store_run(const Params& p, uint8_t* stage, const float (&v)[2][16],
+                                          int lane, int64_t row, int nv, int n0) {
+    if (nv <= 0) return;
+    if (p.vec_out && n0 + 32 <= p.N) {
+        store_run16(stage, v, p.out == OUT_BF16, lane,
+                    static_cast<uint16_t*>(p.y) + row * p.ldy + n0, p.ldy, nv);
+        return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            const int c = 4 * (x >> 1) + (lane & 3);
+            const int n = n0 + 16 * h + 8 * (x & 1) + (lane >> 2);
+            if (c < nv && n < p.N) store_out(p.y, (row + c) * p.ldy + n, p.out, v[h][x]);
+        }
+}
 
 template <class C>
 __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
@@ -71,9 +157,11 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* empty = full + C::NST;          // [NST] each CTA's
     uint64_t* sc_full = empty + C::NST;
     uint64_t* sc_empty = sc_full + SC_RING;
-    uint64_t* acc_full = sc_empty + SC_RING;  // [2] each CTA's
-    uint64_t* acc_empty = acc_full + 2;       // [2] first CTA's: both epilogues are done
-    uint64_t* mma_done = acc_empty + 2;
+    uint64_t* acc_full = sc_empty + SC_RING;  // [NBUF] each CTA's
+    uint64_t* acc_empty = acc_full + C::NBUF; // [NBUF] first CTA's: both epilogues have read it
+    uint64_t* mma_done = acc_empty + C::NBUF;
+    uint64_t* up_full = mma_done + 1;         // [8] SwiGLU form: up's values of a run are staged
+    uint64_t* up_empty = up_full + P_EPI / 2; // [8] and have been read
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BAR);
     int* t_lo = reinterpret_cast<int*>(base + C::O_TAB);
     int* t_hi = t_lo + p.E;
@@ -92,10 +180,15 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&sc_full[i], 64);
             mbar_init(&sc_empty[i], P_EPI);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::NBUF; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 2 * P_EPI);
         }
+        if constexpr (C::GU)
+            for (int i = 0; i < P_EPI / 2; ++i) {
+                mbar_init(&up_full[i], 32);
+                mbar_init(&up_empty[i], 32);
+            }
         mbar_init(mma_done, 1);
         fence_barrier_init();
     }
@@ -171,11 +264,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
                 for (int kb = 0; kb < p.kb; ++kb) {
                     const bool fresh = C::F8 || kb == 0;
-                    if (fresh && !mbar_wait_spin(&acc_empty[ab], aph, p.err, DEV_GMM_TIMEOUT)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT)) {
+                    if (!mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT) ||
+                        (fresh &&
+                         !mbar_wait_spin(&acc_empty[ab], aph, p.err, DEV_GMM_TIMEOUT))) {
                         ok = false;
                         break;
                     }
@@ -201,7 +292,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                         if (last) umma::commit_pair(&acc_full[ab]);
                     }
                     __syncwarp();
-                    if (last && (ab ^= 1) == 0) aph ^= 1;
+                    if (last && ++ab == C::NBUF) {
+                        ab = 0;
+                        aph ^= 1;
+                    }
                     if (++s == C::NST) {
                         s = 0;
                         ph ^= 1;
@@ -237,7 +331,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                     const int nk = min(SC_BLK, p.kb - k0);
                     for (int j = lt; j < w.np; j += 64)
                         for (int b = 0; b < nk; ++b)
-                            cp_async4(dst + (b * C::SC_ROW + j) * 4,
+                            cp_async4(dst + (b * C::SC_ROW + sc_slot(j)) * 4,
                                       xs + (j < w.nv ? j : 0) * static_cast<int64_t>(p.kb) + k0 + b,
                                       j < w.nv);
                     if (has_w)
@@ -252,206 +346,194 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         // ------------------------------------------------------- epilogue
         regs_inc<P_REGS_EPI>();
         const int quad = warp & 3, cg = (warp - 4) >> 2;
-        const int lr = lane >> 2, lc = 2 * (lane & 3);  // fragment row and column
-        const uint32_t tm_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const int lr = lane >> 2, lc = lane & 3;  // fragment row and column
         const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
+        // this warp's first run: its column among the tokens, its buffer column
+        const int run_col = (C::GU ? cg & 1 : cg) * P_CH;
+        const uint32_t tm_run = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
+                                (C::GU ? (cg >> 1) * C::NT + run_col : run_col);
         uint8_t* stage = base + C::O_OUT + (warp - 4) * C::OUT_BYTES;
-        int ab = 0, ch = 0, par = 0;
+        uint32_t ab = 0, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step, par ^= 1) {
-            const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
-            const int nbi = 2 * w.nbi + static_cast<int>(rank);
-            // acc[part][row half][4 i + 2 j + b]: weight row 16 half + 8 j + lr of this
-            // warp's 32, column 8 i + lc + b of its run.  Parts: runs cg and
-            // cg + P_CG of the columns, or run cg of gate and of up.
-            float acc[2][2][16];
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int c = 0; c < 32; ++c) acc[q][c >> 4][c & 15] = 0.f;
-            const int parts = C::GU ? (cg * P_CH < w.np ? 2 : 0)
-                                    : (cg * P_CH < w.np) + ((cg + P_CG) * P_CH < w.np);
-            const int periods = C::F8 ? p.kb : 1;
-            for (int k = 0; k < periods; ++k, ++ab) {
-                const float* sc = nullptr;
-                const int kk = k % SC_BLK;
-                if constexpr (C::F8) {
-                    const int s = ch % SC_RING;
-                    if (kk == 0 && !mbar_wait_spin(&sc_full[s], (ch / SC_RING) & 1, p.err,
-                                                   DEV_GMM_TIMEOUT)) {
-                        ok = false;
-                        break;
-                    }
-                    sc = ring + s * C::SC_STAGE + kk * C::SC_ROW;
-                }
-                if (!mbar_wait_spin(&acc_full[ab & 1], (ab >> 1) & 1, p.err, DEV_GMM_TIMEOUT)) {
-                    ok = false;
-                    break;
-                }
+            if constexpr (!C::F8) {
+                const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
+                const int n0 = (2 * w.nbi + static_cast<int>(rank)) * TILE_W + quad * 32;
+                ok = mbar_wait_spin(&acc_full[ab], aph, p.err, DEV_GMM_TIMEOUT);
+                if (!ok) break;
                 umma::fence_after_sync();
-                const uint32_t src0 = tm_lane + (ab & 1) * C::TM_BUF + cg * P_CH;
-                if (parts == 0 && lane == 0) mbar_arrive_cluster(acc_empty0 + (ab & 1) * 8);
+#pragma unroll 1
+                for (int i = 0; i < C::RUNS; ++i) {
+                    const int col = run_col + i * (P_CG * P_CH);
+                    Frag f;
+                    float v[2][16];
+                    if (col < w.np) {
+                        frag_load(tm_run + ab * C::TM_BUF + i * (P_CG * P_CH), f);
+                        frag_wait(f);
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (q < parts) {
-                        uint32_t r0[16], r1[16];
-                        umma::ld_16x256b_x4(src0 + q * (P_CG * P_CH), r0);
-                        umma::ld_16x256b_x4(src0 + q * (P_CG * P_CH) + (16u << 16), r1);
-                        float2 s[4];
-                        if constexpr (C::F8) {
-                            const float sw = sc[C::NT + (C::GU ? q : 0)];
-                            const float* sx = sc + (C::GU ? cg : cg + P_CG * q) * P_CH + lc;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                s[i] = *reinterpret_cast<const float2*>(sx + 8 * i);
-                                s[i].x *= sw;
-                                s[i].y *= sw;
-                            }
-                        }
-                        umma::wait_ld(r0);
-                        umma::wait_ld(r1);
-                        if (q == parts - 1) {
-                            umma::fence_before_sync();
-                            if (lane == 0) mbar_arrive_cluster(acc_empty0 + (ab & 1) * 8);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 16; c += 2) {
-                            if constexpr (C::F8) {
-                                fma2(acc[q][0][c], acc[q][0][c + 1], __uint_as_float(r0[c]),
-                                     __uint_as_float(r0[c + 1]), s[c / 4].x, s[c / 4].y);
-                                fma2(acc[q][1][c], acc[q][1][c + 1], __uint_as_float(r1[c]),
-                                     __uint_as_float(r1[c + 1]), s[c / 4].x, s[c / 4].y);
-                            } else {
-                                acc[q][0][c] = __uint_as_float(r0[c]);
-                                acc[q][0][c + 1] = __uint_as_float(r0[c + 1]);
-                                acc[q][1][c] = __uint_as_float(r1[c]);
-                                acc[q][1][c + 1] = __uint_as_float(r1[c + 1]);
-                            }
+                        for (int c = 0; c < 16; ++c) {
+                            v[0][c] = __uint_as_float(f.lo[c]);
+                            v[1][c] = __uint_as_float(f.hi[c]);
                         }
                     }
-                if constexpr (C::F8) {
-                    if (kk == SC_BLK - 1 || k == periods - 1) {
+                    if (i == C::RUNS - 1) {
+                        umma::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sc_empty[ch % SC_RING]);
-                        ++ch;
+                        if (lane == 0) mbar_arrive_cluster(acc_empty0 + ab * 8);
+                    }
+                    if (col < w.np)
+                        store_run(p, stage, v, lane, w.row0 + col, w.nv - col, n0);
+                }
+                if (++ab == C::NBUF) {
+                    ab = 0;
+                    aph ^= 1;
+                }
+            } else {
+                // acc[row half][2 i + j]: weight row 16 half + 8 j + lr of this warp's 32,
+                // column 4 i + lc of its run
+                float acc[2][16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) acc[0][c] = acc[1][c] = 0.f;
+                const bool live = run_col < tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E).np;
+#pragma unroll 1
+                for (int k0 = 0; k0 < p.kb && ok; k0 += SC_BLK) {
+                    ok = mbar_wait_spin(&sc_full[cs], cph, p.err, DEV_GMM_TIMEOUT);
+                    const int nk = min(SC_BLK, p.kb - k0);
+                    const float* row = ring + cs * C::SC_STAGE;
+#pragma unroll 1
+                    for (int k = 0; k < nk && ok; ++k, row += C::SC_ROW) {
+                        ok = mbar_wait_spin(&acc_full[ab], aph, p.err, DEV_GMM_TIMEOUT);
+                        if (!ok) break;
+                        umma::fence_after_sync();
+                        if (live) {
+                            Frag f;
+                            frag_load(tm_run + ab * C::TM_BUF, f);
+                            const float sw = row[C::NT + (C::GU ? cg >> 1 : 0)];
+                            const float4* sx =
+                                reinterpret_cast<const float4*>(row + run_col + lc * 8);
+                            const float4 s0 = sx[0], s1 = sx[1];
+                            const float s[8] = {s0.x * sw, s0.y * sw, s0.z * sw, s0.w * sw,
+                                                s1.x * sw, s1.y * sw, s1.z * sw, s1.w * sw};
+                            frag_wait(f);
+                            umma::fence_before_sync();
+                            if (lane == 0) mbar_arrive_cluster(acc_empty0 + ab * 8);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                acc[0][c] = fmaf(__uint_as_float(f.lo[c]), s[c / 2], acc[0][c]);
+                                acc[1][c] = fmaf(__uint_as_float(f.hi[c]), s[c / 2], acc[1][c]);
+                            }
+                        } else if (lane == 0) {
+                            mbar_arrive_cluster(acc_empty0 + ab * 8);
+                        }
+                        if (++ab == C::NBUF) {
+                            ab = 0;
+                            aph ^= 1;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_empty[cs]);
+                    if (++cs == SC_RING) {
+                        cs = 0;
+                        cph ^= 1;
                     }
                 }
-            }
-            if (!ok) break;
-            const int n0 = nbi * TILE_W + quad * 32;  // first of this warp's weight rows
-            if constexpr (C::GU) {
-                // a = silu(g) u; this CTA's 128 rows are one scale block of the
-                // activations: maxima over a thread's rows, the lanes, the four warps
-                uint32_t* am = amax + par * 4 * C::NT;
-                const int col = cg * P_CH;
-                if (parts > 0) {
+                if (!ok) break;
+                // the tile, from an index the compiler cannot trace: its fields would
+                // take registers through the K loop
+                int t_again = t;
+                asm volatile("" : "+r"(t_again));
+                const Tile w = tile_at(t_again, C::NT, 32, t_lo, t_hi, t_pre, p.E);
+                const int nbi = 2 * w.nbi + static_cast<int>(rank);
+                const int n0 = nbi * TILE_W + quad * 32;  // first of this warp's weight rows
+                if constexpr (!C::GU) {
+                    store_run(p, stage, acc, lane, w.row0 + run_col, w.nv - run_col, n0);
+                } else {
+                    // up's warps hand their values to gate's warp of the same rows and
+                    // run, thread by thread
+                    const int pair = (cg & 1) * 4 + quad;
+                    float* x = reinterpret_cast<float*>(base + C::O_OUT + pair * 4096);
+                    if (cg >= 2) {
+                        ok = mbar_wait_spin(&up_empty[pair], par ^ 1, p.err, DEV_GMM_TIMEOUT);
+                        if (!ok) break;
+                        if (live) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                            for (int c = 0; c < 16; ++c) {
+                                x[c * 32 + lane] = acc[0][c];
+                                x[(16 + c) * 32 + lane] = acc[1][c];
+                            }
+                        }
+                        mbar_arrive(&up_full[pair]);
+                        continue;
+                    }
+                    ok = mbar_wait_spin(&up_full[pair], par, p.err, DEV_GMM_TIMEOUT);
+                    if (!ok) break;
+                    // a = silu(g) u; this CTA's 128 rows are one scale block of the
+                    // activations: maxima over a thread's rows, the lanes, the four warps
+                    uint32_t* am = amax + par * 4 * C::NT;
+                    if (live) {
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
+                        for (int i = 0; i < 8; ++i) {
                             uint32_t m = 0;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const int x = 4 * q + 2 * j + b;
-                                    const float g = acc[0][h][x], u = acc[1][h][x];
-                                    const float v = __fdividef(g, 1.0f + __expf(-g)) * u;
-                                    acc[0][h][x] = v;
-                                    m = max(m, finite_abs_bits(v));
-                                }
+                            for (int r = 0; r < 4; ++r) {
+                                const float g = acc[r >> 1][2 * i + (r & 1)];
+                                const float u = x[((r >> 1) * 16 + 2 * i + (r & 1)) * 32 + lane];
+                                const float v = __fdividef(g, 1.0f + __expf(-g)) * u;
+                                acc[r >> 1][2 * i + (r & 1)] = v;
+                                m = max(m, finite_abs_bits(v));
+                            }
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
                                 m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                            if (lr == 0) am[quad * C::NT + col + 8 * q + lc + b] = m;
+                            if (lr == 0) am[quad * C::NT + run_col + 4 * i + lc] = m;
                         }
-                }
-                named_bar(1 + cg, 128);
-                if (parts > 0) {
+                    }
+                    named_bar(1 + cg, 128);
+                    if (live) {
+                        uint32_t* codes = reinterpret_cast<uint32_t*>(x);
+                        __syncwarp();  // every lane has read its values of x
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float inv[2];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int j = col + 8 * q + lc + b;
+                        for (int i = 0; i < 8; ++i) {
+                            const int j = run_col + 4 * i + lc;
                             const uint32_t m = max(max(am[j], am[C::NT + j]),
                                                    max(am[2 * C::NT + j], am[3 * C::NT + j]));
-                            float s;
-                            f8_scale(m, &s, &inv[b]);
+                            float s, inv;
+                            f8_scale(m, &s, &inv);
                             if (quad == 0 && lr == 0 && j < w.nv && nbi < p.nb)
                                 p.as[static_cast<int64_t>(w.row0 + j) * p.nb + nbi] = s;
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int x = 4 * q + 2 * j;
-                                const uint32_t c = f8_pack2(acc[0][h][x] * inv[0],
-                                                            acc[0][h][x + 1] * inv[1]);
-                                uint8_t* d = stage + (8 * q + lc) * 32 + 16 * h + 8 * j + lr;
-                                d[0] = static_cast<uint8_t>(c & 0xFF);
-                                d[32] = static_cast<uint8_t>(c >> 8);
-                            }
-                    }
-                    __syncwarp();
-                    // lane = token: 32 bytes of one row of the activations
-                    if (col + lane < w.nv && nbi < p.nb) {
-                        const uint4* src = reinterpret_cast<const uint4*>(stage + lane * 32);
-                        uint4* dst = reinterpret_cast<uint4*>(
-                            p.aq + static_cast<int64_t>(w.row0 + col + lane) * p.N + n0);
-                        dst[0] = src[0];
-                        dst[1] = src[1];
-                    }
-                    __syncwarp();
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int col = (P_CG * i + cg) * P_CH;
-                    if (i >= parts) continue;
-                    if (p.vec_out && n0 + 32 <= p.N) {
-                        // 16-bit y: transposed through shared memory, then 64-byte
-                        // runs of y's rows.  Token c's four 16-byte units lie at
-                        // c * 64 in an order that keeps stores and loads apart in
-                        // the banks.
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const float lo = acc[i][m >> 1][4 * q + 2 * (m & 1)];
-                                const float hi = acc[i][m >> 1][4 * q + 2 * (m & 1) + 1];
-                                v[m] = p.out == OUT_BF16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);
-                            }
-                            const int tok = 8 * q + (lane & 7), unit = lane >> 3;
-                            stmatrix_x4_trans(stage + tok * 64 + ((unit ^ ((tok >> 1) & 3)) << 4),
-                                              v[0], v[1], v[2], v[3]);
+                            // one word: rows lr, lr + 8, lr + 16, lr + 24 of token 4 i + lc
+                            codes[(4 * i + lc) * 8 + lr] =
+                                f8_pack2(acc[0][2 * i] * inv, acc[0][2 * i + 1] * inv) |
+                                (f8_pack2(acc[1][2 * i] * inv, acc[1][2 * i + 1] * inv) << 16);
                         }
                         __syncwarp();
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int tok = 8 * q + (lane >> 2), unit = lane & 3;
-                            const uint4 v = *reinterpret_cast<const uint4*>(
-                                stage + tok * 64 + ((unit ^ ((tok >> 1) & 3)) << 4));
-                            if (col + tok < w.nv)
-                                *reinterpret_cast<uint4*>(
-                                    static_cast<uint16_t*>(p.y) +
-                                    static_cast<int64_t>(w.row0 + col + tok) * p.ldy + n0 +
-                                    8 * unit) = v;
+                        // lane = token: its eight words' bytes in row order, 32 bytes of
+                        // one row of the activations
+                        if (run_col + lane < w.nv && nbi < p.nb) {
+                            const uint4 a = *reinterpret_cast<const uint4*>(codes + lane * 8);
+                            const uint4 b = *reinterpret_cast<const uint4*>(codes + lane * 8 + 4);
+                            // bytes k, k+8, k+16, k+24 of word k -> four runs of eight
+                            const uint32_t a01 = __byte_perm(a.x, a.y, 0x5140),
+                                           a23 = __byte_perm(a.z, a.w, 0x5140),
+                                           b01 = __byte_perm(b.x, b.y, 0x5140),
+                                           b23 = __byte_perm(b.z, b.w, 0x5140),
+                                           c01 = __byte_perm(a.x, a.y, 0x7362),
+                                           c23 = __byte_perm(a.z, a.w, 0x7362),
+                                           d01 = __byte_perm(b.x, b.y, 0x7362),
+                                           d23 = __byte_perm(b.z, b.w, 0x7362);
+                            uint4* dst = reinterpret_cast<uint4*>(
+                                p.aq + static_cast<int64_t>(w.row0 + run_col + lane) * p.N + n0);
+                            dst[0] = make_uint4(__byte_perm(a01, a23, 0x5410),
+                                                __byte_perm(b01, b23, 0x5410),
+                                                __byte_perm(a01, a23, 0x7632),
+                                                __byte_perm(b01, b23, 0x7632));
+                            dst[1] = make_uint4(__byte_perm(c01, c23, 0x5410),
+                                                __byte_perm(d01, d23, 0x5410),
+                                                __byte_perm(c01, c23, 0x7632),
+                                                __byte_perm(d01, d23, 0x7632));
                         }
-                        __syncwarp();
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const int c = col + 8 * (x >> 2) + lc + (x & 1);
-                                const int n = n0 + 16 * h + 8 * ((x >> 1) & 1) + lr;
-                                if (c < w.nv && n < p.N)
-                                    store_out(p.y, static_cast<int64_t>(w.row0 + c) * p.ldy + n,
-                                              p.out, acc[i][h][x]);
-                            }
                     }
+                    mbar_arrive(&up_empty[pair]);
                 }
             }
         }

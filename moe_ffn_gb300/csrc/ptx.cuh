@@ -303,15 +303,4 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Four 8x8 tiles of 16-bit values to shared memory, transposed: thread T
-// holds row T / 4, columns 2 (T % 4) and + 1 of each; lane 8 m + j gives the
-// address of column j of tile m.
-__device__ __forceinline__ void stmatrix_x4_trans(void* dst, uint32_t a, uint32_t b, uint32_t c,
-                                                  uint32_t d) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                     smem_u32(dst)),
-                 "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
-
 }  // namespace qmoe

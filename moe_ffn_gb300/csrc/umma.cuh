@@ -193,11 +193,11 @@ __device__ __forceinline__ void wait_ld() {
 }
 
 // 16 lanes (from taddr's, a multiple of 16) x 32 columns: thread T gets, for
-// i = 0..3, columns 8 i + 2 (T % 4) and + 1 of lane T / 4 in r[4i], r[4i+1]
-// and of lane T / 4 + 8 in r[4i+2], r[4i+3].
-__device__ __forceinline__ void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+// i = 0..7, column 4 i + T % 4 of lane T / 4 in r[2i] and of lane T / 4 + 8 in
+// r[2i+1].
+__device__ __forceinline__ void ld_16x128b_x8(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
