@@ -51,8 +51,7 @@ struct PairCfg {
     static constexpr int TM_COLS = 512;
     static constexpr int NBUF = TM_COLS / TM_BUF;      // accumulator buffers
     static constexpr int RUNS = TM_BUF / P_CH / P_CG;  // runs per epilogue warp and buffer
-    static constexpr int SC_ROW = NT + 4;  // scales of x, then of W (gate, up)
-    static constexpr int SC_STAGE = SC_BLK * SC_ROW;  // floats
+    static constexpr int SC_STAGE = SC_BLK * NA * NT;  // floats: sx sw of every column
     // staging per epilogue warp: 32 tokens of 32 16-bit values; SwiGLU form:
     // per pair of warps, up's 32 x 32 f32 values on their way to gate's warp
     static constexpr int OUT_BYTES = 2048;
@@ -66,6 +65,7 @@ struct PairCfg {
     static_assert(TM_BUF * NBUF == TM_COLS && STAGE % 1024 == 0, "tile shape");
     static_assert((NT / 2) % BOX == 0, "boxes fill a stage exactly");
     static_assert(RUNS == (F8 ? 1 : 2), "e4m3: one run per warp; 16-bit: two");
+    static_assert(!F8 || NBUF == SC_BLK, "a tile's k-block b uses buffer b % 4");
 };
 
 // Where token j's scale lies in a row of the ring: a thread's eight columns of
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < SC_RING; ++i) {
-            mbar_init(&sc_full[i], 64);
+            mbar_init(&sc_full[i], 2);
             mbar_init(&sc_empty[i], P_EPI);
         }
         for (int i = 0; i < C::NBUF; ++i) {
@@ -255,18 +255,21 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         } else if (warp == 1 && rank == 0) {
             // -------------------------------------------------------- MMA
             int s = 0;
-            uint32_t ph = 0, ab = 0, aph = 1;  // stage and accumulator phases
+            uint32_t ph = 0, aph = ~0u;  // stage phase; a phase bit per accumulator buffer
+            uint32_t ab = C::NBUF - 1;
             bool ok = true;
             const uint64_t da0 = umma::desc_sw128(smem_u32(base));
             const uint64_t db0 = umma::desc_sw128(smem_u32(base) + C::NA * C::A_BYTES);
             for (int t = first; t < tiles && ok; t += step) {
                 const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
+                if constexpr (!C::F8) ab = (ab + 1) % C::NBUF;
                 for (int kb = 0; kb < p.kb; ++kb) {
                     const bool fresh = C::F8 || kb == 0;
+                    if constexpr (C::F8) ab = kb % C::NBUF;
                     if (!mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT) ||
-                        (fresh &&
-                         !mbar_wait_spin(&acc_empty[ab], aph, p.err, DEV_GMM_TIMEOUT))) {
+                        (fresh && !mbar_wait_spin(&acc_empty[ab], (aph >> ab) & 1, p.err,
+                                                  DEV_GMM_TIMEOUT))) {
                         ok = false;
                         break;
                     }
@@ -292,10 +295,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                         if (last) umma::commit_pair(&acc_full[ab]);
                     }
                     __syncwarp();
-                    if (last && ++ab == C::NBUF) {
-                        ab = 0;
-                        aph ^= 1;
-                    }
+                    if (last) aph ^= 1u << ab;
                     if (++s == C::NST) {
                         s = 0;
                         ph ^= 1;
@@ -307,40 +307,66 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_wait_spin(mma_done, 0, p.err, DEV_GMM_TIMEOUT);
         } else if (C::F8 && warp >= 2) {
             // ----------------------------------------------------- scales
-            // sx[row][kb] to ring[kb][row] by 4-byte asynchronous copies (zeros
-            // past the tile's rows), with this CTA's sw[kb] behind them
+            // ring[kb][column] = sx[column][kb] sw[kb] (0 past the tile's rows); the
+            // next four k-blocks' scales are in flight while these are stored
             const int lt = tid - 64;
-            int ch = 0;
+            constexpr int RPT = C::NT / 64;
+            const bool vec = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.xs) & 15) == 0;
+            int s = 0;
+            uint32_t ph = 1;
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
                 const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const int nbi = 2 * w.nbi + static_cast<int>(rank);
+                const bool rows_in = nbi < p.nb;  // the last weight tile's second half may be empty
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + nbi) * p.kb;
-                const float* xs = p.xs + static_cast<int64_t>(w.row0) * p.kb;
-                // the second half of the last weight tile may be empty
-                const float* ws = (lt == 0 ? p.ws : p.ws2) + wo;
-                const bool has_w = lt < C::NA && nbi < p.nb;
-                for (int k0 = 0; k0 < p.kb; k0 += SC_BLK, ++ch) {
-                    const int s = ch % SC_RING, round = ch / SC_RING;
-                    if (round > 0 && !mbar_wait_spin(&sc_empty[s], (round - 1) & 1, p.err,
-                                                     DEV_GMM_TIMEOUT)) {
+                const float* xs = p.xs + (static_cast<int64_t>(w.row0) + lt) * p.kb;
+                float v[RPT][SC_BLK], g[C::NA][SC_BLK];
+                auto fetch = [&](int k0) {
+#pragma unroll
+                    for (int i = 0; i < RPT; ++i) {
+                        const float* src = xs + static_cast<int64_t>(64 * i) * p.kb + k0;
+                        const bool in = lt + 64 * i < w.nv;
+                        if (vec && in) {
+                            const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
+                            v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < SC_BLK; ++b)
+                                v[i][b] = in && k0 + b < p.kb ? __ldcg(src + b) : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < SC_BLK; ++b) {
+                        const bool in = rows_in && k0 + b < p.kb;
+                        g[0][b] = in ? __ldg(p.ws + wo + k0 + b) : 0.f;
+                        if constexpr (C::GU) g[1][b] = in ? __ldg(p.ws2 + wo + k0 + b) : 0.f;
+                    }
+                };
+                fetch(0);
+                for (int k0 = 0; k0 < p.kb; k0 += SC_BLK) {
+                    if (!mbar_wait_spin(&sc_empty[s], ph, p.err, DEV_GMM_TIMEOUT)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = smem_u32(ring + s * C::SC_STAGE);
-                    const int nk = min(SC_BLK, p.kb - k0);
-                    for (int j = lt; j < w.np; j += 64)
-                        for (int b = 0; b < nk; ++b)
-                            cp_async4(dst + (b * C::SC_ROW + sc_slot(j)) * 4,
-                                      xs + (j < w.nv ? j : 0) * static_cast<int64_t>(p.kb) + k0 + b,
-                                      j < w.nv);
-                    if (has_w)
-                        for (int b = 0; b < nk; ++b)
-                            cp_async4(dst + (b * C::SC_ROW + C::NT + lt) * 4, ws + k0 + b, true);
-                    cp_async_arrive(&sc_full[s]);
+                    float* dst = ring + s * C::SC_STAGE;
+#pragma unroll
+                    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+                        for (int b = 0; b < SC_BLK; ++b)
+#pragma unroll
+                            for (int a = 0; a < C::NA; ++a)
+                                dst[(b * C::NA + a) * C::NT + sc_slot(lt + 64 * i)] =
+                                    v[i][b] * g[a][b];
+                    if (k0 + SC_BLK < p.kb) fetch(k0 + SC_BLK);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[s]);
+                    if (++s == SC_RING) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
             }
-            cp_async_drain();
         }
     } else {
         // ------------------------------------------------------- epilogue
@@ -353,14 +379,16 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         const uint32_t tm_run = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
                                 (C::GU ? (cg >> 1) * C::NT + run_col : run_col);
         uint8_t* stage = base + C::O_OUT + (warp - 4) * C::OUT_BYTES;
-        uint32_t ab = 0, aph = 0, cs = 0, cph = 0, par = 0;
+        uint32_t ab = C::NBUF - 1, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step, par ^= 1) {
             if constexpr (!C::F8) {
                 const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const int n0 = (2 * w.nbi + static_cast<int>(rank)) * TILE_W + quad * 32;
-                ok = mbar_wait_spin(&acc_full[ab], aph, p.err, DEV_GMM_TIMEOUT);
+                ab = (ab + 1) % C::NBUF;
+                ok = mbar_wait_spin(&acc_full[ab], (aph >> ab) & 1, p.err, DEV_GMM_TIMEOUT);
                 if (!ok) break;
+                aph ^= 1u << ab;
                 umma::fence_after_sync();
 #pragma unroll 1
                 for (int i = 0; i < C::RUNS; ++i) {
@@ -384,10 +412,6 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                     if (col < w.np)
                         store_run(p, stage, v, lane, w.row0 + col, w.nv - col, n0);
                 }
-                if (++ab == C::NBUF) {
-                    ab = 0;
-                    aph ^= 1;
-                }
             } else {
                 // acc[row half][2 i + j]: weight row 16 half + 8 j + lr of this warp's 32,
                 // column 4 i + lc of its run
@@ -395,41 +419,40 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                 for (int c = 0; c < 16; ++c) acc[0][c] = acc[1][c] = 0.f;
                 const bool live = run_col < tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E).np;
+                const float* run = ring + (C::GU ? (cg >> 1) * C::NT : 0) + run_col + lc * 8;
 #pragma unroll 1
-                for (int k0 = 0; k0 < p.kb && ok; k0 += SC_BLK) {
+                for (int k0 = 0; k0 < p.kb; k0 += SC_BLK) {
                     ok = mbar_wait_spin(&sc_full[cs], cph, p.err, DEV_GMM_TIMEOUT);
+                    if (!ok) break;
+                    const float* row = run + cs * C::SC_STAGE;
                     const int nk = min(SC_BLK, p.kb - k0);
-                    const float* row = ring + cs * C::SC_STAGE;
-#pragma unroll 1
-                    for (int k = 0; k < nk && ok; ++k, row += C::SC_ROW) {
-                        ok = mbar_wait_spin(&acc_full[ab], aph, p.err, DEV_GMM_TIMEOUT);
+#pragma unroll
+                    for (int k = 0; k < SC_BLK; ++k) {
+                        if (k >= nk) break;
+                        ok = mbar_wait_spin(&acc_full[k], (aph >> k) & 1, p.err, DEV_GMM_TIMEOUT);
                         if (!ok) break;
-                        umma::fence_after_sync();
                         if (live) {
+                            umma::fence_after_sync();
                             Frag f;
-                            frag_load(tm_run + ab * C::TM_BUF, f);
-                            const float sw = row[C::NT + (C::GU ? cg >> 1 : 0)];
+                            frag_load(tm_run + k * C::TM_BUF, f);
                             const float4* sx =
-                                reinterpret_cast<const float4*>(row + run_col + lc * 8);
+                                reinterpret_cast<const float4*>(row + k * C::NA * C::NT);
                             const float4 s0 = sx[0], s1 = sx[1];
-                            const float s[8] = {s0.x * sw, s0.y * sw, s0.z * sw, s0.w * sw,
-                                                s1.x * sw, s1.y * sw, s1.z * sw, s1.w * sw};
+                            const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
                             frag_wait(f);
                             umma::fence_before_sync();
-                            if (lane == 0) mbar_arrive_cluster(acc_empty0 + ab * 8);
+                            if (lane == 0) mbar_arrive_cluster(acc_empty0 + k * 8);
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
                                 acc[0][c] = fmaf(__uint_as_float(f.lo[c]), s[c / 2], acc[0][c]);
                                 acc[1][c] = fmaf(__uint_as_float(f.hi[c]), s[c / 2], acc[1][c]);
                             }
                         } else if (lane == 0) {
-                            mbar_arrive_cluster(acc_empty0 + ab * 8);
-                        }
-                        if (++ab == C::NBUF) {
-                            ab = 0;
-                            aph ^= 1;
+                            mbar_arrive_cluster(acc_empty0 + k * 8);
                         }
                     }
+                    if (!ok) break;
+                    aph ^= (1u << nk) - 1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_empty[cs]);
                     if (++cs == SC_RING) {
