@@ -22,8 +22,8 @@
 // the buffers are four of 128 columns, a warp reads one fragment of each, and
 // hands the buffer back before it adds the values.
 //
-// Roles (640 threads): warp 0 loads, warp 1 (of the first CTA) issues the
-// MMAs, warps 2-3 copy scales, warps 4-19 are the epilogue: warp w reads
+// Roles (640 threads): warps 0 and 2 load, warp 1 (of the first CTA)
+// issues the MMAs, warp 3 stages scale products, warps 4-19 are the epilogue: warp w reads
 // lanes 32 (w % 4) .. + 31 and every fourth run of 32 columns (SwiGLU form:
 // run w / 4 % 2 of gate, w < 12, or of up).
 #pragma once
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < SC_RING; ++i) {
-            mbar_init(&sc_full[i], 2);
+            mbar_init(&sc_full[i], 1);
             mbar_init(&sc_empty[i], P_EPI);
         }
         for (int i = 0; i < C::NBUF; ++i) {
@@ -206,8 +206,11 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
 
     if (warp < 4) {
         regs_dec<P_REGS_LOAD>();
-        if (warp == 0) {
+        if (warp == 0 || warp == 2) {
             // ------------------------------------------------------ loads
+            // warp 0 the weights, warp 2 the token rows: one warp issuing both
+            // was as slow as the MMAs of a stage
+            const bool wgt = warp == 0;
             int it = 0, s = 0;
             uint32_t ph = 1;  // parity of the wait for a free stage
             bool ok = true;
@@ -217,8 +220,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                 const int half = w.np >> 1;
                 const int boxes = (half + C::BOX - 1) / C::BOX;
                 const uint32_t bytes = 2 * (C::NA * C::A_BYTES + boxes * C::BOX * KBLK);
-                const int wrow = (2 * w.nbi + static_cast<int>(rank)) * TILE_W;
-                const int xrow = w.row0 + static_cast<int>(rank) * half;
+                const int y = wgt ? (2 * w.nbi + static_cast<int>(rank)) * TILE_W
+                                  : w.row0 + static_cast<int>(rank) * half;
+                int kx = 0;  // coordinates along K: multiples of 128 bytes
                 for (int kb = 0; kb < p.kb; ++kb, ++it) {
                     // (before any use of a stage the wait passes at once)
                     if (!mbar_wait_spin(&empty[s], ph, p.err, DEV_GMM_TIMEOUT)) {
@@ -228,19 +232,22 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                     if (elect_one()) {
                         uint8_t* st = base + s * C::STAGE;
                         const uint32_t bar = full0 + s * 8;
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                        const int kx = C::F8 ? kb * KBLK : kb * (KBLK / 2);
-                        tma_load_3d_pair(st, &tm_w, kx, wrow, w.e, bar);
-                        if constexpr (C::GU)
-                            tma_load_3d_pair(st + C::A_BYTES, &tm_w2, kx, wrow, w.e, bar);
-                        uint8_t* sb = st + C::NA * C::A_BYTES;
+                        if (wgt) {
+                            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                            tma_load_3d_pair(st, &tm_w, kx, y, w.e, bar);
+                            if constexpr (C::GU)
+                                tma_load_3d_pair(st + C::A_BYTES, &tm_w2, kx, y, w.e, bar);
+                        } else {
+                            st += C::NA * C::A_BYTES;
 #pragma unroll
-                        for (int b = 0; b < C::NT / 2 / C::BOX; ++b)
-                            if (b < boxes)
-                                tma_load_2d_pair(sb + b * C::BOX * KBLK, &tm_x, kx,
-                                                 xrow + b * C::BOX, bar);
+                            for (int b = 0; b < C::NT / 2 / C::BOX; ++b)
+                                if (b < boxes)
+                                    tma_load_2d_pair(st + b * C::BOX * KBLK, &tm_x, kx,
+                                                     y + b * C::BOX, bar);
+                        }
                     }
                     __syncwarp();
+                    kx += C::F8 ? KBLK : KBLK / 2;
                     if (++s == C::NST) {
                         s = 0;
                         ph ^= 1;
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             }
             // never leave with copies in flight (the pair's: the other CTA
             // leaves only after the cluster barrier at the end)
-            if (rank == 0)
+            if (wgt && rank == 0)
                 for (int k = max(it - C::NST, 0); k < it; ++k)
                     mbar_wait_spin(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
         } else if (warp == 1 && rank == 0) {
@@ -259,58 +266,66 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             uint32_t ab = C::NBUF - 1;
             bool ok = true;
             const uint64_t da0 = umma::desc_sw128(smem_u32(base));
-            const uint64_t db0 = umma::desc_sw128(smem_u32(base) + C::NA * C::A_BYTES);
+            const uint32_t hi = static_cast<uint32_t>(da0 >> 32), lo0 = static_cast<uint32_t>(da0);
+            uint32_t lo = lo0;  // the stage's descriptor, low word
             for (int t = first; t < tiles && ok; t += step) {
                 const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
                 if constexpr (!C::F8) ab = (ab + 1) % C::NBUF;
-                for (int kb = 0; kb < p.kb; ++kb) {
-                    const bool fresh = C::F8 || kb == 0;
-                    if constexpr (C::F8) ab = kb % C::NBUF;
-                    if (!mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT) ||
-                        (fresh && !mbar_wait_spin(&acc_empty[ab], (aph >> ab) & 1, p.err,
-                                                  DEV_GMM_TIMEOUT))) {
-                        ok = false;
-                        break;
-                    }
-                    umma::fence_after_sync();
-                    const bool last = C::F8 || kb == p.kb - 1;
-                    if (elect_one()) {
-                        // 32 bytes of K further: the descriptors' address field + 2
-                        const uint64_t da = da0 + s * (C::STAGE >> 4);
-                        const uint64_t db = db0 + s * (C::STAGE >> 4);
-                        const uint32_t d = tmem + ab * C::TM_BUF;
+#pragma unroll 1
+                for (int k0 = 0; k0 < p.kb && ok; k0 += C::NBUF) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                    for (int k = 0; k < C::NBUF; ++k) {
+                        if (k0 + k >= p.kb) break;
+                        if constexpr (C::F8) ab = k;
+                        const bool fresh = C::F8 || k0 + k == 0;
+                        const bool last = C::F8 || k0 + k == p.kb - 1;
+                        // both waits tried before either is acted on
+                        bool r0 = mbar_try_wait(&full[s], ph), r1 = true;
+                        if (fresh) r1 = mbar_try_wait(&acc_empty[ab], (aph >> ab) & 1);
+                        if (!r0) r0 = mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT);
+                        if (!r1)
+                            r1 = mbar_wait_spin(&acc_empty[ab], (aph >> ab) & 1, p.err,
+                                                DEV_GMM_TIMEOUT);
+                        if (!(r0 && r1)) {
+                            ok = false;
+                            break;
+                        }
+                        umma::fence_after_sync();
+                        if (elect_one()) {
+                            const uint32_t d = tmem + ab * C::TM_BUF;
+                            // 32 bytes of K further: the descriptors' address field + 2
 #pragma unroll
-                            for (int a = 0; a < C::NA; ++a) {
-                                const uint32_t acc = (!fresh || j > 0) ? 1u : 0u;
-                                const uint64_t daj = da + a * (C::A_BYTES >> 4) + 2 * j;
-                                if constexpr (C::F8)
-                                    umma::mma_f8_pair(d + a * C::NT, daj, db + 2 * j, idesc, acc);
-                                else
-                                    umma::mma_f16_pair(d + a * C::NT, daj, db + 2 * j, idesc, acc);
-                            }
-                        umma::commit_pair(&empty[s]);
-                        if (last) umma::commit_pair(&acc_full[ab]);
-                    }
-                    __syncwarp();
-                    if (last) aph ^= 1u << ab;
-                    if (++s == C::NST) {
-                        s = 0;
-                        ph ^= 1;
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int a = 0; a < C::NA; ++a) {
+                                    const uint32_t acc = (!fresh || j > 0) ? 1u : 0u;
+                                    const uint32_t aj = lo + a * (C::A_BYTES >> 4) + 2 * j;
+                                    const uint32_t bj = lo + C::NA * (C::A_BYTES >> 4) + 2 * j;
+                                    umma::mma_pair<C::F8>(d + a * C::NT, aj, bj, hi, idesc, acc);
+                                }
+                            umma::commit_pair(&empty[s]);
+                            if (last) umma::commit_pair(&acc_full[ab]);
+                        }
+                        __syncwarp();
+                        if (last) aph ^= 1u << ab;
+                        lo += C::STAGE >> 4;
+                        if (++s == C::NST) {
+                            s = 0;
+                            ph ^= 1;
+                            lo = lo0;
+                        }
                     }
                 }
             }
             if (elect_one()) umma::commit_pair(mma_done);
             __syncwarp();
             mbar_wait_spin(mma_done, 0, p.err, DEV_GMM_TIMEOUT);
-        } else if (C::F8 && warp >= 2) {
+        } else if (C::F8 && warp == 3) {
             // ----------------------------------------------------- scales
             // ring[kb][column] = sx[column][kb] sw[kb] (0 past the tile's rows); the
             // next four k-blocks' scales are in flight while these are stored
-            const int lt = tid - 64;
-            constexpr int RPT = C::NT / 64;
+            constexpr int RPT = C::NT / 32;
             const bool vec = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.xs) & 15) == 0;
             int s = 0;
             uint32_t ph = 1;
@@ -320,13 +335,13 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                 const int nbi = 2 * w.nbi + static_cast<int>(rank);
                 const bool rows_in = nbi < p.nb;  // the last weight tile's second half may be empty
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + nbi) * p.kb;
-                const float* xs = p.xs + (static_cast<int64_t>(w.row0) + lt) * p.kb;
+                const float* xs = p.xs + (static_cast<int64_t>(w.row0) + lane) * p.kb;
                 float v[RPT][SC_BLK], g[C::NA][SC_BLK];
                 auto fetch = [&](int k0) {
 #pragma unroll
                     for (int i = 0; i < RPT; ++i) {
-                        const float* src = xs + static_cast<int64_t>(64 * i) * p.kb + k0;
-                        const bool in = lt + 64 * i < w.nv;
+                        const float* src = xs + static_cast<int64_t>(32 * i) * p.kb + k0;
+                        const bool in = lane + 32 * i < w.nv;
                         if (vec && in) {
                             const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
                             v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                         for (int b = 0; b < SC_BLK; ++b)
 #pragma unroll
                             for (int a = 0; a < C::NA; ++a)
-                                dst[(b * C::NA + a) * C::NT + sc_slot(lt + 64 * i)] =
+                                dst[(b * C::NA + a) * C::NT + sc_slot(lane + 32 * i)] =
                                     v[i][b] * g[a][b];
                     if (k0 + SC_BLK < p.kb) fetch(k0 + SC_BLK);
                     __syncwarp();
