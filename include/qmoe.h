@@ -378,8 +378,9 @@ size_t moe_experts_f8_workspace_size(const qmoe_moe_shape* shape);
  *   xq = f8_quantize(x_t);  for each slot s with e = topk_idx[t][s] in [0, E):
  *   a = silu(G_e xq) * (U_e xq) in f32,  aq = f8_quantize(a),
  *   out_t = residual_t + sum_s topk_w[t][s] * (D_e aq)
- * with sums in f32 and one rounding into out.  topk_idx and topk_w are as
- * moe_ffn returns them; any other routing rule may supply them.
+ * with sums in f32 and one rounding into out; for QMOE_BF16, D_e aq is rounded
+ * to bf16 before its weight multiplies it.  topk_idx and topk_w are as moe_ffn
+ * returns them; any other routing rule may supply them.
  *   gate_stack, up_stack  [E][F][H] e4m3;  scales [E][F/128][H/128]
  *   down_stack            [E][H][F] e4m3;  scales [E][H/128][F/128]
  *   shape       hidden and expert_dim multiples of 128, num_experts <= 256,

@@ -167,8 +167,9 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
 
 // --------------------------------------------------------------- quantise
 template <class T>
-static cudaError_t launch_quantize(const f8::QuantParams& q, cudaStream_t st) {
-    const int64_t items = q.rows * q.nblk;
+static cudaError_t launch_quantize(f8::QuantParams q, cudaStream_t st) {
+    q.nrun = (q.nblk + f8::Q_RUN - 1) / f8::Q_RUN;
+    const int64_t items = q.rows * q.nrun;
     const unsigned grid = static_cast<unsigned>((items + f8::Q_THREADS / 16 - 1) /
                                                 (f8::Q_THREADS / 16));
     const bool vec = q.cols % 8 == 0 && (q.ldx * sizeof(T)) % 16 == 0 && aligned(q.x, 16) &&
@@ -238,13 +239,36 @@ static qmoe_status moe_f8_shape(const qmoe_moe_shape* s) {
     return QMOE_OK;
 }
 
-template <class T>
-static cudaError_t launch_combine(const float* y, const int32_t* pos, const float* w,
+template <class T, class Y>
+static cudaError_t launch_combine(const void* y, const int32_t* pos, const float* w,
                                   const void* residual, void* out, int T_, int H, int k,
                                   cudaStream_t st) {
-    const int per = f8::C_THREADS * 4;
-    return launch_pdl(f8::combine_kernel<T>, dim3(T_, (H + per - 1) / per), dim3(f8::C_THREADS), 0,
-                      st, y, pos, w, static_cast<const T*>(residual), static_cast<T*>(out), H, k);
+    const int per = f8::C_THREADS * 8;
+    return launch_pdl(f8::combine_kernel<T, Y>, dim3(T_, (H + per - 1) / per),
+                      dim3(f8::C_THREADS), 0, st, static_cast<const Y*>(y), pos, w,
+                      static_cast<const T*>(residual), static_cast<T*>(out), H, k);
+}
+
+// The group kernel: one CTA up to 4,096 pairs, else a cluster of them.
+static cudaError_t launch_group(const int32_t* idx, int P, int E, int32_t* offsets, int32_t* pos,
+                                cudaStream_t st) {
+    int ranks = 1;
+    while (ranks < f8::G_CLUSTER && ranks * 4096 < P) ranks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ranks));
+    cfg.blockDim = dim3(f8::G_THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(f8::G_WARPS + 1) * E * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, f8::group_kernel, idx, P, E, offsets, pos);
 }
 
 }  // namespace qmoe
@@ -431,13 +455,11 @@ qmoe_status moe_experts_f8(const void* gate_stack, const float* gate_scale, cons
     uint8_t* w = static_cast<uint8_t*>(ws);
     int32_t* offsets = reinterpret_cast<int32_t*>(w + L.offsets);
     int32_t* pos = reinterpret_cast<int32_t*>(w + L.pos);
-    float* y = reinterpret_cast<float*>(w + L.y);
+    void* y = w + L.y;
     const int T = s.n_tokens, k = s.top_k, H = s.hidden, F = s.expert_dim, E = s.num_experts;
     const int P = T * k;
 
-    cudaError_t e = launch_pdl(f8::group_kernel, dim3(1), dim3(f8::G_THREADS),
-                               static_cast<size_t>(f8::G_WARPS) * E * 4, st, topk_idx, P, E,
-                               offsets, pos);
+    cudaError_t e = launch_group(topk_idx, P, E, offsets, pos, st);
     if (e != cudaSuccess) return cuda_fail(e, "group launch");
     f8::QuantParams q = {};
     q.x = x;
@@ -483,13 +505,14 @@ qmoe_status moe_experts_f8(const void* gate_stack, const float* gate_scale, cons
     h.p.M = P;
     h.p.N = H;
     h.p.E = E;
-    h.p.out = gmm::OUT_F32;
+    h.p.out = xtype == QMOE_BF16 ? gmm::OUT_BF16 : gmm::OUT_F32;
     if (qmoe_status r = run_gmm(h, *d, st)) return r;
 
-    e = xtype == QMOE_F32    ? launch_combine<float>(y, pos, topk_w, residual, out, T, H, k, st)
-        : xtype == QMOE_BF16 ? launch_combine<__nv_bfloat16>(y, pos, topk_w, residual, out, T, H,
-                                                             k, st)
-                             : launch_combine<__half>(y, pos, topk_w, residual, out, T, H, k, st);
+    e = xtype == QMOE_F32 ? launch_combine<float, float>(y, pos, topk_w, residual, out, T, H, k, st)
+        : xtype == QMOE_BF16
+            ? launch_combine<__nv_bfloat16, __nv_bfloat16>(y, pos, topk_w, residual, out, T, H, k,
+                                                           st)
+            : launch_combine<__half, float>(y, pos, topk_w, residual, out, T, H, k, st);
     if (e != cudaSuccess) return cuda_fail(e, "combine launch");
     return QMOE_OK;
 }

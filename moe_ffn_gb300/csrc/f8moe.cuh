@@ -1,6 +1,8 @@
 // f8moe.cuh — the kernels around the e4m3 products: quantising rows, sorting
 // a layer's (token, slot) pairs by expert, and adding the experts' outputs.
 #pragma once
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -17,9 +19,12 @@ __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
 // ---------------------------------------------------------------- quantise
 // Sixteen lanes share a 128-column block, eight consecutive columns each:
-// one or two 16-byte loads, a four-step maximum, one 8-byte store.  Bound by
-// HBM: (size + 1) bytes per element.  VEC needs 16-byte aligned rows and
-// whole groups of eight columns; the other form loads element by element.
+// one or two 16-byte loads, a four-step maximum, one 8-byte store.  They take
+// Q_RUN neighbouring blocks of a row, all loaded before the first is reduced:
+// bound by HBM, (size + 1) bytes per element, this keeps 64 bytes per thread in
+// flight (one block at a time reached 3.1 TB/s).  VEC needs 16-byte aligned
+// rows and whole groups of eight columns; the other form loads element by
+// element.
 //
 // With pos (the MoE layer), row t is token t and its codes go to the rows
 // pos[t * k + s] of q, one for each slot that names an expert.
@@ -32,8 +37,10 @@ struct QuantParams {
     int k;            // slots per token (pos)
     int64_t rows;
     int cols, nblk;
+    int nrun;         // runs of Q_RUN blocks per row
 };
 constexpr int Q_THREADS = 256;
+constexpr int Q_RUN = 4;
 
 template <class T>
 __device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
@@ -54,90 +61,135 @@ template <class T, bool VEC>
 __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const QuantParams p) {
     pdl_wait();
     pdl_trigger();
-    const int64_t item = (static_cast<int64_t>(blockIdx.x) * Q_THREADS + threadIdx.x) >> 4;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (Q_THREADS / 16) + (threadIdx.x >> 4);
     const int sub = threadIdx.x & 15;
-    const bool live = item < p.rows * p.nblk;
-    const int64_t row = live ? item / p.nblk : 0;
-    const int blk = live ? static_cast<int>(item - row * p.nblk) : 0;
-    const int c0 = blk * F8_BLOCK + sub * 8;
-    const T* src = static_cast<const T*>(p.x) + row * p.ldx + c0;
-    float v[8];
+    int64_t row;
+    int blk0;
+    if (p.rows * p.nrun <= 0x7fffffff) {
+        row = static_cast<uint32_t>(item) / static_cast<uint32_t>(p.nrun);
+        blk0 = (static_cast<int>(item) - static_cast<int>(row) * p.nrun) * Q_RUN;
+    } else {
+        row = item / p.nrun;
+        blk0 = static_cast<int>(item - row * p.nrun) * Q_RUN;
+    }
+    const bool live = row < p.rows;
+    const int nb = live ? min(Q_RUN, p.nblk - blk0) : 0;
+    const int c0 = blk0 * F8_BLOCK + sub * 8;
+    const T* src = static_cast<const T*>(p.x) + (live ? row : 0) * p.ldx + c0;
+    float v[Q_RUN][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (live) {
-        if constexpr (VEC) {
-            if (c0 < p.cols) load8(src, v);
-        } else {
+    for (int b = 0; b < Q_RUN; ++b) {
+        const int c = c0 + b * F8_BLOCK;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c0 + i < p.cols) v[i] = to_f32(src[i]);
+        for (int i = 0; i < 8; ++i) v[b][i] = 0.f;
+        if (b < nb) {
+            if constexpr (VEC) {
+                if (c < p.cols) load8(src + b * F8_BLOCK, v[b]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < p.cols) v[b][i] = to_f32(src[b * F8_BLOCK + i]);
+            }
         }
     }
-    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[i]));
+    for (int b = 0; b < Q_RUN; ++b) {
+        uint32_t m = 0;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (!live) return;
-    float s, inv;
-    f8_scale(m, &s, &inv);
-    uint2 q;
-    q.x = f8_pack2(v[0] * inv, v[1] * inv) | (f8_pack2(v[2] * inv, v[3] * inv) << 16);
-    q.y = f8_pack2(v[4] * inv, v[5] * inv) | (f8_pack2(v[6] * inv, v[7] * inv) << 16);
-    const int nslot = p.pos ? p.k : 1;
-    for (int i = 0; i < nslot; ++i) {
-        const int64_t r = p.pos ? __ldcg(p.pos + row * p.k + i) : row;
-        if (r < 0) continue;
-        uint8_t* dst = p.q + r * p.cols + c0;
-        if constexpr (VEC) {
-            if (c0 < p.cols) *reinterpret_cast<uint2*>(dst) = q;
-        } else {
+        for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[b][i]));
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
-                if (c0 + b < p.cols)
-                    dst[b] = static_cast<uint8_t>((b < 4 ? q.x : q.y) >> (8 * (b & 3)));
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (b >= nb) continue;
+        const int c = c0 + b * F8_BLOCK;
+        float s, inv;
+        f8_scale(m, &s, &inv);
+        uint2 q;
+        q.x = f8_pack2(v[b][0] * inv, v[b][1] * inv) | (f8_pack2(v[b][2] * inv, v[b][3] * inv) << 16);
+        q.y = f8_pack2(v[b][4] * inv, v[b][5] * inv) | (f8_pack2(v[b][6] * inv, v[b][7] * inv) << 16);
+        const int nslot = p.pos ? p.k : 1;
+        for (int i = 0; i < nslot; ++i) {
+            const int64_t r = p.pos ? __ldg(p.pos + row * p.k + i) : row;
+            if (r < 0) continue;
+            uint8_t* dst = p.q + r * p.cols + c;
+            if constexpr (VEC) {
+                if (c < p.cols) *reinterpret_cast<uint2*>(dst) = q;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < p.cols)
+                        dst[e] = static_cast<uint8_t>((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+            }
+            if (sub == 0) p.s[r * p.nblk + blk0 + b] = s;
         }
-        if (sub == 0) p.s[r * p.nblk + blk] = s;
     }
 }
 
 // ------------------------------------------------------------------- group
-// Stable counting sort of the P = T k pairs by expert, in one CTA: warp w
-// takes the w-th run of pairs, counts its experts, the counts are summed
-// over (expert, warp), and a second pass over the run gives every pair its
-// row.  Pairs whose expert lies outside [0, E) get row -1.
+// Stable counting sort of the P = T k pairs by expert, in one cluster of up
+// to eight CTAs.  Every warp takes one run of pairs and counts its experts;
+// the counts are summed over (expert, CTA, warp), the CTAs' totals read from
+// each other's shared memory, and a second pass over the run gives every pair
+// its row.  Pairs whose expert lies outside [0, E) get row -1.  Bound by
+// latency: G_AHEAD loads of a run are in flight at a time (one CTA with one
+// load in flight took 59 us for 32,768 pairs).
 //   offsets[E+1]  first row of each expert, total last
 //   pos[P]        row of each pair, or -1
 constexpr int G_THREADS = 1024;
 constexpr int G_WARPS = G_THREADS / 32;
+constexpr int G_AHEAD = 4;
+constexpr int G_CLUSTER = 8;
 
 __global__ void __launch_bounds__(G_THREADS) group_kernel(const int32_t* __restrict__ idx, int P,
                                                           int E, int32_t* __restrict__ offsets,
                                                           int32_t* __restrict__ pos) {
-    extern __shared__ int hist[];  // [G_WARPS][E]
+    extern __shared__ int hist[];  // [G_WARPS][E], then this CTA's totals [E]
     __shared__ int wsum[G_WARPS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+    int* totals = hist + G_WARPS * E;
     for (int i = tid; i < G_WARPS * E; i += G_THREADS) hist[i] = 0;
     pdl_wait();
     pdl_trigger();
     __syncthreads();
-    const int run = ((P + G_WARPS - 1) / G_WARPS + 31) & ~31;
-    const int beg = min(warp * run, P), end = min(beg + run, P);
+    const int run = ((P + G_WARPS * ranks - 1) / (G_WARPS * ranks) + 31) & ~31;
+    const int beg = min((rank * G_WARPS + warp) * run, P), end = min(beg + run, P);
     int* h = hist + warp * E;
-    for (int i = beg; i < end; i += 32) {
-        const int e = i + lane < end ? __ldcg(idx + i + lane) : -1;
-        const bool in = e >= 0 && e < E;
-        const unsigned same = __match_any_sync(0xffffffffu, in ? e : -1);
-        if (in && lane == __ffs(same) - 1) h[e] += __popc(same);
-        __syncwarp();
+    auto load = [&](int i, int (&e)[G_AHEAD]) {
+#pragma unroll
+        for (int a = 0; a < G_AHEAD; ++a) {
+            const int j = i + 32 * a + lane;
+            const int v = j < end ? __ldg(idx + j) : -1;
+            e[a] = v >= 0 && v < E ? v : -1;
+        }
+    };
+    for (int i = beg; i < end; i += 32 * G_AHEAD) {
+        int e[G_AHEAD];
+        load(i, e);
+#pragma unroll
+        for (int a = 0; a < G_AHEAD; ++a) {
+            if (i + 32 * a >= end) break;
+            const unsigned same = __match_any_sync(0xffffffffu, e[a]);
+            if (e[a] >= 0 && lane == __ffs(same) - 1) h[e[a]] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
-    // exclusive sums: over the warps of an expert, then over the experts
-    int total = 0;
-    if (tid < E)
+    // exclusive sums: over the warps of an expert, the CTAs, then the experts
+    int mine = 0;
+    if (tid < E) {
         for (int w = 0; w < G_WARPS; ++w) {
             const int c = hist[w * E + tid];
-            hist[w * E + tid] = total;
+            hist[w * E + tid] = mine;
+            mine += c;
+        }
+        totals[tid] = mine;
+    }
+    cluster_sync();
+    int total = 0, before = 0;
+    if (tid < E)
+        for (int r = 0; r < ranks; ++r) {
+            const int c = cluster_ld_s32(totals + tid, static_cast<uint32_t>(r));
+            if (r < rank) before += c;
             total += c;
         }
     int incl = total;
@@ -148,63 +200,93 @@ __global__ void __launch_bounds__(G_THREADS) group_kernel(const int32_t* __restr
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    const int first = before + incl - total;
+    int first = incl - total;
+    for (int w = 0; w < warp; ++w) first += wsum[w];
     if (tid < E) {
-        offsets[tid] = first;
-        if (tid == E - 1) offsets[E] = first + total;
-        for (int w = 0; w < G_WARPS; ++w) hist[w * E + tid] += first;
+        if (rank == 0) {
+            offsets[tid] = first;
+            if (tid == E - 1) offsets[E] = first + total;
+        }
+        for (int w = 0; w < G_WARPS; ++w) hist[w * E + tid] += first + before;
     }
     __syncthreads();
-    for (int i = beg; i < end; i += 32) {
-        const int e = i + lane < end ? __ldcg(idx + i + lane) : -1;
-        const bool in = e >= 0 && e < E;
-        const unsigned same = __match_any_sync(0xffffffffu, in ? e : -1);
-        int row = -1;
-        if (in) row = h[e] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (in && lane == __ffs(same) - 1) h[e] += __popc(same);
-        __syncwarp();
-        if (i + lane < end) pos[i + lane] = row;
+    for (int i = beg; i < end; i += 32 * G_AHEAD) {
+        int e[G_AHEAD];
+        load(i, e);
+#pragma unroll
+        for (int a = 0; a < G_AHEAD; ++a) {
+            if (i + 32 * a >= end) break;
+            const unsigned same = __match_any_sync(0xffffffffu, e[a]);
+            int row = -1;
+            if (e[a] >= 0) row = h[e[a]] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (e[a] >= 0 && lane == __ffs(same) - 1) h[e[a]] += __popc(same);
+            __syncwarp();
+            if (i + 32 * a + lane < end) pos[i + 32 * a + lane] = row;
+        }
     }
+    cluster_sync();  // no CTA leaves while another may read its totals
 }
 
 // ----------------------------------------------------------------- combine
 // out[t] = residual[t] + sum_s w[t][s] y[pos[t][s]], summed in f32 in slot
-// order and rounded once.  A thread takes four columns of one token.  Bound
-// by reading y: 4 k bytes per output element.
+// order and rounded once.  A thread takes eight columns of one token and loads
+// four slots' values before it adds them.  Bound by reading y: for bf16
+// activations y is bf16 (the layer rounds each expert's output once: 2^-9 of
+// it, below out's own rounding; y is the layer's largest traffic), else f32.
 constexpr int C_THREADS = 128;
+constexpr int C_AHEAD = 4;
 
 template <class T>
+__device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint4 q;
+        uint32_t* u = reinterpret_cast<uint32_t*>(&q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u[i] = std::is_same<T, __half>::value ? gmm::pack_f16(v[2 * i], v[2 * i + 1])
+                                                  : gmm::pack_bf16(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<uint4*>(dst) = q;
+    }
+}
+
+template <class T, class Y>
 __global__ void __launch_bounds__(C_THREADS) combine_kernel(
-    const float* __restrict__ y, const int32_t* __restrict__ pos, const float* __restrict__ w,
+    const Y* __restrict__ y, const int32_t* __restrict__ pos, const float* __restrict__ w,
     const T* residual, T* out, int H, int k) {
     const int64_t t = blockIdx.x;
+    const int c = (blockIdx.y * C_THREADS + threadIdx.x) * 8;
     pdl_wait();
     pdl_trigger();
-    for (int c = (blockIdx.y * C_THREADS + threadIdx.x) * 4; c < H;
-         c += gridDim.y * C_THREADS * 4) {
-        float a[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < k; ++s) {
-            const int r = __ldcg(pos + t * k + s);
-            if (r < 0) continue;
-            const float ws = __ldcg(w + t * k + s);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(r) * H + c));
-            a[0] = fmaf(ws, v.x, a[0]);
-            a[1] = fmaf(ws, v.y, a[1]);
-            a[2] = fmaf(ws, v.z, a[2]);
-            a[3] = fmaf(ws, v.w, a[3]);
-        }
-        const int64_t o = t * H + c;
+    if (c >= H) return;
+    float a[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float v = (residual ? to_f32(residual[o + i]) : 0.f) + a[i];
-            if constexpr (sizeof(T) == 4) out[o + i] = v;
-            else if constexpr (std::is_same<T, __half>::value) out[o + i] = __float2half_rn(v);
-            else out[o + i] = __float2bfloat16_rn(v);
+    for (int i = 0; i < 8; ++i) a[i] = 0.f;
+    for (int s0 = 0; s0 < k; s0 += C_AHEAD) {
+        float v[C_AHEAD][8], ws[C_AHEAD];
+#pragma unroll
+        for (int s = 0; s < C_AHEAD; ++s) {
+            const int r = s0 + s < k ? __ldg(pos + t * k + s0 + s) : -1;
+            ws[s] = r >= 0 ? __ldg(w + t * k + s0 + s) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
+            if (r >= 0) load8(y + static_cast<int64_t>(r) * H + c, v[s]);
         }
+#pragma unroll
+        for (int s = 0; s < C_AHEAD; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = fmaf(ws[s], v[s][i], a[i]);
     }
+    if (residual) {
+        float r[8];
+        load8(residual + t * H + c, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] += r[i];
+    }
+    store8(out + t * H + c, a);
 }
 
 }  // namespace f8

@@ -243,6 +243,14 @@ __device__ __forceinline__ float cluster_ld_f32(const float* p, uint32_t rank) {
     return v;
 }
 
+__device__ __forceinline__ int cluster_ld_s32(const int* p, uint32_t rank) {
+    uint32_t a;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
 // The address in shared::cluster space that `p` has in CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     uint32_t a;

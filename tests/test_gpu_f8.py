@@ -308,12 +308,13 @@ def silu(v):
     return v / (1.0 + np.exp(-v))
 
 
-def moe_reference(x, idx, w, stacks, residual):
+def moe_reference(x, idx, w, stacks, residual, kind="f32"):
     """(out, error bound before rounding).  The bound carries the products'
     errors through SwiGLU (|silu'| <= 1.1; the two fast f32 functions are within
     2^-20), lets an activation within its error of a rounding border take
     either code, and adds the down product's, the weighted sum's (k terms) and
-    the residual addition's roundings."""
+    the residual addition's roundings.  In bf16 each expert's output is rounded
+    to bf16 before the sum: 2^-8 of it (and of its error), half a step."""
     (G, U, D) = stacks
     T, k = idx.shape
     H, F, E = G.shape[2], G.shape[1], G.shape[0]
@@ -348,6 +349,8 @@ def moe_reference(x, idx, w, stacks, residual):
                     slack[:, c] += 2.0 ** -9 * 2 * a_s[:, b:b + 1]
             y, ey = ref.product(av, D[e], ref.f8_terms(F))
             ey = ey + slack @ np.abs(D[e]).T
+            if kind == "bf16":
+                ey = ref.rounded(y, ey, "bf16")
             out[t] += float(w[t, s]) * y[0]
             err[t] += abs(float(w[t, s])) * ey[0]
             mag[t] += np.abs(float(w[t, s]) * y[0])
@@ -396,7 +399,7 @@ def test_moe_experts(qm, dims, kind):
     out = run_moe(qm, dims, kind, x.cuda(), dev(idx), dev(w), dev_stacks(stacks), residual.cuda())
     assert qm.device_status() == qm.OK
     want, err = moe_reference(x.double().numpy(), idx, w, [s[2] for s in stacks],
-                              residual.double().numpy())
+                              residual.double().numpy(), kind)
     check(f64(out), want, ref.rounded(want, err, kind), "moe")
 
 
@@ -412,7 +415,7 @@ def test_moe_padding_duplicates_and_aliases(qm):
     idx[8] = -1
     st, X, I, W = dev_stacks(stacks), x.cuda(), dev(idx), dev(w)
     values = [s[2] for s in stacks]
-    want, err = moe_reference(x.double().numpy(), idx, w, values, residual.double().numpy())
+    want, err = moe_reference(x.double().numpy(), idx, w, values, residual.double().numpy(), "bf16")
     R = residual.cuda()
     out = run_moe(qm, dims, "bf16", X, I, W, st, R)
     check(f64(out), want, ref.rounded(want, err, "bf16"), "padded")
@@ -420,7 +423,7 @@ def test_moe_padding_duplicates_and_aliases(qm):
     run_moe(qm, dims, "bf16", X, I, W, st, R, out=R)
     assert (R == out).all()
     bare = run_moe(qm, dims, "bf16", X, I, W, st, None)
-    want0, err0 = moe_reference(x.double().numpy(), idx, w, values, None)
+    want0, err0 = moe_reference(x.double().numpy(), idx, w, values, None, "bf16")
     check(f64(bare), want0, ref.rounded(want0, err0, "bf16"), "no residual")
     assert (bare[0] == 0).all()
     assert qm.device_status() == qm.OK
@@ -531,7 +534,7 @@ def test_chain_matches_reference(qm):
     check(f64(h), want, ref.rounded(want, err, "bf16"), "dense")
     out = run_moe(qm, dims, "bf16", h, dev(idx), dev(w), dev_stacks(stacks), h)
     hv = f64(h)
-    want, err = moe_reference(hv, idx, w, [c[2] for c in stacks], hv)
+    want, err = moe_reference(hv, idx, w, [c[2] for c in stacks], hv, "bf16")
     check(f64(out), want, ref.rounded(want, err, "bf16"), "experts")
     assert qm.device_status() == qm.OK
 
