@@ -141,7 +141,7 @@ static qmoe_status run_gmm_kind(Gmm& g, const DevInfo& d, cudaStream_t st) {
                                                                   static_cast<int>(tiles), d, st);
     }
     g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
-    return launch_pairs<gmm::PairCfg<F8, F8 ? 128 : 256, F8 ? 7 : 5, false>>(g, d, st);
+    return launch_pairs<gmm::PairCfg<F8, F8 ? 192 : 256, F8 ? 6 : 5, false>>(g, d, st);
 }
 
 static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
@@ -158,7 +158,7 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
     if (g.type == QMOE_E4M3) {
         if (g.W2) {
             g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
-            return launch_pairs<gmm::PairCfg<true, 64, 5, true>>(g, d, st);
+            return launch_pairs<gmm::PairCfg<true, 96, 5, true>>(g, d, st);
         }
         return run_gmm_kind<true>(g, d, st);
     }

@@ -1,6 +1,7 @@
 // gmm_pair.cuh — the grouped products' kernel for many rows: a pair of CTAs
-// (a cluster of two) computes 256 weight rows by up to 256 token rows (16-bit)
-// or 128 (e4m3) with tcgen05.mma cta_group::2.
+// (a cluster of two) computes 256 weight rows by up to 256 token rows (16-bit) or
+// 192 (e4m3) with tcgen05.mma cta_group::2; SwiGLU form: 256 rows of gate and of
+// up by 96.
 //
 // Why pairs: each CTA loads its own 128 weight rows and half of the token
 // rows.  A stage of 128 bytes of K is then 32 KB per CTA for
@@ -15,57 +16,56 @@
 // 256-column k-block of 512 clocks).  Measured over 12 warps: 32x32b 439,
 // 16x128b 431, 16x256b 255 bytes per clock.
 //
-// What bounds the e4m3 form is not a rate but the round trip of an
-// accumulator buffer, once per k-block: issue, MMA, commit, the sixteen warps
-// of two CTAs reading it, their arrivals at the issuing CTA - about 2,300
-// clocks with two buffers of 192 columns, whatever the instruction count.  So
-// the buffers are four of 128 columns, a warp reads one fragment of each, and
-// hands the buffer back before it adds the values.
+// What bounds the e4m3 form is shared memory: per k-block the MMAs read both
+// operands, the copies write them and the epilogue reads scales, 92 KB for 192
+// columns (720 clocks at 128 bytes per clock, against 384 of MMA).  Narrower
+// tiles read the weight rows more often: four buffers of 128 columns took 760
+// clocks per 128.  256 columns do not leave the epilogue's threads the
+// registers: 64 sums, a fragment of 32 values and its scales without spilling
+// take 512 threads (any spill in these loops cost 15 to 30 percent).
 //
-// Roles (640 threads): warps 0 and 2 load, warp 1 (of the first CTA)
-// issues the MMAs, warp 3 stages scale products, warps 4-19 are the epilogue: warp w reads
-// lanes 32 (w % 4) .. + 31 and every fourth run of 32 columns (SwiGLU form:
-// run w / 4 % 2 of gate, w < 12, or of up).
+// Roles (512 threads): warps 0 and 2 load, warp 1 (of the first CTA)
+// issues the MMAs, warp 3 stages scale products, warps 4-15 are the epilogue: warp w reads
+// lanes 32 (w % 4) .. + 31 and two runs of 32 columns, 96 apart (SwiGLU form:
+// the same run of gate and of up).
 #pragma once
 #include "gmm.cuh"
 
 namespace qmoe {
 namespace gmm {
 
-constexpr int P_CG = 4;            // runs of columns in flight, one per four warps
+constexpr int P_CG = 3;            // runs of columns in flight, one per four warps
 constexpr int P_EPI = 4 * P_CG;    // epilogue warps
 constexpr int P_THREADS = 128 + 32 * P_EPI;
 constexpr int P_CH = 32;           // columns per run
-// registers per thread: 128 x 64 + 512 x 104 = 61,440, the launch's 640 x 96
-constexpr int P_REGS_LOAD = 64, P_REGS_EPI = 104;
+// registers per thread: 128 x 80 + 384 x 144 = 65,536, the launch's 512 x 128
+constexpr int P_REGS_LOAD = 80, P_REGS_EPI = 144;
 
 template <bool F8_, int NT_, int NST_, bool GU_>
 struct PairCfg {
     static constexpr bool F8 = F8_, GU = GU_;
     static constexpr int NT = NT_, NST = NST_;
     static constexpr int NA = GU ? 2 : 1;
-    static constexpr int BOX = 32;  // token rows per TMA box; divides NT / 2
+    static constexpr int BOX = GU ? 16 : 32;  // token rows per TMA box; divides NT / 2
     static constexpr int A_BYTES = TILE_W * KBLK;
     static constexpr int STAGE = NA * A_BYTES + NT / 2 * KBLK;
     static constexpr int TM_BUF = NA * NT;
     static constexpr int TM_COLS = 512;
-    static constexpr int NBUF = TM_COLS / TM_BUF;      // accumulator buffers
-    static constexpr int RUNS = TM_BUF / P_CH / P_CG;  // runs per epilogue warp and buffer
-    static constexpr int SC_STAGE = SC_BLK * NA * NT;  // floats: sx sw of every column
-    // staging per epilogue warp: 32 tokens of 32 16-bit values; SwiGLU form:
-    // per pair of warps, up's 32 x 32 f32 values on their way to gate's warp
-    static constexpr int OUT_BYTES = 2048;
+    static constexpr int NBUF = 2;  // accumulator buffers
+        static constexpr int SC_STAGE = SC_BLK * NA * NT;  // floats: sx sw of every column
+    // staging per epilogue warp: 32 tokens of 32 values
+    static constexpr int OUT_BYTES = GU ? 1024 : 2048;
     static constexpr int O_SC = NST * STAGE;
     static constexpr int O_OUT = O_SC + (F8 ? SC_RING * SC_STAGE * 4 : 0);
     static constexpr int O_AMAX = O_OUT + P_EPI * OUT_BYTES;
     static constexpr int O_BAR = O_AMAX + (GU ? 2 * 4 * NT * 4 : 0);
-    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1 + (GU ? P_EPI : 0);
+    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1;
     static constexpr int O_TAB = O_BAR + (N_BAR + 1) * 8;
     static constexpr int smem(int E) { return 1024 + O_TAB + (3 * E + 4) * 4; }
-    static_assert(TM_BUF * NBUF == TM_COLS && STAGE % 1024 == 0, "tile shape");
+    static_assert(TM_BUF * NBUF <= TM_COLS && STAGE % 1024 == 0, "tile shape");
     static_assert((NT / 2) % BOX == 0, "boxes fill a stage exactly");
-    static_assert(RUNS == (F8 ? 1 : 2), "e4m3: one run per warp; 16-bit: two");
-    static_assert(!F8 || NBUF == SC_BLK, "a tile's k-block b uses buffer b % 4");
+    static_assert(!F8 || TM_BUF == 2 * P_CG * P_CH, "two runs per warp");
+    static_assert(!F8 || NT % 96 == 0, "scales are staged 96 columns at a time");
 };
 
 // Where token j's scale lies in a row of the ring: a thread's eight columns of
@@ -132,14 +132,22 @@ __device__ __forceinline__ void store_run(const Params& p, uint8_t* stage, const
                     static_cast<uint16_t*>(p.y) + row * p.ldy + n0, p.ldy, nv);
         return;
     }
+    // otherwise as f32 through shared memory, a row half at a time: runs of 16
+    // values of y's rows
+    float* f = reinterpret_cast<float*>(stage);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            const int c = 4 * (x >> 1) + (lane & 3);
-            const int n = n0 + 16 * h + 8 * (x & 1) + (lane >> 2);
-            if (c < nv && n < p.N) store_out(p.y, (row + c) * p.ldy + n, p.out, v[h][x]);
-        }
+        for (int x = 0; x < 16; ++x)
+            f[(4 * (x >> 1) + (lane & 3)) * 16 + 8 * (x & 1) + (lane >> 2)] = v[h][x];
+        __syncwarp();
+        const int n = n0 + 16 * h + (lane & 15);
+        int64_t o = (row + (lane >> 4)) * p.ldy + n;
+#pragma unroll 2
+        for (int i = lane >> 4; i < nv && i < 32; i += 2, o += 2 * p.ldy)
+            if (n < p.N) store_out(p.y, o, p.out, f[i * 16 + (lane & 15)]);
+        __syncwarp();
+    }
 }
 
 template <class C>
@@ -160,8 +168,6 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* acc_full = sc_empty + SC_RING;  // [NBUF] each CTA's
     uint64_t* acc_empty = acc_full + C::NBUF; // [NBUF] first CTA's: both epilogues have read it
     uint64_t* mma_done = acc_empty + C::NBUF;
-    uint64_t* up_full = mma_done + 1;         // [8] SwiGLU form: up's values of a run are staged
-    uint64_t* up_empty = up_full + P_EPI / 2; // [8] and have been read
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BAR);
     int* t_lo = reinterpret_cast<int*>(base + C::O_TAB);
     int* t_hi = t_lo + p.E;
@@ -184,11 +190,6 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 2 * P_EPI);
         }
-        if constexpr (C::GU)
-            for (int i = 0; i < P_EPI / 2; ++i) {
-                mbar_init(&up_full[i], 32);
-                mbar_init(&up_empty[i], 32);
-            }
         mbar_init(mma_done, 1);
         fence_barrier_init();
     }
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int k = 0; k < C::NBUF; ++k) {
                         if (k0 + k >= p.kb) break;
-                        if constexpr (C::F8) ab = k;
+                        if constexpr (C::F8) ab ^= 1;
                         const bool fresh = C::F8 || k0 + k == 0;
                         const bool last = C::F8 || k0 + k == p.kb - 1;
                         // both waits tried before either is acted on
@@ -323,9 +324,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_wait_spin(mma_done, 0, p.err, DEV_GMM_TIMEOUT);
         } else if (C::F8 && warp == 3) {
             // ----------------------------------------------------- scales
-            // ring[kb][column] = sx[column][kb] sw[kb] (0 past the tile's rows); the
-            // next four k-blocks' scales are in flight while these are stored
-            constexpr int RPT = C::NT / 32;
+            // ring[kb][column] = sx[column][kb] sw[kb] (0 past the tile's rows),
+            // four k-blocks at a time, 96 columns in flight
             const bool vec = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.xs) & 15) == 0;
             int s = 0;
             uint32_t ph = 1;
@@ -336,44 +336,42 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                 const bool rows_in = nbi < p.nb;  // the last weight tile's second half may be empty
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + nbi) * p.kb;
                 const float* xs = p.xs + (static_cast<int64_t>(w.row0) + lane) * p.kb;
-                float v[RPT][SC_BLK], g[C::NA][SC_BLK];
-                auto fetch = [&](int k0) {
-#pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const float* src = xs + static_cast<int64_t>(32 * i) * p.kb + k0;
-                        const bool in = lane + 32 * i < w.nv;
-                        if (vec && in) {
-                            const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
-                            v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < SC_BLK; ++b)
-                                v[i][b] = in && k0 + b < p.kb ? __ldcg(src + b) : 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int b = 0; b < SC_BLK; ++b) {
-                        const bool in = rows_in && k0 + b < p.kb;
-                        g[0][b] = in ? __ldg(p.ws + wo + k0 + b) : 0.f;
-                        if constexpr (C::GU) g[1][b] = in ? __ldg(p.ws2 + wo + k0 + b) : 0.f;
-                    }
-                };
-                fetch(0);
                 for (int k0 = 0; k0 < p.kb; k0 += SC_BLK) {
                     if (!mbar_wait_spin(&sc_empty[s], ph, p.err, DEV_GMM_TIMEOUT)) {
                         ok = false;
                         break;
                     }
                     float* dst = ring + s * C::SC_STAGE;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < w.np; j0 += 96) {
+                        float v[3][SC_BLK];
 #pragma unroll
-                    for (int i = 0; i < RPT; ++i)
+                        for (int i = 0; i < 3; ++i) {
+                            const int j = j0 + 32 * i;
+                            const float* src = xs + static_cast<int64_t>(j) * p.kb + k0;
+                            const bool in = lane + j < w.nv;
+                            if (vec && in) {
+                                const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
+                                v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
+                            } else {
+#pragma unroll
+                                for (int b = 0; b < SC_BLK; ++b)
+                                    v[i][b] = in && k0 + b < p.kb ? __ldcg(src + b) : 0.f;
+                            }
+                        }
 #pragma unroll
                         for (int b = 0; b < SC_BLK; ++b)
 #pragma unroll
-                            for (int a = 0; a < C::NA; ++a)
-                                dst[(b * C::NA + a) * C::NT + sc_slot(lane + 32 * i)] =
-                                    v[i][b] * g[a][b];
-                    if (k0 + SC_BLK < p.kb) fetch(k0 + SC_BLK);
+                            for (int a = 0; a < C::NA; ++a) {
+                                const float g = rows_in && k0 + b < p.kb
+                                                    ? __ldg((a ? p.ws2 : p.ws) + wo + k0 + b)
+                                                    : 0.f;
+#pragma unroll
+                                for (int i = 0; i < 3; ++i)
+                                    dst[(b * C::NA + a) * C::NT + sc_slot(lane + j0 + 32 * i)] =
+                                        v[i][b] * g;
+                            }
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_full[s]);
                     if (++s == SC_RING) {
@@ -390,9 +388,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         const int lr = lane >> 2, lc = lane & 3;  // fragment row and column
         const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
         // this warp's first run: its column among the tokens, its buffer column
-        const int run_col = (C::GU ? cg & 1 : cg) * P_CH;
-        const uint32_t tm_run = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
-                                (C::GU ? (cg >> 1) * C::NT + run_col : run_col);
+        const int run_col = cg * P_CH;
+        const uint32_t tm_run = tmem + (static_cast<uint32_t>(quad * 32) << 16) + run_col;
+        // column distance of the two runs, in the buffer and in the ring
+        constexpr int R2 = P_CG * P_CH;
         uint8_t* stage = base + C::O_OUT + (warp - 4) * C::OUT_BYTES;
         uint32_t ab = C::NBUF - 1, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
@@ -405,69 +404,74 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                 if (!ok) break;
                 aph ^= 1u << ab;
                 umma::fence_after_sync();
+                if (run_col >= w.np && lane == 0) mbar_arrive_cluster(acc_empty0 + ab * 8);
 #pragma unroll 1
-                for (int i = 0; i < C::RUNS; ++i) {
-                    const int col = run_col + i * (P_CG * P_CH);
+                for (int col = run_col; col < w.np; col += R2) {
                     Frag f;
-                    float v[2][16];
-                    if (col < w.np) {
-                        frag_load(tm_run + ab * C::TM_BUF + i * (P_CG * P_CH), f);
-                        frag_wait(f);
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            v[0][c] = __uint_as_float(f.lo[c]);
-                            v[1][c] = __uint_as_float(f.hi[c]);
-                        }
-                    }
-                    if (i == C::RUNS - 1) {
+                    frag_load(tm_run + ab * C::TM_BUF + col - run_col, f);
+                    frag_wait(f);
+                    if (col + R2 >= w.np) {
                         umma::fence_before_sync();
-                        __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc_empty0 + ab * 8);
                     }
-                    if (col < w.np)
-                        store_run(p, stage, v, lane, w.row0 + col, w.nv - col, n0);
+                    float v[2][16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        v[0][c] = __uint_as_float(f.lo[c]);
+                        v[1][c] = __uint_as_float(f.hi[c]);
+                    }
+                    store_run(p, stage, v, lane, w.row0 + col, w.nv - col, n0);
                 }
             } else {
-                // acc[row half][2 i + j]: weight row 16 half + 8 j + lr of this warp's 32,
-                // column 4 i + lc of its run
-                float acc[2][16];
+                // acc[run][row half][2 i + j]: weight row 16 half + 8 j + lr of this warp's
+                // 32, column 4 i + lc of the run
+                float acc[2][2][16];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) acc[0][c] = acc[1][c] = 0.f;
-                const bool live = run_col < tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E).np;
-                const float* run = ring + (C::GU ? (cg >> 1) * C::NT : 0) + run_col + lc * 8;
+                for (int c = 0; c < 64; ++c) acc[c >> 5][(c >> 4) & 1][c & 15] = 0.f;
+                const int np = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E).np;
+                const int runs = C::GU ? (run_col < np ? 2 : 0)
+                                       : (run_col < np) + (run_col + R2 < np);
+                const float* run = ring + run_col + lc * 8;
 #pragma unroll 1
                 for (int k0 = 0; k0 < p.kb; k0 += SC_BLK) {
                     ok = mbar_wait_spin(&sc_full[cs], cph, p.err, DEV_GMM_TIMEOUT);
                     if (!ok) break;
                     const float* row = run + cs * C::SC_STAGE;
                     const int nk = min(SC_BLK, p.kb - k0);
-#pragma unroll
-                    for (int k = 0; k < SC_BLK; ++k) {
-                        if (k >= nk) break;
-                        ok = mbar_wait_spin(&acc_full[k], (aph >> k) & 1, p.err, DEV_GMM_TIMEOUT);
+#pragma unroll 1
+                    for (int k = 0; k < nk; ++k, row += C::NA * C::NT) {
+                        ab ^= 1;
+                        ok = mbar_wait_spin(&acc_full[ab], (aph >> ab) & 1, p.err,
+                                            DEV_GMM_TIMEOUT);
                         if (!ok) break;
-                        if (live) {
-                            umma::fence_after_sync();
-                            Frag f;
-                            frag_load(tm_run + k * C::TM_BUF, f);
-                            const float4* sx =
-                                reinterpret_cast<const float4*>(row + k * C::NA * C::NT);
-                            const float4 s0 = sx[0], s1 = sx[1];
-                            const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                            frag_wait(f);
-                            umma::fence_before_sync();
-                            if (lane == 0) mbar_arrive_cluster(acc_empty0 + k * 8);
+                        aph ^= 1u << ab;
+                        umma::fence_after_sync();
+                        const uint32_t src = tm_run + ab * C::TM_BUF;
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) {
-                                acc[0][c] = fmaf(__uint_as_float(f.lo[c]), s[c / 2], acc[0][c]);
-                                acc[1][c] = fmaf(__uint_as_float(f.hi[c]), s[c / 2], acc[1][c]);
+                        for (int q = 0; q < 2; ++q)
+                            if (q < runs) {
+                                Frag f;
+                                frag_load(src + q * R2, f);
+                                const float4* sx = reinterpret_cast<const float4*>(row + q * R2);
+                                const float4 s0 = sx[0], s1 = sx[1];
+                                const float s[8] = {s0.x, s0.y, s0.z, s0.w,
+                                                    s1.x, s1.y, s1.z, s1.w};
+                                frag_wait(f);
+                                if (q == runs - 1) {
+                                    umma::fence_before_sync();
+                                    if (lane == 0) mbar_arrive_cluster(acc_empty0 + ab * 8);
+                                }
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    acc[q][0][c] =
+                                        fmaf(__uint_as_float(f.lo[c]), s[c / 2], acc[q][0][c]);
+                                    acc[q][1][c] =
+                                        fmaf(__uint_as_float(f.hi[c]), s[c / 2], acc[q][1][c]);
+                                }
                             }
-                        } else if (lane == 0) {
-                            mbar_arrive_cluster(acc_empty0 + k * 8);
-                        }
+                        if (runs == 0 && lane == 0) mbar_arrive_cluster(acc_empty0 + ab * 8);
                     }
                     if (!ok) break;
-                    aph ^= (1u << nk) - 1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_empty[cs]);
                     if (++cs == SC_RING) {
@@ -484,40 +488,24 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                 const int nbi = 2 * w.nbi + static_cast<int>(rank);
                 const int n0 = nbi * TILE_W + quad * 32;  // first of this warp's weight rows
                 if constexpr (!C::GU) {
-                    store_run(p, stage, acc, lane, w.row0 + run_col, w.nv - run_col, n0);
-                } else {
-                    // up's warps hand their values to gate's warp of the same rows and
-                    // run, thread by thread
-                    const int pair = (cg & 1) * 4 + quad;
-                    float* x = reinterpret_cast<float*>(base + C::O_OUT + pair * 4096);
-                    if (cg >= 2) {
-                        ok = mbar_wait_spin(&up_empty[pair], par ^ 1, p.err, DEV_GMM_TIMEOUT);
-                        if (!ok) break;
-                        if (live) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) {
-                                x[c * 32 + lane] = acc[0][c];
-                                x[(16 + c) * 32 + lane] = acc[1][c];
-                            }
-                        }
-                        mbar_arrive(&up_full[pair]);
-                        continue;
-                    }
-                    ok = mbar_wait_spin(&up_full[pair], par, p.err, DEV_GMM_TIMEOUT);
-                    if (!ok) break;
+                    for (int q = 0; q < 2; ++q)
+                        store_run(p, stage, acc[q], lane, w.row0 + run_col + q * R2,
+                                  w.nv - run_col - q * R2, n0);
+                } else {
                     // a = silu(g) u; this CTA's 128 rows are one scale block of the
                     // activations: maxima over a thread's rows, the lanes, the four warps
                     uint32_t* am = amax + par * 4 * C::NT;
-                    if (live) {
+                    if (runs > 0) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             uint32_t m = 0;
 #pragma unroll
                             for (int r = 0; r < 4; ++r) {
-                                const float g = acc[r >> 1][2 * i + (r & 1)];
-                                const float u = x[((r >> 1) * 16 + 2 * i + (r & 1)) * 32 + lane];
+                                const float g = acc[0][r >> 1][2 * i + (r & 1)];
+                                const float u = acc[1][r >> 1][2 * i + (r & 1)];
                                 const float v = __fdividef(g, 1.0f + __expf(-g)) * u;
-                                acc[r >> 1][2 * i + (r & 1)] = v;
+                                acc[0][r >> 1][2 * i + (r & 1)] = v;
                                 m = max(m, finite_abs_bits(v));
                             }
 #pragma unroll
@@ -527,9 +515,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                         }
                     }
                     named_bar(1 + cg, 128);
-                    if (live) {
-                        uint32_t* codes = reinterpret_cast<uint32_t*>(x);
-                        __syncwarp();  // every lane has read its values of x
+                    if (runs > 0) {
+                        uint32_t* codes = reinterpret_cast<uint32_t*>(stage);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int j = run_col + 4 * i + lc;
@@ -541,8 +528,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                                 p.as[static_cast<int64_t>(w.row0 + j) * p.nb + nbi] = s;
                             // one word: rows lr, lr + 8, lr + 16, lr + 24 of token 4 i + lc
                             codes[(4 * i + lc) * 8 + lr] =
-                                f8_pack2(acc[0][2 * i] * inv, acc[0][2 * i + 1] * inv) |
-                                (f8_pack2(acc[1][2 * i] * inv, acc[1][2 * i + 1] * inv) << 16);
+                                f8_pack2(acc[0][0][2 * i] * inv, acc[0][0][2 * i + 1] * inv) |
+                                (f8_pack2(acc[0][1][2 * i] * inv, acc[0][1][2 * i + 1] * inv)
+                                 << 16);
                         }
                         __syncwarp();
                         // lane = token: its eight words' bytes in row order, 32 bytes of
@@ -571,7 +559,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                                                 __byte_perm(d01, d23, 0x7632));
                         }
                     }
-                    mbar_arrive(&up_empty[pair]);
+                    __syncwarp();  // the codes are read before the next tile's are written
                 }
             }
         }
