@@ -46,12 +46,12 @@ struct PairCfg {
     static constexpr bool F8 = F8_, GU = GU_;
     static constexpr int NT = NT_, NST = NST_;
     static constexpr int NA = GU ? 2 : 1;
-    static constexpr int BOX = GU ? 16 : 32;  // token rows per TMA box; divides NT / 2
+    static constexpr int BOX = NT % 64 ? 16 : 32;  // token rows per TMA box; divides NT / 2
     static constexpr int A_BYTES = TILE_W * KBLK;
     static constexpr int STAGE = NA * A_BYTES + NT / 2 * KBLK;
     static constexpr int TM_BUF = NA * NT;
     static constexpr int TM_COLS = 512;
-    static constexpr int NBUF = 2;  // accumulator buffers
+    static constexpr int NBUF = TM_COLS / TM_BUF;  // accumulator buffers
         static constexpr int SC_STAGE = SC_BLK * NA * NT;  // floats: sx sw of every column
     // staging per epilogue warp: 32 tokens of 32 values
     static constexpr int OUT_BYTES = GU ? 1024 : 2048;
@@ -64,8 +64,8 @@ struct PairCfg {
     static constexpr int smem(int E) { return 1024 + O_TAB + (3 * E + 4) * 4; }
     static_assert(TM_BUF * NBUF <= TM_COLS && STAGE % 1024 == 0, "tile shape");
     static_assert((NT / 2) % BOX == 0, "boxes fill a stage exactly");
-    static_assert(!F8 || TM_BUF == 2 * P_CG * P_CH, "two runs per warp");
-    static_assert(!F8 || NT % 96 == 0, "scales are staged 96 columns at a time");
+    static_assert(!F8 || TM_BUF <= 2 * P_CG * P_CH, "at most two runs per warp");
+    static_assert(NT % P_CH == 0, "whole runs");
 };
 
 // Where token j's scale lies in a row of the ring: a thread's eight columns of
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int k = 0; k < C::NBUF; ++k) {
                         if (k0 + k >= p.kb) break;
-                        if constexpr (C::F8) ab ^= 1;
+                        if constexpr (C::F8) ab = ab == C::NBUF - 1 ? 0 : ab + 1;
                         const bool fresh = C::F8 || k0 + k == 0;
                         const bool last = C::F8 || k0 + k == p.kb - 1;
                         // both waits tried before either is acted on
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         } else if (C::F8 && warp == 3) {
             // ----------------------------------------------------- scales
             // ring[kb][column] = sx[column][kb] sw[kb] (0 past the tile's rows),
-            // four k-blocks at a time, 96 columns in flight
+            // four k-blocks at a time
             const bool vec = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.xs) & 15) == 0;
             int s = 0;
             uint32_t ph = 1;
@@ -342,36 +342,32 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                         break;
                     }
                     float* dst = ring + s * C::SC_STAGE;
-#pragma unroll 1
-                    for (int j0 = 0; j0 < w.np; j0 += 96) {
-                        float v[3][SC_BLK];
+                    float v[C::NT / 32][SC_BLK];
 #pragma unroll
-                        for (int i = 0; i < 3; ++i) {
-                            const int j = j0 + 32 * i;
-                            const float* src = xs + static_cast<int64_t>(j) * p.kb + k0;
-                            const bool in = lane + j < w.nv;
-                            if (vec && in) {
-                                const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
-                                v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
-                            } else {
+                    for (int i = 0; i < C::NT / 32; ++i) {
+                        const float* src = xs + static_cast<int64_t>(32 * i) * p.kb + k0;
+                        const bool in = lane + 32 * i < w.nv;
+                        if (vec && in) {
+                            const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
+                            v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
+                        } else {
 #pragma unroll
-                                for (int b = 0; b < SC_BLK; ++b)
-                                    v[i][b] = in && k0 + b < p.kb ? __ldcg(src + b) : 0.f;
-                            }
+                            for (int b = 0; b < SC_BLK; ++b)
+                                v[i][b] = in && k0 + b < p.kb ? __ldcg(src + b) : 0.f;
                         }
-#pragma unroll
-                        for (int b = 0; b < SC_BLK; ++b)
-#pragma unroll
-                            for (int a = 0; a < C::NA; ++a) {
-                                const float g = rows_in && k0 + b < p.kb
-                                                    ? __ldg((a ? p.ws2 : p.ws) + wo + k0 + b)
-                                                    : 0.f;
-#pragma unroll
-                                for (int i = 0; i < 3; ++i)
-                                    dst[(b * C::NA + a) * C::NT + sc_slot(lane + j0 + 32 * i)] =
-                                        v[i][b] * g;
-                            }
                     }
+#pragma unroll
+                    for (int b = 0; b < SC_BLK; ++b)
+#pragma unroll
+                        for (int a = 0; a < C::NA; ++a) {
+                            const float g = rows_in && k0 + b < p.kb
+                                                ? __ldg((a ? p.ws2 : p.ws) + wo + k0 + b)
+                                                : 0.f;
+#pragma unroll
+                            for (int i = 0; i < C::NT / 32; ++i)
+                                dst[(b * C::NA + a) * C::NT + sc_slot(lane + 32 * i)] =
+                                    v[i][b] * g;
+                        }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_full[s]);
                     if (++s == SC_RING) {
@@ -391,7 +387,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         const int run_col = cg * P_CH;
         const uint32_t tm_run = tmem + (static_cast<uint32_t>(quad * 32) << 16) + run_col;
         // column distance of the two runs, in the buffer and in the ring
-        constexpr int R2 = P_CG * P_CH;
+        constexpr int R2 = C::GU ? C::NT : P_CG * P_CH;
         uint8_t* stage = base + C::O_OUT + (warp - 4) * C::OUT_BYTES;
         uint32_t ab = C::NBUF - 1, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                     const int nk = min(SC_BLK, p.kb - k0);
 #pragma unroll 1
                     for (int k = 0; k < nk; ++k, row += C::NA * C::NT) {
-                        ab ^= 1;
+                        ab = ab == C::NBUF - 1 ? 0 : ab + 1;
                         ok = mbar_wait_spin(&acc_full[ab], (aph >> ab) & 1, p.err,
                                             DEV_GMM_TIMEOUT);
                         if (!ok) break;
