@@ -71,10 +71,10 @@ struct Gmm {
     gmm::Params p;
 };
 
-// Launches kernel `kern` of configuration C; SPLIT: clusters of `ranks` CTAs
-// (the pair kernel has its cluster shape in its code).
+// Launches kernel `kern` of configuration C; `shaped`: as clusters of `ranks`
+// CTAs (the pair kernel has its cluster shape in its code).
 template <class C, class Kern>
-static qmoe_status launch_gmm(Kern kern, int threads, bool split, const Gmm& g, int ranks,
+static qmoe_status launch_gmm(Kern kern, int threads, bool shaped, const Gmm& g, int ranks,
                               int clusters, const DevInfo& d, cudaStream_t st) {
     const int smem = C::smem(g.p.E);
     constexpr int most = C::smem(C::GU ? MAX_F8_EXPERTS : MAX_GROUPS);
@@ -110,16 +110,33 @@ static qmoe_status launch_gmm(Kern kern, int threads, bool split, const Gmm& g, 
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split ? 2 : 1;
+    cfg.numAttrs = shaped ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, g.p, tw, tw2, tx);
     if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
     return QMOE_OK;
 }
 
+// The kernel for few rows per group.  Fewer tiles than SMs: clusters of as many
+// CTAs as the SMs have room for share a tile's K range; else one CTA per SM
+// takes tile after tile.
 template <class C>
-static qmoe_status launch_split(const Gmm& g, int ranks, int tiles, const DevInfo& d,
-                                cudaStream_t st) {
-    return launch_gmm<C>(gmm::gmm_kernel<C>, gmm::THREADS, true, g, ranks, tiles, d, st);
+static qmoe_status launch_few(const Gmm& g, const DevInfo& d, cudaStream_t st) {
+    const int64_t tiles = gmm::max_tiles(g.p.M, g.p.E, C::NT, g.p.nb);
+    int ranks = 1;
+    if (tiles < d.sms) {
+        // (a power of two: clusters of three left SMs of a GPC idle and took a
+        // second wave: 48 tiles on 144 CTAs 19 us, on 96 CTAs half of it)
+        while (ranks < gmm::MAX_RANKS && 2 * ranks * tiles <= d.sms && 2 * ranks <= g.p.kb)
+            ranks *= 2;
+    }
+    const int clusters = static_cast<int>(tiles < d.sms ? tiles : d.sms);
+    return launch_gmm<C>(gmm::gmm_kernel<C>, gmm::THREADS, true, g, ranks, clusters, d, st);
+}
+// Rows per group up to which that kernel is used: at 16 a tile of 32 columns
+// holds most groups.
+static bool few_rows(const gmm::Params& p) {
+    const int64_t groups = p.M < p.E ? p.M : p.E;
+    return p.M <= (p.offsets ? 16 * groups : 32);
 }
 // One CTA pair per two SMs, or as many as there can be tiles.
 template <class C>
@@ -131,15 +148,7 @@ static qmoe_status launch_pairs(const Gmm& g, const DevInfo& d, cudaStream_t st)
 
 template <bool F8>
 static qmoe_status run_gmm_kind(Gmm& g, const DevInfo& d, cudaStream_t st) {
-    const gmm::Params& p = g.p;
-    if (p.M <= 32LL * (p.offsets ? p.E : 1) && p.M <= 512) {
-        const int64_t tiles = gmm::max_tiles(p.M, p.E, 32, p.nb);
-        int ranks = 1;
-        while (ranks < 8 && tiles * ranks * 2 <= 2 * d.sms && p.kb >= ranks * 4) ranks *= 2;
-        if (tiles <= 65536)
-            return launch_split<gmm::Cfg<F8, 32, 6, false, true>>(g, ranks,
-                                                                  static_cast<int>(tiles), d, st);
-    }
+    if (few_rows(g.p)) return launch_few<gmm::Cfg<F8, 8, false>>(g, d, st);
     g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
     return launch_pairs<gmm::PairCfg<F8, F8 ? 192 : 256, F8 ? 6 : 5, false>>(g, d, st);
 }
@@ -157,6 +166,7 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
                 (static_cast<uint32_t>(gmm::TILE_W >> 4) << 24);
     if (g.type == QMOE_E4M3) {
         if (g.W2) {
+            if (few_rows(g.p)) return launch_few<gmm::Cfg<true, 5, true>>(g, d, st);
             g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
             return launch_pairs<gmm::PairCfg<true, 96, 5, true>>(g, d, st);
         }
@@ -166,22 +176,34 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
 }
 
 // --------------------------------------------------------------- quantise
-template <class T>
-static cudaError_t launch_quantize(f8::QuantParams q, cudaStream_t st) {
-    q.nrun = (q.nblk + f8::Q_RUN - 1) / f8::Q_RUN;
+template <class T, bool VEC, int RUN>
+static cudaError_t launch_quantize_run(f8::QuantParams q, cudaStream_t st) {
+    q.nrun = (q.nblk + RUN - 1) / RUN;
     const int64_t items = q.rows * q.nrun;
     const unsigned grid = static_cast<unsigned>((items + f8::Q_THREADS / 16 - 1) /
                                                 (f8::Q_THREADS / 16));
+    return launch_pdl(f8::quantize_kernel<T, VEC, RUN>, dim3(grid), dim3(f8::Q_THREADS), 0, st, q);
+}
+template <class T>
+static cudaError_t launch_quantize(const f8::QuantParams& q, int sms, cudaStream_t st) {
     const bool vec = q.cols % 8 == 0 && (q.ldx * sizeof(T)) % 16 == 0 && aligned(q.x, 16) &&
                      aligned(q.q, 8);
-    return vec ? launch_pdl(f8::quantize_kernel<T, true>, dim3(grid), dim3(f8::Q_THREADS), 0, st, q)
-               : launch_pdl(f8::quantize_kernel<T, false>, dim3(grid), dim3(f8::Q_THREADS), 0, st,
-                            q);
+    // runs of four blocks once they fill the GPU's threads
+    const bool many = q.rows * q.nblk >= static_cast<int64_t>(sms) * (2048 / 16) * 2;
+    return vec ? (many ? launch_quantize_run<T, true, 4>(q, st)
+                       : launch_quantize_run<T, true, 1>(q, st))
+               : launch_quantize_run<T, false, 1>(q, st);
 }
-static qmoe_status run_quantize(int type, const f8::QuantParams& q, cudaStream_t st) {
-    const cudaError_t e = type == QMOE_F32    ? launch_quantize<float>(q, st)
-                          : type == QMOE_BF16 ? launch_quantize<__nv_bfloat16>(q, st)
-                                              : launch_quantize<__half>(q, st);
+template <class T>
+static cudaError_t launch_group_quantize(const f8::QuantParams& q, const int32_t* idx, int P, int E,
+                                         int32_t* offsets, int32_t* pos, cudaStream_t st) {
+    return launch_pdl(f8::group_quantize_kernel<T>, dim3(static_cast<unsigned>(q.rows)),
+                      dim3(f8::Q_THREADS), 0, st, q, idx, P, E, offsets, pos);
+}
+static qmoe_status run_quantize(int type, const f8::QuantParams& q, int sms, cudaStream_t st) {
+    const cudaError_t e = type == QMOE_F32    ? launch_quantize<float>(q, sms, st)
+                          : type == QMOE_BF16 ? launch_quantize<__nv_bfloat16>(q, sms, st)
+                                              : launch_quantize<__half>(q, sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "quantize launch");
     return QMOE_OK;
 }
@@ -249,11 +271,11 @@ static cudaError_t launch_combine(const void* y, const int32_t* pos, const float
                       static_cast<const T*>(residual), static_cast<T*>(out), H, k);
 }
 
-// The group kernel: one CTA up to 4,096 pairs, else a cluster of them.
+// The group kernel: a CTA for every 512 pairs, up to a cluster of eight.
 static cudaError_t launch_group(const int32_t* idx, int P, int E, int32_t* offsets, int32_t* pos,
                                 cudaStream_t st) {
     int ranks = 1;
-    while (ranks < f8::G_CLUSTER && ranks * 4096 < P) ranks *= 2;
+    while (ranks < f8::G_CLUSTER && ranks * 512 < P) ranks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ranks));
     cfg.blockDim = dim3(f8::G_THREADS);
@@ -309,7 +331,7 @@ qmoe_status f8_quantize(int xtype, const void* x, int64_t rows, int64_t cols, in
                     (long long)rows, (long long)cols);
     DevInfo* d = nullptr;
     if (qmoe_status s = device_info(&d)) return s;
-    return run_quantize(xtype, p, static_cast<cudaStream_t>(stream));
+    return run_quantize(xtype, p, d->sms, static_cast<cudaStream_t>(stream));
 }
 
 // Checks shared by f8_mm and mm_grouped.
@@ -459,8 +481,6 @@ qmoe_status moe_experts_f8(const void* gate_stack, const float* gate_scale, cons
     const int T = s.n_tokens, k = s.top_k, H = s.hidden, F = s.expert_dim, E = s.num_experts;
     const int P = T * k;
 
-    cudaError_t e = launch_group(topk_idx, P, E, offsets, pos, st);
-    if (e != cudaSuccess) return cuda_fail(e, "group launch");
     f8::QuantParams q = {};
     q.x = x;
     q.ldx = H;
@@ -471,7 +491,18 @@ qmoe_status moe_experts_f8(const void* gate_stack, const float* gate_scale, cons
     q.rows = T;
     q.cols = H;
     q.nblk = H / F8_BLOCK;
-    if (qmoe_status r = run_quantize(xtype, q, st)) return r;
+    cudaError_t e;
+    if (P <= f8::GQ_PAIRS) {
+        e = xtype == QMOE_F32 ? launch_group_quantize<float>(q, topk_idx, P, E, offsets, pos, st)
+            : xtype == QMOE_BF16
+                ? launch_group_quantize<__nv_bfloat16>(q, topk_idx, P, E, offsets, pos, st)
+                : launch_group_quantize<__half>(q, topk_idx, P, E, offsets, pos, st);
+        if (e != cudaSuccess) return cuda_fail(e, "group and quantize launch");
+    } else {
+        e = launch_group(topk_idx, P, E, offsets, pos, st);
+        if (e != cudaSuccess) return cuda_fail(e, "group launch");
+        if (qmoe_status r = run_quantize(xtype, q, d->sms, st)) return r;
+    }
 
     Gmm g = {};
     g.type = QMOE_E4M3;

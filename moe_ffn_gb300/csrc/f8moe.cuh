@@ -20,9 +20,10 @@ __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 // ---------------------------------------------------------------- quantise
 // Sixteen lanes share a 128-column block, eight consecutive columns each:
 // one or two 16-byte loads, a four-step maximum, one 8-byte store.  They take
-// Q_RUN neighbouring blocks of a row, all loaded before the first is reduced:
-// bound by HBM, (size + 1) bytes per element, this keeps 64 bytes per thread in
-// flight (one block at a time reached 3.1 TB/s).  VEC needs 16-byte aligned
+// RUN neighbouring blocks of a row, all loaded before the first is reduced.
+// Bound by HBM, (size + 1) bytes per element: RUN = 4 keeps 64 bytes per thread
+// in flight (4096 x 14336 bf16: 46 us, with RUN = 1 58 us); RUN = 1 spreads few
+// rows over more threads (1 x 2048: 1.9 against 2.7 us).  VEC needs 16-byte aligned
 // rows and whole groups of eight columns; the other form loads element by
 // element.
 //
@@ -37,10 +38,9 @@ struct QuantParams {
     int k;            // slots per token (pos)
     int64_t rows;
     int cols, nblk;
-    int nrun;         // runs of Q_RUN blocks per row
+    int nrun;         // runs of RUN blocks per row
 };
 constexpr int Q_THREADS = 256;
-constexpr int Q_RUN = 4;
 
 template <class T>
 __device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
@@ -57,7 +57,7 @@ __device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
     }
 }
 
-template <class T, bool VEC>
+template <class T, bool VEC, int RUN>
 __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const QuantParams p) {
     pdl_wait();
     pdl_trigger();
@@ -67,18 +67,18 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const QuantParams p
     int blk0;
     if (p.rows * p.nrun <= 0x7fffffff) {
         row = static_cast<uint32_t>(item) / static_cast<uint32_t>(p.nrun);
-        blk0 = (static_cast<int>(item) - static_cast<int>(row) * p.nrun) * Q_RUN;
+        blk0 = (static_cast<int>(item) - static_cast<int>(row) * p.nrun) * RUN;
     } else {
         row = item / p.nrun;
-        blk0 = static_cast<int>(item - row * p.nrun) * Q_RUN;
+        blk0 = static_cast<int>(item - row * p.nrun) * RUN;
     }
     const bool live = row < p.rows;
-    const int nb = live ? min(Q_RUN, p.nblk - blk0) : 0;
+    const int nb = live ? min(RUN, p.nblk - blk0) : 0;
     const int c0 = blk0 * F8_BLOCK + sub * 8;
     const T* src = static_cast<const T*>(p.x) + (live ? row : 0) * p.ldx + c0;
-    float v[Q_RUN][8];
+    float v[RUN][8];
 #pragma unroll
-    for (int b = 0; b < Q_RUN; ++b) {
+    for (int b = 0; b < RUN; ++b) {
         const int c = c0 + b * F8_BLOCK;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[b][i] = 0.f;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const QuantParams p
         }
     }
 #pragma unroll
-    for (int b = 0; b < Q_RUN; ++b) {
+    for (int b = 0; b < RUN; ++b) {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[b][i]));
@@ -226,6 +226,78 @@ __global__ void __launch_bounds__(G_THREADS) group_kernel(const int32_t* __restr
         }
     }
     cluster_sync();  // no CTA leaves while another may read its totals
+}
+
+// ------------------------------------------------------- group + quantise
+// Both steps for few pairs (P <= GQ_PAIRS), one CTA per token: every CTA reads
+// all the expert indices and counts, for each of its token's slots, the pairs
+// that come before it (smaller expert, or the same expert earlier); the first
+// also counts the offsets.  One launch instead of two, whose cost is latency.
+constexpr int GQ_PAIRS = 256;
+
+template <class T>
+__global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
+    const QuantParams p, const int32_t* __restrict__ idx, int P, int E,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ pos_out) {
+    __shared__ int s_idx[GQ_PAIRS];
+    __shared__ int s_pos[32];
+    const int tid = threadIdx.x, t = blockIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    for (int i = tid; i < P; i += Q_THREADS) {
+        const int e = __ldg(idx + i);
+        s_idx[i] = e >= 0 && e < E ? e : -1;
+    }
+    if (tid < 32) s_pos[tid] = 0;
+    __syncthreads();
+    // a warp per slot
+    for (int s = tid >> 5; s < p.k; s += Q_THREADS / 32) {
+        const int me = t * p.k + s, e = s_idx[me];
+        int n = 0;
+        for (int i = tid & 31; i < P; i += 32) {
+            const int o = s_idx[i];
+            n += o >= 0 && (o < e || (o == e && i < me));
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if ((tid & 31) == 0) {
+            s_pos[s] = e < 0 ? -1 : n;
+            pos_out[me] = e < 0 ? -1 : n;
+        }
+    }
+    if (t == 0)
+        for (int e = tid; e <= E; e += Q_THREADS) {
+            int n = 0;
+            for (int i = 0; i < P; ++i) n += s_idx[i] >= 0 && s_idx[i] < e;
+            offsets[e] = n;
+        }
+    __syncthreads();
+    const T* src = static_cast<const T*>(p.x) + t * p.ldx;
+    const int sub = tid & 15;
+    for (int b0 = 0; b0 < p.nblk; b0 += Q_THREADS / 16) {
+        const int b = b0 + (tid >> 4);
+        const int c = b * F8_BLOCK + sub * 8;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        if (b < p.nblk) load8(src + c, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[i]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (b >= p.nblk) continue;
+        float s, inv;
+        f8_scale(m, &s, &inv);
+        uint2 q;
+        q.x = f8_pack2(v[0] * inv, v[1] * inv) | (f8_pack2(v[2] * inv, v[3] * inv) << 16);
+        q.y = f8_pack2(v[4] * inv, v[5] * inv) | (f8_pack2(v[6] * inv, v[7] * inv) << 16);
+        for (int i = 0; i < p.k; ++i) {
+            const int64_t r = s_pos[i];
+            if (r < 0) continue;
+            *reinterpret_cast<uint2*>(p.q + r * p.cols + c) = q;
+            if (sub == 0) p.s[r * p.nblk + b] = s;
+        }
+    }
 }
 
 // ----------------------------------------------------------------- combine

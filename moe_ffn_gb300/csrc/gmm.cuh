@@ -14,13 +14,20 @@
 //   y[r][n] = sum_b sx sw sum_{k in b} xq Wq.
 // The tensor core forms the inner sum of one k-block exactly as products
 // and in f32 as sums; the epilogue warps then add (sx sw) * partial to f32
-// registers while the tensor core works on the next block (two TMEM
-// buffers).  f16/bf16 products accumulate in TMEM over the whole of K.
+// registers while the tensor core works on the next blocks.  f16/bf16 products
+// accumulate in TMEM over the whole of K.
+//
+// This file holds the parts all forms share and the kernel for few rows per
+// group (gmm_kernel): bound by streaming the weights, so its tiles are small
+// (128 weight rows, 32 tokens) and, where there are fewer tiles than SMs, the
+// CTAs of a cluster share a tile's K range and add their parts through
+// distributed shared memory, in rank order.  gmm_pair.cuh has the kernel for
+// many rows.
 //
 // Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs,
 // warps 2-3 stage the scale products, warps 4-11 are the epilogue: warp w
 // reads TMEM lanes 32 (w % 4) .. +31, and the two groups of four warps take
-// alternate runs of columns.
+// sixteen columns each.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -61,55 +68,44 @@ struct Params {
     DevCtl* err;
 };
 
-// Configuration of one instantiation.
+// Configuration of one instantiation of the kernel for few rows.
 //   F8     e4m3 operands with scales (else 16-bit)
-//   NT     largest token tile (columns)
 //   NST    pipeline stages
 //   GU     two weight stacks (gate, up) and the SwiGLU + e4m3 epilogue
-//   SPLIT  the CTAs of a cluster share a tile's K range and add their parts
-template <bool F8_, int NT_, int NST_, bool GU_, bool SPLIT_>
+template <bool F8_, int NST_, bool GU_>
 struct Cfg {
-    static constexpr bool F8 = F8_, GU = GU_, SPLIT = SPLIT_;
-    static constexpr int NT = NT_, NST = NST_;
+    static constexpr bool F8 = F8_, GU = GU_;
+    static constexpr int NT = 32, NST = NST_;  // token tile
     static constexpr int NA = GU ? 2 : 1;
-    static constexpr int BOX = NT < 64 ? NT : 64;  // token rows per TMA box
+    static constexpr int BOX = NT;  // token rows per TMA box
     static constexpr int A_BYTES = TILE_W * KBLK;
-    static constexpr int B_BYTES = NT * KBLK;
-    static constexpr int STAGE = NA * A_BYTES + B_BYTES;
-    static constexpr int CH = NT >= 64 ? 32 : 16;  // columns per TMEM load
-    static constexpr int NCH = NT / CH / 2;        // such runs per epilogue warp
+    static constexpr int STAGE = NA * A_BYTES + NT * KBLK;
+    static constexpr int CH = 16;  // columns per epilogue warp
+    static constexpr int NBUF = 4;                 // accumulator buffers
     static constexpr int TM_BUF = NA * NT;         // TMEM columns per buffer
-    static constexpr int TM_COLS = 2 * TM_BUF < 32 ? 32 : 2 * TM_BUF;
+    static constexpr int TM_COLS = NBUF * TM_BUF;
     static constexpr int SC_STAGE = SC_BLK * NA * NT;  // floats
     // byte offsets in shared memory
     static constexpr int O_SC = NST * STAGE;
     static constexpr int O_PART = O_SC + (F8 ? SC_RING * SC_STAGE * 4 : 0);
-    static constexpr int O_AMAX = O_PART + (SPLIT ? NT * TILE_W * 4 : 0);
+    static constexpr int O_AMAX = O_PART + NA * NT * TILE_W * 4;
     static constexpr int O_BAR = O_AMAX + (GU ? 2 * 4 * NT * 4 : 0);
-    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 4 + 1;
+    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1;
     static constexpr int O_TAB = O_BAR + (N_BAR + 1) * 8;
     // tables: first row, end row and first tile of each group, total last
     static constexpr int smem(int E) { return 1024 + O_TAB + (3 * E + 4) * 4; }
-    static_assert(NT % (2 * CH) == 0 && NT <= 256 && TM_COLS <= 512, "tile shape");
-    static_assert((TM_COLS & (TM_COLS - 1)) == 0, "TMEM columns: a power of two");
+    static_assert((TM_COLS & (TM_COLS - 1)) == 0 && TM_COLS <= 512, "TMEM columns");
 };
+constexpr int MAX_RANKS = 8;  // CTAs that may share a tile
 
-// acc += v * s on pairs (one packed FMA).
-__device__ __forceinline__ void fma2(float& a0, float& a1, float v0, float v1, float s0,
+// a += v * s on pairs (one packed FMA), v as bits.
+__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t v1, float s0,
                                      float s1) {
     asm("{\n\t.reg .b64 a, v, s;\n\t"
         "mov.b64 a, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\t"
         "fma.rn.f32x2 a, v, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
         : "+f"(a0), "+f"(a1)
-        : "f"(v0), "f"(v1), "f"(s0), "f"(s1));
-}
-
-template <class C>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[C::CH]) {
-    if constexpr (C::CH == 32)
-        umma::ld_32x32b_x32(addr, r);
-    else
-        umma::ld_32x32b_x16(addr, r);
+        : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
 }
 
 __device__ __forceinline__ void store_out(void* y, int64_t i, int type, float v) {
@@ -121,6 +117,25 @@ __device__ __forceinline__ void store_out(void* y, int64_t i, int type, float v)
         static_cast<float*>(y)[i] = v;
 }
 
+// silu(g) u with the fast f32 exponential and division (2^-20 or better).
+__device__ __forceinline__ float swiglu(float g, float u) {
+    return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
+// The cluster's values at this CTA's address `src`, added in rank order; all
+// loads are issued before the first sum.
+__device__ __forceinline__ float cluster_sum(const float* src, int ranks) {
+    float v[MAX_RANKS];
+#pragma unroll
+    for (int q = 0; q < MAX_RANKS; ++q)
+        v[q] = q < ranks ? cluster_ld_f32(src, static_cast<uint32_t>(q)) : 0.f;
+    float s = v[0];
+#pragma unroll
+    for (int q = 1; q < MAX_RANKS; ++q)
+        if (q < ranks) s += v[q];
+    return s;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -130,39 +145,40 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The groups' tables, by one warp: rows [lo, hi) of each group and the tiles
-// before it, the total last.  Offsets are clamped into [0, M], so that no
-// value of theirs forms an address outside x or y.
-__device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, int lane, int* t_lo,
+// The groups' tables, by the whole CTA (ends with a barrier): rows [lo, hi) of
+// each group and the tiles before it, the total last.  Offsets are clamped into
+// [0, M], so that no value of theirs forms an address outside x or y.  Every
+// thread loads its groups' offsets first, so the loads cost one latency.
+__device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, int* t_lo,
                                              int* t_hi, int* t_pre) {
-    int total = 0;
     bool bad = false;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < p.E) {
-            if (p.offsets)
-                bad |= !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M, &lo,
-                                   &hi);
-            else
-                hi = p.M;
-        }
-        const int n = group_tiles(hi - lo, nt, nb);
-        int s = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += v;
-        }
-        if (e < p.E) {
-            t_lo[e] = lo;
-            t_hi[e] = hi;
-            t_pre[e] = total + s - n;
-        }
-        total += __shfl_sync(0xffffffffu, s, 31);
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        int lo = 0, hi = p.M;
+        if (p.offsets)
+            bad |= !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M, &lo, &hi);
+        t_lo[e] = lo;
+        t_hi[e] = hi;
     }
-    if (lane == 0) t_pre[p.E] = total;
     if (bad) record_error(p.err, DEV_GMM_OFFSETS);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int total = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int n = e < p.E ? group_tiles(t_hi[e] - t_lo[e], nt, nb) : 0;
+            int s = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += v;
+            }
+            if (e < p.E) t_pre[e] = total + s - n;
+            total += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) t_pre[p.E] = total;
+    }
+    __syncthreads();
 }
 
 template <class C>
@@ -181,9 +197,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* empty = full + C::NST;
     uint64_t* sc_full = empty + C::NST;
     uint64_t* sc_empty = sc_full + SC_RING;
-    uint64_t* acc_full = sc_empty + SC_RING;  // [2]
-    uint64_t* acc_empty = acc_full + 2;       // [2]
-    uint64_t* mma_done = acc_empty + 2;
+    uint64_t* acc_full = sc_empty + SC_RING;
+    uint64_t* acc_empty = acc_full + C::NBUF;
+    uint64_t* mma_done = acc_empty + C::NBUF;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BAR);
     int* t_lo = reinterpret_cast<int*>(base + C::O_TAB);
     int* t_hi = t_lo + p.E;
@@ -201,36 +217,32 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&sc_full[i], 2);
             mbar_init(&sc_empty[i], EPI_WARPS);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::NBUF; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], EPI_WARPS);
         }
         mbar_init(mma_done, 1);
         fence_barrier_init();
+        prefetch_tensormap(&tm_w);
+        prefetch_tensormap(&tm_x);
+        if constexpr (C::GU) prefetch_tensormap(&tm_w2);
     }
     // Every operand may be an earlier launch's output (weights quantised on
     // this stream too), so nothing is read before the dependency wait.
     pdl_wait();
     pdl_trigger();
-    if (warp == 0) build_tables(p, C::NT, p.nb, lane, t_lo, t_hi, t_pre);
     umma::fence_before_sync();
-    __syncthreads();
+    build_tables(p, C::NT, p.nb, t_lo, t_hi, t_pre);
     umma::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const int tiles = t_pre[p.E];
 
-    // tiles first, first + step, ...; with SPLIT a cluster has one tile and
-    // each of its CTAs a share of K
-    int first = blockIdx.x, step = gridDim.x, kbeg = 0, kend = p.kb;
-    uint32_t rank = 0, ranks = 1;
-    if constexpr (C::SPLIT) {
-        rank = cluster_rank();
-        ranks = cluster_size();
-        first = blockIdx.x / ranks;
-        step = tiles > 0 ? tiles : 1;
-        kbeg = static_cast<int>(rank * p.kb / ranks);
-        kend = static_cast<int>((rank + 1) * p.kb / ranks);
-    }
+    // A cluster takes tiles first, first + step, ...; a cluster of more than one
+    // CTA takes one tile, each of its CTAs a share of K.
+    const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+    const int first = blockIdx.x / ranks;
+    const int step = ranks > 1 ? max(tiles, 1) : gridDim.x;
+    const int kbeg = rank * p.kb / ranks, kend = (rank + 1) * p.kb / ranks;
 
     if (warp == 0) {
         // ---------------------------------------------------------- loads
@@ -284,11 +296,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
             for (int kb = kbeg; kb < kend; ++kb) {
                 const bool fresh = C::F8 || kb == kbeg;  // a new accumulator buffer
-                if (fresh && !mbar_wait_spin(&acc_empty[ab], aph, p.err, DEV_GMM_TIMEOUT)) {
-                    ok = false;
-                    break;
-                }
-                if (!mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT)) {
+                if ((fresh && !mbar_wait_spin(&acc_empty[ab], aph, p.err, DEV_GMM_TIMEOUT)) ||
+                    !mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT)) {
                     ok = false;
                     break;
                 }
@@ -314,7 +323,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (last) umma::commit(&acc_full[ab]);
                 }
                 __syncwarp();
-                if (last && (ab ^= 1) == 0) aph ^= 1;
+                if (last && ++ab == C::NBUF) {
+                    ab = 0;
+                    aph ^= 1;
+                }
                 if (++s == C::NST) {
                     s = 0;
                     ph ^= 1;
@@ -384,106 +396,97 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         // ------------------------------------------------------- epilogue
         const int quad = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t tm_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        int ab = 0, ch = 0, par = 0;
+        const int col = half * C::CH;  // this warp's columns
+        const uint32_t tm_run = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col;
+        uint32_t ab = 0, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step, par ^= 1) {
             const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
-            float acc[C::NA][C::NCH][C::CH];
+            float acc[C::NA][C::CH];
 #pragma unroll
             for (int a = 0; a < C::NA; ++a)
 #pragma unroll
-                for (int i = 0; i < C::NCH; ++i)
-#pragma unroll
-                    for (int c = 0; c < C::CH; ++c) acc[a][i][c] = 0.f;
+                for (int c = 0; c < C::CH; ++c) acc[a][c] = 0.f;
             const int periods = C::F8 ? kend - kbeg : 1;
-            for (int k = 0; k < periods; ++k, ++ab) {
-                const float* sc = nullptr;
-                if constexpr (C::F8) {
-                    const int s = ch % SC_RING;
-                    if ((k % SC_BLK) == 0 && !mbar_wait_spin(&sc_full[s], (ch / SC_RING) & 1,
-                                                                p.err, DEV_GMM_TIMEOUT)) {
-                        ok = false;
-                        break;
-                    }
-                    sc = ring + s * C::SC_STAGE + (k % SC_BLK) * C::NA * C::NT;
-                }
-                if (!mbar_wait_spin(&acc_full[ab & 1], (ab >> 1) & 1, p.err,
-                                       DEV_GMM_TIMEOUT)) {
-                    ok = false;
-                    break;
-                }
+            for (int k = 0; k < periods; ++k) {
+                const int kk = k % SC_BLK;
+                if (C::F8 && kk == 0)
+                    ok = mbar_wait_spin(&sc_full[cs], cph, p.err, DEV_GMM_TIMEOUT);
+                ok = ok && mbar_wait_spin(&acc_full[ab], aph, p.err, DEV_GMM_TIMEOUT);
+                if (!ok) break;
                 umma::fence_after_sync();
+                if (col < w.np) {
+                    uint32_t r[C::NA][C::CH];
+#pragma unroll
+                    for (int a = 0; a < C::NA; ++a)
+                        umma::ld_32x32b_x16(tm_run + ab * C::TM_BUF + a * C::NT, r[a]);
+#pragma unroll
+                    for (int a = 0; a < C::NA; ++a) umma::wait_ld(r[a]);
+                    if constexpr (C::F8) {
+                        const float* sc =
+                            ring + cs * C::SC_STAGE + kk * C::NA * C::NT + col;
+#pragma unroll
+                        for (int a = 0; a < C::NA; ++a)
+#pragma unroll
+                            for (int c = 0; c < C::CH; c += 4) {
+                                const float4 s =
+                                    *reinterpret_cast<const float4*>(sc + a * C::NT + c);
+                                fma2(acc[a][c], acc[a][c + 1], r[a][c], r[a][c + 1], s.x, s.y);
+                                fma2(acc[a][c + 2], acc[a][c + 3], r[a][c + 2], r[a][c + 3], s.z,
+                                     s.w);
+                            }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < C::CH; ++c) acc[0][c] = __uint_as_float(r[0][c]);
+                    }
+                }
+                umma::fence_before_sync();
+                __syncwarp();
+                const bool ring_done = C::F8 && (kk == SC_BLK - 1 || k == periods - 1);
+                if (lane == 0) {
+                    mbar_arrive(&acc_empty[ab]);
+                    if (ring_done) mbar_arrive(&sc_empty[cs]);
+                }
+                if (++ab == C::NBUF) {
+                    ab = 0;
+                    aph ^= 1;
+                }
+                if (ring_done && ++cs == SC_RING) {
+                    cs = 0;
+                    cph ^= 1;
+                }
+            }
+            if (ranks > 1) {
+                // this CTA's part of the tile, [a][column][weight row]; NaN if a wait
+                // ran out, so that the cluster's sum does not pass for a result
 #pragma unroll
                 for (int a = 0; a < C::NA; ++a)
 #pragma unroll
-                    for (int i = 0; i < C::NCH; ++i) {
-                        const int col = (2 * i + half) * C::CH;
-                        if (col < w.np) {
-                            uint32_t r[C::CH];
-                            tmem_ld<C>(tm_lane + (ab & 1) * C::TM_BUF + a * C::NT + col, r);
-                            umma::wait_ld(r);
-                            if constexpr (C::F8) {
-                                const float4* s4 =
-                                    reinterpret_cast<const float4*>(sc + a * C::NT + col);
-#pragma unroll
-                                for (int c = 0; c < C::CH; c += 4) {
-                                    const float4 s = s4[c / 4];
-                                    fma2(acc[a][i][c], acc[a][i][c + 1], __uint_as_float(r[c]),
-                                         __uint_as_float(r[c + 1]), s.x, s.y);
-                                    fma2(acc[a][i][c + 2], acc[a][i][c + 3],
-                                         __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]),
-                                         s.z, s.w);
-                                }
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < C::CH; ++c)
-                                    acc[a][i][c] = __uint_as_float(r[c]);
-                            }
-                        }
-                    }
-                umma::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&acc_empty[ab & 1]);
-                    if (C::F8 && ((k % SC_BLK) == SC_BLK - 1 || k == periods - 1))
-                        mbar_arrive(&sc_empty[ch % SC_RING]);
-                }
-                if (C::F8 && ((k % SC_BLK) == SC_BLK - 1 || k == periods - 1)) ++ch;
-            }
-            if (!ok) {
-                // the cluster's sum must not pass for a result
-                if constexpr (C::SPLIT)
-                    for (int j = half; j < w.nv; j += 2)
-                        part[j * TILE_W + quad * 32 + lane] = __int_as_float(0x7FC00000);
+                    for (int c = 0; c < C::CH; ++c)
+                        if (col + c < w.nv)
+                            part[(a * C::NT + col + c) * TILE_W + quad * 32 + lane] =
+                                ok ? acc[a][c] : __int_as_float(0x7FC00000);
                 break;
             }
+            if (!ok) break;
             const int nr = w.nbi * TILE_W + quad * 32 + lane;  // this thread's weight row
             if constexpr (C::GU) {
                 // a = silu(g) u; a tile's 128 rows are one scale block of the
-                // activations, so the maximum over lanes and warps is the
-                // block's
+                // activations, so the maximum over lanes and warps is the block's
                 uint32_t* am = amax + par * 4 * C::NT;
-#pragma unroll
-                for (int i = 0; i < C::NCH; ++i) {
-                    const int col = (2 * i + half) * C::CH;
-                    if (col >= w.np) continue;
+                if (col < w.np) {
                     uint32_t mine = 0;
 #pragma unroll
                     for (int c = 0; c < C::CH; ++c) {
-                        const float g = acc[0][i][c], u = acc[C::NA - 1][i][c];
-                        const float v = __fdividef(g, 1.0f + __expf(-g)) * u;
-                        acc[0][i][c] = v;
-                        const uint32_t m = __reduce_max_sync(0xffffffffu, finite_abs_bits(v));
+                        acc[0][c] = swiglu(acc[0][c], acc[C::NA - 1][c]);
+                        const uint32_t m =
+                            __reduce_max_sync(0xffffffffu, finite_abs_bits(acc[0][c]));
                         if (lane == c) mine = m;
                     }
                     if (lane < C::CH) am[quad * C::NT + col + lane] = mine;
                 }
                 named_bar(1 + half, 128);
-#pragma unroll
-                for (int i = 0; i < C::NCH; ++i) {
-                    const int col = (2 * i + half) * C::CH;
-                    if (col >= w.np) continue;
+                if (col < w.np) {
                     float s = 1.f, inv = 1.f;
                     if (lane < C::CH) {
                         const int j = col + lane;
@@ -497,57 +500,61 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int c = 0; c < C::CH; c += 2) {
                         const float i0 = __shfl_sync(0xffffffffu, inv, c);
                         const float i1 = __shfl_sync(0xffffffffu, inv, c + 1);
-                        const uint32_t q = f8_pack2(acc[0][i][c] * i0, acc[0][i][c + 1] * i1);
-                        const int64_t o = static_cast<int64_t>(w.row0 + col + c) * p.N + nr;
-                        if (col + c < w.nv) p.aq[o] = static_cast<uint8_t>(q & 0xFF);
-                        if (col + c + 1 < w.nv) p.aq[o + p.N] = static_cast<uint8_t>(q >> 8);
+                        const uint32_t q = f8_pack2(acc[0][c] * i0, acc[0][c + 1] * i1);
+                        uint8_t* dst =
+                            p.aq + static_cast<int64_t>(w.row0 + col + c) * p.N + nr;
+                        if (col + c < w.nv) dst[0] = static_cast<uint8_t>(q & 0xFF);
+                        if (col + c + 1 < w.nv) dst[p.N] = static_cast<uint8_t>(q >> 8);
                     }
                 }
-            } else if constexpr (C::SPLIT) {
+            } else if (nr < p.N) {
 #pragma unroll
-                for (int i = 0; i < C::NCH; ++i) {
-                    const int col = (2 * i + half) * C::CH;
-#pragma unroll
-                    for (int c = 0; c < C::CH; ++c)
-                        if (col + c < w.nv)
-                            part[(col + c) * TILE_W + quad * 32 + lane] = acc[0][i][c];
-                }
-            } else {
-                if (nr < p.N) {
-#pragma unroll
-                    for (int i = 0; i < C::NCH; ++i) {
-                        const int col = (2 * i + half) * C::CH;
-#pragma unroll
-                        for (int c = 0; c < C::CH; ++c)
-                            if (col + c < w.nv)
-                                store_out(p.y,
-                                          static_cast<int64_t>(w.row0 + col + c) * p.ldy + nr,
-                                          p.out, acc[0][i][c]);
-                    }
-                }
+                for (int c = 0; c < C::CH; ++c)
+                    if (col + c < w.nv)
+                        store_out(p.y, static_cast<int64_t>(w.row0 + col + c) * p.ldy + nr, p.out,
+                                  acc[0][c]);
             }
         }
     }
 
     __syncwarp();
-    if constexpr (C::SPLIT) {
-        // add the ranks' parts in rank order; rank r takes columns r, r + ranks, ...
+    if (ranks > 1) {
+        // add the ranks' parts in rank order; rank r takes columns r, r + ranks, ...,
+        // a thread one weight row
         cluster_sync();
         if (warp >= 4 && first < tiles) {
             const Tile w = tile_at(first, C::NT, 16, t_lo, t_hi, t_pre, p.E);
-            const int et = tid - 128, r = et & 127;
+            const int half = (warp - 4) >> 2, r = (tid - 128) & 127;
             const int nr = w.nbi * TILE_W + r;
-            if (nr < p.N)
-                for (int j = static_cast<int>(rank) + static_cast<int>(ranks) * (et >> 7);
-                     j < w.nv; j += 2 * static_cast<int>(ranks)) {
-                    float v = 0.f;
-                    for (uint32_t q = 0; q < ranks; ++q)
-                        v += cluster_ld_f32(part + j * TILE_W + r, q);
-                    store_out(p.y, static_cast<int64_t>(w.row0 + j) * p.ldy + nr, p.out, v);
+            for (int j0 = 0; j0 < w.nv; j0 += 2 * ranks) {
+                const int j = j0 + rank + ranks * half;
+                float v[C::NA];
+                if (j < w.nv) {
+#pragma unroll
+                    for (int a = 0; a < C::NA; ++a)
+                        v[a] = cluster_sum(part + (a * C::NT + j) * TILE_W + r, ranks);
                 }
+                if constexpr (C::GU) {
+                    float a = 0.f;
+                    if (j < w.nv) a = swiglu(v[0], v[C::NA - 1]);
+                    const uint32_t m = __reduce_max_sync(0xffffffffu, finite_abs_bits(a));
+                    uint32_t* am = amax + ((j0 / (2 * ranks)) & 1) * 8 + half * 4;
+                    if (lane == 0) am[warp & 3] = m;
+                    named_bar(1 + half, 128);
+                    float s, inv;
+                    f8_scale(max(max(am[0], am[1]), max(am[2], am[3])), &s, &inv);
+                    if (j < w.nv) {
+                        p.aq[static_cast<int64_t>(w.row0 + j) * p.N + nr] =
+                            static_cast<uint8_t>(f8_pack2(a * inv, 0.f) & 0xFF);
+                        if (r == 0) p.as[static_cast<int64_t>(w.row0 + j) * p.nb + w.nbi] = s;
+                    }
+                } else if (j < w.nv && nr < p.N) {
+                    store_out(p.y, static_cast<int64_t>(w.row0 + j) * p.ldy + nr, p.out, v[0]);
+                }
+            }
         }
         __syncwarp();
-        cluster_sync();
+        cluster_sync();  // no CTA leaves while another may read its part
     }
     umma::fence_before_sync();
     __syncthreads();

@@ -192,13 +192,14 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         mbar_init(mma_done, 1);
         fence_barrier_init();
+        prefetch_tensormap(&tm_w);
+        prefetch_tensormap(&tm_x);
+        if constexpr (C::GU) prefetch_tensormap(&tm_w2);
     }
     pdl_wait();
     pdl_trigger();
-    const int nbt = (p.nb + 1) / 2;  // tiles of 256 weight rows
-    if (warp == 0) build_tables(p, C::NT, nbt, lane, t_lo, t_hi, t_pre);
     umma::fence_before_sync();
-    __syncthreads();
+    build_tables(p, C::NT, (p.nb + 1) / 2, t_lo, t_hi, t_pre);
     cluster_sync();  // both CTAs' barriers exist before either is signalled
     umma::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                             for (int r = 0; r < 4; ++r) {
                                 const float g = acc[0][r >> 1][2 * i + (r & 1)];
                                 const float u = acc[1][r >> 1][2 * i + (r & 1)];
-                                const float v = __fdividef(g, 1.0f + __expf(-g)) * u;
+                                const float v = swiglu(g, u);
                                 acc[0][r >> 1][2 * i + (r & 1)] = v;
                                 m = max(m, finite_abs_bits(v));
                             }

@@ -301,6 +301,11 @@ __device__ __forceinline__ void cp_async_drain() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// Brings a tensor map (a __grid_constant__ parameter) to the copy engine.
+__device__ __forceinline__ void prefetch_tensormap(const void* tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // Register share of a warpgroup (every warp of it executes this).
 template <int N>
 __device__ __forceinline__ void regs_dec() {
