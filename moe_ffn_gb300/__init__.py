@@ -266,32 +266,49 @@ def moe_ffn_noalloc(router_W, gate_stack, up_stack, down_stack, shape: _Shape, x
 
 
 # ------------------------------- e4m3 / bf16 / f16 products (include/qmoe.h)
+# One-token calls take a few microseconds on the GPU, so these functions keep
+# their own cost low: cheap tensor checks, and the current device and stream
+# asked of torch once per call.
+_I32 = -1
 _DTYPES = {}
 
 
-def _arg(fn: str, name: str, t, kind: int, need: int):
-    """Address of a device array of at least `need` elements of type `kind`.
+def _context(stream):
+    """(current CUDA device or -1, stream address); an int stream is taken as is."""
+    import torch
+    if not _DTYPES:
+        _DTYPES.update({F32: (torch.float32,), BF16: (torch.bfloat16,), F16: (torch.float16,),
+                        E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8),
+                        _I32: (torch.int32,)})
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    return dev, stream
+
+
+def _arg(fn: str, name: str, t, kind, need: int, dev: int):
+    """Address of a device array of at least `need` elements of type `kind`
+    (None: any type).
 
     Integers (addresses) and None pass through unchecked; a tensor must live
     on the current CUDA device, have the element type the call names (one-byte
     types for E4M3) and reach `need` elements from its first one."""
     if t is None or isinstance(t, int):
         return t
-    import torch
-    if not _DTYPES:
-        _DTYPES.update({F32: (torch.float32,), BF16: (torch.bfloat16,), F16: (torch.float16,),
-                        E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8),
-                        "i32": (torch.int32,)})
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != dev:
         raise QmoeError(ERR_INVALID_ARGUMENT,
                         f"{fn}: {name} is on {t.device}, not on the current CUDA device")
-    want = _DTYPES.get(kind)
-    if want is not None and t.dtype not in want:
-        raise QmoeError(ERR_INVALID_ARGUMENT, f"{fn}: {name} has dtype {t.dtype}, not {want[0]}")
-    have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-    if have < need:
+    # (an unknown type number is left to the library, which refuses it)
+    if kind in _DTYPES and t.dtype not in _DTYPES[kind]:
         raise QmoeError(ERR_INVALID_ARGUMENT,
-                        f"{fn}: {name} holds {have} elements, {need} are needed")
+                        f"{fn}: {name} has dtype {t.dtype}, not {_DTYPES[kind][0]}")
+    if not (t.is_contiguous() and t.numel() >= need):
+        have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+        if have < need:
+            raise QmoeError(ERR_INVALID_ARGUMENT,
+                            f"{fn}: {name} holds {have} elements, {need} are needed")
     return t.data_ptr()
 
 
@@ -307,10 +324,11 @@ def f8_blocks(n: int) -> int:
 def f8_quantize(xtype: int, x, rows: int, cols: int, q, scale, ldx=None, stream=None) -> None:
     """q, scale = e4m3 rows of x with one scale per 128 columns (see include/qmoe.h)."""
     fn, ldx = "f8_quantize", cols if ldx is None else ldx
-    _check(lib().f8_quantize(xtype, _arg(fn, "x", x, xtype, _span(rows, cols, ldx)), rows, cols,
-                             ldx, _arg(fn, "q", q, E4M3, rows * cols),
-                             _arg(fn, "scale", scale, F32, rows * f8_blocks(cols)),
-                             _stream(stream)))
+    dev, st = _context(stream)
+    _check((_libh or lib()).f8_quantize(
+        xtype, _arg(fn, "x", x, xtype, _span(rows, cols, ldx), dev), rows, cols, ldx,
+        _arg(fn, "q", q, E4M3, rows * cols, dev),
+        _arg(fn, "scale", scale, F32, rows * f8_blocks(cols), dev), st))
 
 
 def f8_mm(W, w_scale, rows: int, cols: int, x, x_scale, n_tokens: int, ytype: int, y, ldx=None,
@@ -318,12 +336,13 @@ def f8_mm(W, w_scale, rows: int, cols: int, x, x_scale, n_tokens: int, ytype: in
     """y = x W^T with e4m3 operands and block scales (see include/qmoe.h)."""
     fn, kb = "f8_mm", f8_blocks(cols)
     ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
-    _check(lib().f8_mm(_arg(fn, "W", W, E4M3, rows * cols),
-                       _arg(fn, "w_scale", w_scale, F32, f8_blocks(rows) * kb), rows, cols,
-                       _arg(fn, "x", x, E4M3, _span(n_tokens, cols, ldx)),
-                       _arg(fn, "x_scale", x_scale, F32, n_tokens * kb), n_tokens, ldx, ytype,
-                       _arg(fn, "y", y, ytype, _span(n_tokens, rows, ldy)), ldy,
-                       _stream(stream)))
+    dev, st = _context(stream)
+    _check((_libh or lib()).f8_mm(
+        _arg(fn, "W", W, E4M3, rows * cols, dev),
+        _arg(fn, "w_scale", w_scale, F32, f8_blocks(rows) * kb, dev), rows, cols,
+        _arg(fn, "x", x, E4M3, _span(n_tokens, cols, ldx), dev),
+        _arg(fn, "x_scale", x_scale, F32, n_tokens * kb, dev), n_tokens, ldx, ytype,
+        _arg(fn, "y", y, ytype, _span(n_tokens, rows, ldy), dev), ldy, st))
 
 
 def mm_grouped(wtype: int, W, w_scale, num_groups: int, rows: int, cols: int, x, x_scale,
@@ -331,14 +350,14 @@ def mm_grouped(wtype: int, W, w_scale, num_groups: int, rows: int, cols: int, x,
     """y[r] = W_g x[r] for the rows of every group (see include/qmoe.h)."""
     fn, kb = "mm_grouped", f8_blocks(cols)
     ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
-    _check(lib().mm_grouped(wtype, _arg(fn, "W", W, wtype, num_groups * rows * cols),
-                            _arg(fn, "w_scale", w_scale, F32, num_groups * f8_blocks(rows) * kb),
-                            num_groups, rows, cols,
-                            _arg(fn, "x", x, wtype, _span(n_rows, cols, ldx)),
-                            _arg(fn, "x_scale", x_scale, F32, n_rows * kb), n_rows, ldx,
-                            _arg(fn, "offsets", offsets, "i32", num_groups + 1), ytype,
-                            _arg(fn, "y", y, ytype, _span(n_rows, rows, ldy)), ldy,
-                            _stream(stream)))
+    dev, st = _context(stream)
+    _check((_libh or lib()).mm_grouped(
+        wtype, _arg(fn, "W", W, wtype, num_groups * rows * cols, dev),
+        _arg(fn, "w_scale", w_scale, F32, num_groups * f8_blocks(rows) * kb, dev), num_groups,
+        rows, cols, _arg(fn, "x", x, wtype, _span(n_rows, cols, ldx), dev),
+        _arg(fn, "x_scale", x_scale, F32, n_rows * kb, dev), n_rows, ldx,
+        _arg(fn, "offsets", offsets, _I32, num_groups + 1, dev), ytype,
+        _arg(fn, "y", y, ytype, _span(n_rows, rows, ldy), dev), ldy, st))
 
 
 def moe_experts_f8_workspace_size(shape: _Shape) -> int:
@@ -353,22 +372,22 @@ def moe_experts_f8(gate_stack, gate_scale, up_stack, up_scale, down_stack, down_
                    ws_bytes=None, stream=None) -> None:
     """out = residual + the routed experts' weighted outputs (see include/qmoe.h)."""
     fn = "moe_experts_f8"
-    H, F, E = shape.hidden, shape.expert_dim, shape.num_experts
-    T, P = shape.n_tokens, shape.n_tokens * shape.top_k
+    H, F, E, T = shape.hidden, shape.expert_dim, shape.num_experts, shape.n_tokens
+    P, EFH, TH = T * shape.top_k, E * F * H, T * H
     blocks = E * f8_blocks(F) * f8_blocks(H)
     if ws_bytes is None:
         ws_bytes = ws.numel() * ws.element_size()
-    _check(lib().moe_experts_f8(
-        _arg(fn, "gate_stack", gate_stack, E4M3, E * F * H),
-        _arg(fn, "gate_scale", gate_scale, F32, blocks),
-        _arg(fn, "up_stack", up_stack, E4M3, E * F * H),
-        _arg(fn, "up_scale", up_scale, F32, blocks),
-        _arg(fn, "down_stack", down_stack, E4M3, E * H * F),
-        _arg(fn, "down_scale", down_scale, F32, blocks), ctypes.byref(shape), xtype,
-        _arg(fn, "x", x, xtype, T * H), _arg(fn, "topk_idx", topk_idx, "i32", P),
-        _arg(fn, "topk_w", topk_w, F32, P), _arg(fn, "residual", residual, xtype, T * H),
-        _arg(fn, "out", out, xtype, T * H), _arg(fn, "ws", ws, None, 0), ws_bytes,
-        _stream(stream)))
+    dev, st = _context(stream)
+    _check((_libh or lib()).moe_experts_f8(
+        _arg(fn, "gate_stack", gate_stack, E4M3, EFH, dev),
+        _arg(fn, "gate_scale", gate_scale, F32, blocks, dev),
+        _arg(fn, "up_stack", up_stack, E4M3, EFH, dev),
+        _arg(fn, "up_scale", up_scale, F32, blocks, dev),
+        _arg(fn, "down_stack", down_stack, E4M3, EFH, dev),
+        _arg(fn, "down_scale", down_scale, F32, blocks, dev), ctypes.byref(shape), xtype,
+        _arg(fn, "x", x, xtype, TH, dev), _arg(fn, "topk_idx", topk_idx, _I32, P, dev),
+        _arg(fn, "topk_w", topk_w, F32, P, dev), _arg(fn, "residual", residual, xtype, TH, dev),
+        _arg(fn, "out", out, xtype, TH, dev), _arg(fn, "ws", ws, None, 0, dev), ws_bytes, st))
 
 
 # qmoe_set_exec_mode
