@@ -143,14 +143,21 @@ template <class C>
 static qmoe_status launch_pairs(const Gmm& g, const DevInfo& d, cudaStream_t st) {
     const int64_t tiles = gmm::max_tiles(g.p.M, g.p.E, C::NT, (g.p.nb + 1) / 2);
     const int pairs = static_cast<int>(tiles < d.sms / 2 ? tiles : d.sms / 2);
-    return launch_gmm<C>(gmm::gmm_pair_kernel<C>, gmm::P_THREADS, false, g, 2, pairs, d, st);
+    return launch_gmm<C>(gmm::gmm_pair_kernel<C>, C::THREADS, false, g, 2, pairs, d, st);
 }
 
 template <bool F8>
 static qmoe_status run_gmm_kind(Gmm& g, const DevInfo& d, cudaStream_t st) {
     if (few_rows(g.p)) return launch_few<gmm::Cfg<F8, 8, false>>(g, d, st);
     g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
-    return launch_pairs<gmm::PairCfg<F8, F8 ? 192 : 256, F8 ? 6 : 5, false>>(g, d, st);
+    if constexpr (F8) {
+        const int64_t groups = g.p.M < g.p.E ? g.p.M : g.p.E;
+        return g.p.M <= 128 * groups
+                   ? launch_pairs<gmm::PairCfg<true, 128, 7, false, 4>>(g, d, st)
+                   : launch_pairs<gmm::PairCfg<true, 192, 6, false, 3>>(g, d, st);
+    } else {
+        return launch_pairs<gmm::PairCfg<false, 256, 5, false, 3>>(g, d, st);
+    }
 }
 
 static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
@@ -168,7 +175,7 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
         if (g.W2) {
             if (few_rows(g.p)) return launch_few<gmm::Cfg<true, 5, true>>(g, d, st);
             g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
-            return launch_pairs<gmm::PairCfg<true, 96, 5, true>>(g, d, st);
+            return launch_pairs<gmm::PairCfg<true, 96, 5, true, 3>>(g, d, st);
         }
         return run_gmm_kind<true>(g, d, st);
     }

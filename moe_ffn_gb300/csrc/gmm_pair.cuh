@@ -24,9 +24,13 @@
 // registers: 64 sums, a fragment of 32 values and its scales without spilling
 // take 512 threads (any spill in these loops cost 15 to 30 percent).
 //
-// Roles (512 threads): warps 0 and 2 load, warp 1 (of the first CTA)
-// issues the MMAs, warp 3 stages scale products, warps 4-15 are the epilogue: warp w reads
-// lanes 32 (w % 4) .. + 31 and two runs of 32 columns, 96 apart (SwiGLU form:
+// So a wide tile with few epilogue warps is for many rows per group; where
+// groups fill at most 128 columns, four buffers and sixteen warps are faster
+// (64 groups of 64 rows, 1024 x 2048: 34 against 39 us).
+//
+// Roles: warps 0 and 2 load, warp 1 (of the first CTA)
+// issues the MMAs, warp 3 stages scale products, the warps from 4 on are the epilogue: warp w reads
+// lanes 32 (w % 4) .. + 31 and up to two runs of 32 columns (SwiGLU form:
 // the same run of gate and of up).
 #pragma once
 #include "gmm.cuh"
@@ -34,17 +38,23 @@
 namespace qmoe {
 namespace gmm {
 
-constexpr int P_CG = 3;            // runs of columns in flight, one per four warps
-constexpr int P_EPI = 4 * P_CG;    // epilogue warps
-constexpr int P_THREADS = 128 + 32 * P_EPI;
-constexpr int P_CH = 32;           // columns per run
-// registers per thread: 128 x 80 + 384 x 144 = 65,536, the launch's 512 x 128
-constexpr int P_REGS_LOAD = 80, P_REGS_EPI = 144;
+constexpr int P_CH = 32;  // columns per run
 
-template <bool F8_, int NT_, int NST_, bool GU_>
+// Configuration of one instantiation.
+//   F8     e4m3 operands with scales (else 16-bit)
+//   NT     token tile (columns)
+//   NST    pipeline stages
+//   GU     two weight stacks (gate, up) and the SwiGLU + e4m3 epilogue
+//   CG     runs of columns in flight, one per four epilogue warps
+template <bool F8_, int NT_, int NST_, bool GU_, int CG_>
 struct PairCfg {
     static constexpr bool F8 = F8_, GU = GU_;
-    static constexpr int NT = NT_, NST = NST_;
+    static constexpr int NT = NT_, NST = NST_, CG = CG_;
+    static constexpr int EPI = 4 * CG;  // epilogue warps
+    static constexpr int THREADS = 128 + 32 * EPI;
+    // registers per thread: 128 x 80 + 384 x 144 of the launch's 512 x 128, or
+    // 128 x 64 + 512 x 104 of its 640 x 96
+    static constexpr int REGS_LOAD = CG == 3 ? 80 : 64, REGS_EPI = CG == 3 ? 144 : 104;
     static constexpr int NA = GU ? 2 : 1;
     static constexpr int BOX = NT % 64 ? 16 : 32;  // token rows per TMA box; divides NT / 2
     static constexpr int A_BYTES = TILE_W * KBLK;
@@ -57,14 +67,15 @@ struct PairCfg {
     static constexpr int OUT_BYTES = GU ? 1024 : 2048;
     static constexpr int O_SC = NST * STAGE;
     static constexpr int O_OUT = O_SC + (F8 ? SC_RING * SC_STAGE * 4 : 0);
-    static constexpr int O_AMAX = O_OUT + P_EPI * OUT_BYTES;
+    static constexpr int O_AMAX = O_OUT + EPI * OUT_BYTES;
     static constexpr int O_BAR = O_AMAX + (GU ? 2 * 4 * NT * 4 : 0);
     static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1;
     static constexpr int O_TAB = O_BAR + (N_BAR + 1) * 8;
     static constexpr int smem(int E) { return 1024 + O_TAB + (3 * E + 4) * 4; }
     static_assert(TM_BUF * NBUF <= TM_COLS && STAGE % 1024 == 0, "tile shape");
     static_assert((NT / 2) % BOX == 0, "boxes fill a stage exactly");
-    static_assert(!F8 || TM_BUF <= 2 * P_CG * P_CH, "at most two runs per warp");
+    static_assert(!F8 || TM_BUF <= 2 * CG * P_CH, "at most two runs per warp");
+    static_assert(CG == 3 || CG == 4, "register shares");
     static_assert(NT % P_CH == 0, "whole runs");
 };
 
@@ -151,7 +162,7 @@ __device__ __forceinline__ void store_run(const Params& p, uint8_t* stage, const
 }
 
 template <class C>
-__global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     gmm_pair_kernel(const Params p, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_w2,
                     const __grid_constant__ CUtensorMap tm_x) {
@@ -184,11 +195,11 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         for (int i = 0; i < SC_RING; ++i) {
             mbar_init(&sc_full[i], 1);
-            mbar_init(&sc_empty[i], P_EPI);
+            mbar_init(&sc_empty[i], C::EPI);
         }
         for (int i = 0; i < C::NBUF; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 2 * P_EPI);
+            mbar_init(&acc_empty[i], 2 * C::EPI);
         }
         mbar_init(mma_done, 1);
         fence_barrier_init();
@@ -207,7 +218,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp < 4) {
-        regs_dec<P_REGS_LOAD>();
+        regs_dec<C::REGS_LOAD>();
         if (warp == 0 || warp == 2) {
             // ------------------------------------------------------ loads
             // warp 0 the weights, warp 2 the token rows: one warp issuing both
@@ -380,7 +391,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
     } else {
         // ------------------------------------------------------- epilogue
-        regs_inc<P_REGS_EPI>();
+        regs_inc<C::REGS_EPI>();
         const int quad = warp & 3, cg = (warp - 4) >> 2;
         const int lr = lane >> 2, lc = lane & 3;  // fragment row and column
         const uint32_t acc_empty0 = cluster_addr(acc_empty, 0);
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         const int run_col = cg * P_CH;
         const uint32_t tm_run = tmem + (static_cast<uint32_t>(quad * 32) << 16) + run_col;
         // column distance of the two runs, in the buffer and in the ring
-        constexpr int R2 = C::GU ? C::NT : P_CG * P_CH;
+        constexpr int R2 = C::GU ? C::NT : C::CG * P_CH;
         uint8_t* stage = base + C::O_OUT + (warp - 4) * C::OUT_BYTES;
         uint32_t ab = C::NBUF - 1, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
@@ -422,12 +433,13 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
             } else {
                 // acc[run][row half][2 i + j]: weight row 16 half + 8 j + lr of this warp's
                 // 32, column 4 i + lc of the run
-                float acc[2][2][16];
+                constexpr int RUNS = C::GU || C::NT > C::CG * P_CH ? 2 : 1;
+                float acc[RUNS][2][16];
 #pragma unroll
-                for (int c = 0; c < 64; ++c) acc[c >> 5][(c >> 4) & 1][c & 15] = 0.f;
+                for (int c = 0; c < RUNS * 32; ++c) acc[c >> 5][(c >> 4) & 1][c & 15] = 0.f;
                 const int np = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E).np;
                 const int runs = C::GU ? (run_col < np ? 2 : 0)
-                                       : (run_col < np) + (run_col + R2 < np);
+                                       : (run_col < np) + (RUNS > 1 && run_col + R2 < np);
                 const float* run = ring + run_col + lc * 8;
 #pragma unroll 1
                 for (int k0 = 0; k0 < p.kb; k0 += SC_BLK) {
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                         umma::fence_after_sync();
                         const uint32_t src = tm_run + ab * C::TM_BUF;
 #pragma unroll
-                        for (int q = 0; q < 2; ++q)
+                        for (int q = 0; q < RUNS; ++q)
                             if (q < runs) {
                                 Frag f;
                                 frag_load(src + q * R2, f);
@@ -486,7 +498,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                 const int n0 = nbi * TILE_W + quad * 32;  // first of this warp's weight rows
                 if constexpr (!C::GU) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                    for (int q = 0; q < RUNS; ++q)
                         store_run(p, stage, acc[q], lane, w.row0 + run_col + q * R2,
                                   w.nv - run_col - q * R2, n0);
                 } else {
@@ -500,7 +512,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                             for (int r = 0; r < 4; ++r) {
                                 const float g = acc[0][r >> 1][2 * i + (r & 1)];
-                                const float u = acc[1][r >> 1][2 * i + (r & 1)];
+                                const float u = acc[RUNS - 1][r >> 1][2 * i + (r & 1)];
                                 const float v = swiglu(g, u);
                                 acc[0][r >> 1][2 * i + (r & 1)] = v;
                                 m = max(m, finite_abs_bits(v));
