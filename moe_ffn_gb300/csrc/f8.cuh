@@ -33,15 +33,18 @@ __device__ __forceinline__ void f8_scale(uint32_t amax_bits, float* s, float* in
     *inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 }
 
-// Two values to e4m3, round to nearest even: `lo` in the low byte.  The
-// conversion saturates, so infinities are turned into NaN (the only
-// non-finite code) before it.
-__device__ __forceinline__ uint32_t f8_pack2(float lo, float hi) {
-    lo = isinf(lo) ? __int_as_float(0x7FC00000) : lo;
-    hi = isinf(hi) ? __int_as_float(0x7FC00000) : hi;
+// Two values to e4m3, round to nearest even: `lo` in the low byte.  For values
+// without infinities (the conversion saturates them).
+__device__ __forceinline__ uint32_t f8_pack2_finite(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
+}
+// The same for any values: infinities become NaN, the only non-finite code.
+__device__ __forceinline__ uint32_t f8_pack2(float lo, float hi) {
+    lo = isinf(lo) ? __int_as_float(0x7FC00000) : lo;
+    hi = isinf(hi) ? __int_as_float(0x7FC00000) : hi;
+    return f8_pack2_finite(lo, hi);
 }
 
 }  // namespace qmoe

@@ -42,19 +42,86 @@ struct QuantParams {
 };
 constexpr int Q_THREADS = 256;
 
+// Eight consecutive values as they lie in memory.
 template <class T>
-__device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(src));
-        const float4 b = __ldcg(reinterpret_cast<const float4*>(src) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 a = __ldcg(reinterpret_cast<const uint4*>(src));
-        const T* h = reinterpret_cast<const T*>(&a);
+struct Raw8 {
+    uint32_t w[sizeof(T) * 2];
+    __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(h[i]);
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+            const uint4 a = __ldcg(reinterpret_cast<const uint4*>(src) + i);
+            w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+        }
     }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) * 2; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else
+            return to_f32(reinterpret_cast<const T*>(w)[i]);
+    }
+    // The largest magnitude as its type's bits (16-bit values two at a time):
+    // magnitudes order as their bits do, infinities and NaN above the rest.
+    __device__ __forceinline__ uint32_t amax() const {
+        if constexpr (sizeof(T) == 4) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+            return m;
+        } else {
+            uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+            return max(m & 0xFFFFu, m >> 16);
+        }
+    }
+    static __device__ __forceinline__ uint32_t inf() {
+        return sizeof(T) == 4 ? 0x7F800000u : std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    }
+    // f32 bits of a magnitude from its type's
+    static __device__ __forceinline__ uint32_t f32_bits(uint32_t m) {
+        if constexpr (sizeof(T) == 4)
+            return m;
+        else if constexpr (std::is_same<T, __half>::value)
+            return __float_as_uint(
+                __half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+        else
+            return m << 16;
+    }
+};
+
+// Quantises a block held by sixteen lanes, eight values each: this lane's codes
+// and the block's scale.  By a whole warp.
+template <class T>
+__device__ __forceinline__ uint2 quantize8(const Raw8<T>& x, float* scale) {
+    uint32_t m = x.amax();
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float inv;
+    uint2 q;
+    if (!__any_sync(0xffffffffu, m >= Raw8<T>::inf())) {
+        f8_scale(Raw8<T>::f32_bits(m), scale, &inv);
+        q.x = f8_pack2_finite(x.get(0) * inv, x.get(1) * inv) |
+              (f8_pack2_finite(x.get(2) * inv, x.get(3) * inv) << 16);
+        q.y = f8_pack2_finite(x.get(4) * inv, x.get(5) * inv) |
+              (f8_pack2_finite(x.get(6) * inv, x.get(7) * inv) << 16);
+        return q;
+    }
+    // infinities or NaN among the warp's values: the scale is the finite ones'
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(x.get(i)));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    f8_scale(m, scale, &inv);
+    q.x = f8_pack2(x.get(0) * inv, x.get(1) * inv) |
+          (f8_pack2(x.get(2) * inv, x.get(3) * inv) << 16);
+    q.y = f8_pack2(x.get(4) * inv, x.get(5) * inv) |
+          (f8_pack2(x.get(6) * inv, x.get(7) * inv) << 16);
+    return q;
 }
 
 template <class T, bool VEC, int RUN>
@@ -76,36 +143,28 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const QuantParams p
     const int nb = live ? min(RUN, p.nblk - blk0) : 0;
     const int c0 = blk0 * F8_BLOCK + sub * 8;
     const T* src = static_cast<const T*>(p.x) + (live ? row : 0) * p.ldx + c0;
-    float v[RUN][8];
+    Raw8<T> v[RUN];
 #pragma unroll
     for (int b = 0; b < RUN; ++b) {
         const int c = c0 + b * F8_BLOCK;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[b][i] = 0.f;
+        v[b].zero();
         if (b < nb) {
             if constexpr (VEC) {
-                if (c < p.cols) load8(src + b * F8_BLOCK, v[b]);
+                if (c < p.cols) v[b].load(src + b * F8_BLOCK);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (c + i < p.cols) v[b][i] = to_f32(src[b * F8_BLOCK + i]);
+                    if (c + i < p.cols)
+                        reinterpret_cast<T*>(v[b].w)[i] = src[b * F8_BLOCK + i];
             }
         }
     }
 #pragma unroll
     for (int b = 0; b < RUN; ++b) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[b][i]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float s;
+        const uint2 q = quantize8(v[b], &s);
         if (b >= nb) continue;
         const int c = c0 + b * F8_BLOCK;
-        float s, inv;
-        f8_scale(m, &s, &inv);
-        uint2 q;
-        q.x = f8_pack2(v[b][0] * inv, v[b][1] * inv) | (f8_pack2(v[b][2] * inv, v[b][3] * inv) << 16);
-        q.y = f8_pack2(v[b][4] * inv, v[b][5] * inv) | (f8_pack2(v[b][6] * inv, v[b][7] * inv) << 16);
         const int nslot = p.pos ? p.k : 1;
         for (int i = 0; i < nslot; ++i) {
             const int64_t r = p.pos ? __ldg(p.pos + row * p.k + i) : row;
@@ -276,21 +335,12 @@ __global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
     for (int b0 = 0; b0 < p.nblk; b0 += Q_THREADS / 16) {
         const int b = b0 + (tid >> 4);
         const int c = b * F8_BLOCK + sub * 8;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        if (b < p.nblk) load8(src + c, v);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[i]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        Raw8<T> v;
+        v.zero();
+        if (b < p.nblk) v.load(src + c);
+        float s;
+        const uint2 q = quantize8(v, &s);
         if (b >= p.nblk) continue;
-        float s, inv;
-        f8_scale(m, &s, &inv);
-        uint2 q;
-        q.x = f8_pack2(v[0] * inv, v[1] * inv) | (f8_pack2(v[2] * inv, v[3] * inv) << 16);
-        q.y = f8_pack2(v[4] * inv, v[5] * inv) | (f8_pack2(v[6] * inv, v[7] * inv) << 16);
         for (int i = 0; i < p.k; ++i) {
             const int64_t r = s_pos[i];
             if (r < 0) continue;
@@ -309,6 +359,13 @@ __global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
 constexpr int C_THREADS = 128;
 constexpr int C_AHEAD = 4;
 
+template <class T>
+__device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
+    Raw8<T> r;
+    r.load(src);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r.get(i);
+}
 template <class T>
 __device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
     if constexpr (sizeof(T) == 4) {
