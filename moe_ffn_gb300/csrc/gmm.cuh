@@ -147,37 +147,45 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 
 // The groups' tables, by the whole CTA (ends with a barrier): rows [lo, hi) of
 // each group and the tiles before it, the total last.  Offsets are clamped into
-// [0, M], so that no value of theirs forms an address outside x or y.  Every
-// thread loads its groups' offsets first, so the loads cost one latency.
+// [0, M], so that no value of theirs forms an address outside x or y.  A thread
+// per group; the time is one load latency and one scan.
 __device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, int* t_lo,
                                              int* t_hi, int* t_pre) {
-    bool bad = false;
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-        int lo = 0, hi = p.M;
-        if (p.offsets)
-            bad |= !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M, &lo, &hi);
-        t_lo[e] = lo;
-        t_hi[e] = hi;
-    }
-    if (bad) record_error(p.err, DEV_GMM_OFFSETS);
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int total = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int n = e < p.E ? group_tiles(t_hi[e] - t_lo[e], nt, nb) : 0;
-            int s = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += v;
-            }
-            if (e < p.E) t_pre[e] = total + s - n;
-            total += __shfl_sync(0xffffffffu, s, 31);
+    __shared__ int wsum[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int total = 0;
+    for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
+        const int e = e0 + tid;
+        int n = 0;
+        if (e < p.E) {
+            int lo = 0, hi = p.M;
+            if (p.offsets &&
+                !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M, &lo, &hi))
+                record_error(p.err, DEV_GMM_OFFSETS);
+            t_lo[e] = lo;
+            t_hi[e] = hi;
+            n = group_tiles(hi - lo, nt, nb);
         }
-        if (lane == 0) t_pre[p.E] = total;
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += v;
+        }
+        if (lane == 31) wsum[warp] = s;
+        __syncthreads();
+        const int nw = static_cast<int>(blockDim.x >> 5);
+        int before = 0, all = 0;
+        for (int w = 0; w < nw; ++w) {
+            const int v = wsum[w];
+            before += w < warp ? v : 0;
+            all += v;
+        }
+        if (e < p.E) t_pre[e] = total + before + s - n;
+        total += all;
+        if (e0 + static_cast<int>(blockDim.x) < p.E) __syncthreads();  // wsum is used again
     }
+    if (tid == 0) t_pre[p.E] = total;
     __syncthreads();
 }
 
@@ -239,10 +247,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     // A cluster takes tiles first, first + step, ...; a cluster of more than one
     // CTA takes one tile, each of its CTAs a share of K.
+    // The cluster size is a power of two.
     const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
-    const int first = blockIdx.x / ranks;
+    const int lg = 31 - __clz(ranks);
+    const int first = blockIdx.x >> lg;
     const int step = ranks > 1 ? max(tiles, 1) : gridDim.x;
-    const int kbeg = rank * p.kb / ranks, kend = (rank + 1) * p.kb / ranks;
+    const int kbeg = (rank * p.kb) >> lg, kend = ((rank + 1) * p.kb) >> lg;
+    Tile w0 = {};  // the first tile, for every role and the sum over the cluster
+    if (first < tiles) w0 = tile_at(first, C::NT, 16, t_lo, t_hi, t_pre, p.E);
 
     if (warp == 0) {
         // ---------------------------------------------------------- loads
@@ -250,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ph = 1;  // parity of the wait for a free stage
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
-            const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             const int boxes = (w.np + C::BOX - 1) / C::BOX;
             for (int kb = kbeg; kb < kend; ++kb, ++it) {
                 // (before any use of a stage the wait passes at once)
@@ -292,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t da0 = umma::desc_sw128(smem_u32(base));
         const uint64_t db0 = umma::desc_sw128(smem_u32(base) + C::NA * C::A_BYTES);
         for (int t = first; t < tiles && ok; t += step) {
-            const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
             for (int kb = kbeg; kb < kend; ++kb) {
                 const bool fresh = C::F8 || kb == kbeg;  // a new accumulator buffer
@@ -348,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int ch = 0;
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
-                const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+                const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + w.nbi) * p.kb;
                 for (int k0 = kbeg; k0 < kend; k0 += SC_BLK, ++ch) {
                     float v[RPT][SC_BLK], g[C::NA][SC_BLK];
@@ -401,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ab = 0, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step, par ^= 1) {
-            const Tile w = tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             float acc[C::NA][C::CH];
 #pragma unroll
             for (int a = 0; a < C::NA; ++a)
@@ -523,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // a thread one weight row
         cluster_sync();
         if (warp >= 4 && first < tiles) {
-            const Tile w = tile_at(first, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const Tile w = w0;
             const int half = (warp - 4) >> 2, r = (tid - 128) & 127;
             const int nr = w.nbi * TILE_W + r;
             for (int j0 = 0; j0 < w.nv; j0 += 2 * ranks) {

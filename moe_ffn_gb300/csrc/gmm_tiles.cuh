@@ -45,11 +45,16 @@ QMOE_HD Tile tile_at(int t, int nt, int step, const int* lo, const int* hi, cons
     Tile r;
     r.e = a;
     const int rows = hi[a] - lo[a];
-    const int c = (rows - 1) / nt + 1;
     const int local = t - pre[a];
-    r.nbi = local / c;
-    const int ts = ((rows - 1) / c + step) & ~(step - 1);
-    r.row0 = lo[a] + (local - r.nbi * c) * ts;
+    int ts = nt;
+    r.nbi = local;
+    r.row0 = lo[a];
+    if (rows > nt) {  // (the divisions only where a group has several token tiles)
+        const int c = (rows - 1) / nt + 1;
+        ts = ((rows - 1) / c + step) & ~(step - 1);
+        r.nbi = local / c;
+        r.row0 += (local - r.nbi * c) * ts;
+    }
     r.nv = hi[a] - r.row0 < ts ? hi[a] - r.row0 : ts;
     r.np = (r.nv + step - 1) & ~(step - 1);
     return r;
