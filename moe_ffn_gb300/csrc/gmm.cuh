@@ -302,35 +302,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ph = 0, ab = 0, aph = 1;  // stage and accumulator phases
         bool ok = true;
         const uint64_t da0 = umma::desc_sw128(smem_u32(base));
-        const uint64_t db0 = umma::desc_sw128(smem_u32(base) + C::NA * C::A_BYTES);
+        const uint32_t hi = static_cast<uint32_t>(da0 >> 32), lo0 = static_cast<uint32_t>(da0);
+        uint32_t lo = lo0;  // the stage's descriptor, low word
         for (int t = first; t < tiles && ok; t += step) {
             const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
+#pragma unroll 1
             for (int kb = kbeg; kb < kend; ++kb) {
                 const bool fresh = C::F8 || kb == kbeg;  // a new accumulator buffer
-                if ((fresh && !mbar_wait_spin(&acc_empty[ab], aph, p.err, DEV_GMM_TIMEOUT)) ||
-                    !mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT)) {
+                const bool last = C::F8 || kb == kend - 1;
+                // both waits tried before either is acted on
+                bool r0 = mbar_try_wait(&full[s], ph), r1 = true;
+                if (fresh) r1 = mbar_try_wait(&acc_empty[ab], aph);
+                if (!r0) r0 = mbar_wait_spin(&full[s], ph, p.err, DEV_GMM_TIMEOUT);
+                if (!r1) r1 = mbar_wait_spin(&acc_empty[ab], aph, p.err, DEV_GMM_TIMEOUT);
+                if (!(r0 && r1)) {
                     ok = false;
                     break;
                 }
                 umma::fence_after_sync();
-                const bool last = C::F8 || kb == kend - 1;
                 if (elect_one()) {
-                    // 32 bytes of K further: the descriptors' address field + 2
-                    const uint64_t da = da0 + s * (C::STAGE >> 4);
-                    const uint64_t db = db0 + s * (C::STAGE >> 4);
                     const uint32_t d = tmem + ab * C::TM_BUF;
+                    // 32 bytes of K further: the descriptors' address field + 2
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int a = 0; a < C::NA; ++a) {
-                            const uint32_t acc = (!fresh || j > 0) ? 1u : 0u;
-                            const uint64_t daj = da + a * (C::A_BYTES >> 4) + 2 * j;
-                            if constexpr (C::F8)
-                                umma::mma_f8(d + a * C::NT, daj, db + 2 * j, idesc, acc);
-                            else
-                                umma::mma_f16(d + a * C::NT, daj, db + 2 * j, idesc, acc);
-                        }
+                        for (int a = 0; a < C::NA; ++a)
+                            umma::mma_one<C::F8>(d + a * C::NT,
+                                                 lo + a * (C::A_BYTES >> 4) + 2 * j,
+                                                 lo + C::NA * (C::A_BYTES >> 4) + 2 * j, hi, idesc,
+                                                 (!fresh || j > 0) ? 1u : 0u);
                     umma::commit(&empty[s]);
                     if (last) umma::commit(&acc_full[ab]);
                 }
@@ -339,9 +340,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ab = 0;
                     aph ^= 1;
                 }
+                lo += C::STAGE >> 4;
                 if (++s == C::NST) {
                     s = 0;
                     ph ^= 1;
+                    lo = lo0;
                 }
             }
         }

@@ -66,16 +66,6 @@ __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t a, uint64_t b
         : "memory");
 }
 
-// 8-bit float operands (K = 32 per instruction, 32 bytes of every row).
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // Arrive on `bar` once every MMA issued so far by this thread has completed.
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile(
@@ -87,25 +77,33 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 // The same over a CTA pair (cta_group::2), issued by the pair's first CTA:
 // each CTA holds half of A's rows and half of B's, at the same shared-memory
 // offsets, and its half of D's rows in its own tensor memory.
-// Descriptors by their low words; the high word is common.
+// MMA over one CTA or a pair, 16-bit (the instruction descriptor says which) or
+// 8-bit operands; descriptors by their low words, the high word is common.
+#define QMOE_MMA(GROUP, KIND)                                                           \
+    asm volatile(                                                                       \
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"               \
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"                              \
+        "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a, b, %4, p;\n\t}" ::"r"( \
+            d_tmem),                                                                    \
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)                      \
+        : "memory")
+template <bool F8>
+__device__ __forceinline__ void mma_one(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                        uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (F8)
+        QMOE_MMA("1", "f8f6f4");
+    else
+        QMOE_MMA("1", "f16");
+}
 template <bool F8>
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                          uint32_t hi, uint32_t idesc, uint32_t accumulate) {
     if constexpr (F8)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
-            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
-            : "memory");
+        QMOE_MMA("2", "f8f6f4");
     else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
-            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
-            : "memory");
+        QMOE_MMA("2", "f16");
 }
+#undef QMOE_MMA
 // Arrive on the barrier at `bar`'s offset in both CTAs of the pair.
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
     asm volatile(
