@@ -132,11 +132,16 @@ static qmoe_status launch_few(const Gmm& g, const DevInfo& d, cudaStream_t st) {
     const int clusters = static_cast<int>(tiles < d.sms ? tiles : d.sms);
     return launch_gmm<C>(gmm::gmm_kernel<C>, gmm::THREADS, true, g, ranks, clusters, d, st);
 }
-// Rows per group up to which that kernel is used: at 16 a tile of 32 columns
-// holds most groups.
-static bool few_rows(const gmm::Params& p) {
+// Whether that kernel is used: up to 16 rows per group, where its tile of 32
+// columns holds most groups (32 without groups), and beyond that as long as its
+// small tiles still fit the SMs at once, for the other kernel's 256-row tiles
+// then leave most of them idle.  2048 x 2048 e4m3, 33 / 256 rows: 6.4 / 8.5 us
+// against 9.8 / 13.2; 4096 x 4096 (32 row tiles), 128 rows: 12.8 against 16.9,
+// 192 rows (192 tiles): 22.3 against 21.9.
+static bool few_rows(const gmm::Params& p, int sms) {
     const int64_t groups = p.M < p.E ? p.M : p.E;
-    return p.M <= (p.offsets ? 16 * groups : 32);
+    return p.M <= (p.offsets ? 16 * groups : 32) ||
+           gmm::max_tiles(p.M, p.E, 32, p.nb) <= sms;
 }
 // One CTA pair per two SMs, or as many as there can be tiles.
 template <class C>
@@ -148,7 +153,7 @@ static qmoe_status launch_pairs(const Gmm& g, const DevInfo& d, cudaStream_t st)
 
 template <bool F8>
 static qmoe_status run_gmm_kind(Gmm& g, const DevInfo& d, cudaStream_t st) {
-    if (few_rows(g.p)) return launch_few<gmm::Cfg<F8, 8, false>>(g, d, st);
+    if (few_rows(g.p, d.sms)) return launch_few<gmm::Cfg<F8, 8, false>>(g, d, st);
     g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
     if constexpr (F8) {
         const int64_t groups = g.p.M < g.p.E ? g.p.M : g.p.E;
@@ -173,7 +178,7 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
                 (static_cast<uint32_t>(gmm::TILE_W >> 4) << 24);
     if (g.type == QMOE_E4M3) {
         if (g.W2) {
-            if (few_rows(g.p)) return launch_few<gmm::Cfg<true, 5, true>>(g, d, st);
+            if (few_rows(g.p, d.sms)) return launch_few<gmm::Cfg<true, 5, true>>(g, d, st);
             g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
             return launch_pairs<gmm::PairCfg<true, 96, 5, true, 3>>(g, d, st);
         }

@@ -60,11 +60,11 @@ QMOE_HD Tile tile_at(int t, int nt, int step, const int* lo, const int* hi, cons
     return r;
 }
 
-// Most tiles that M rows in E groups can make: every started token tile of
-// every group that has rows.
+// Most tiles that M rows in E groups can make: sum of ceil(r / nt) over at most
+// min(M, E) groups that have rows, each at most (r + nt - 1) / nt.
 QMOE_HD int64_t max_tiles(int64_t M, int E, int nt, int nb) {
     const int64_t groups = M < E ? M : E;
-    return (M / nt + groups) * nb;
+    return (M + groups * (nt - 1)) / nt * nb;
 }
 
 }  // namespace gmm
