@@ -585,3 +585,95 @@ def test_binding_checks_tensors(qm):
     with pytest.raises(qm.QmoeError, match="dtype"):
         qm.mm_grouped(qm.E4M3, w, wsc, 1, 100, 256, q, s, 4, torch.zeros(2, device="cuda"),
                       qm.F32, y)
+
+
+# ----------------------------------------------------- beyond 32-bit offsets
+def test_f8_mm_output_beyond_2_31_elements(qm):
+    """70,000 x 40,000 outputs (2.8e9 elements): sampled rows, the last among
+    them, against the 64-bit form."""
+    import torch
+    m, n, k = 70000, 40000, 32
+    g = np.random.default_rng(61)
+    xq, xs, wq, ws, xv, wv = f8_operands(g, m, n, k)
+    y = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    qm.f8_mm(dev(wq[0]), dev(ws[0]), n, k, dev(xq), dev(xs), m, qm.BF16, y)
+    assert qm.device_status() == qm.OK
+    rows = [0, 1, 53686, 53687, 53688, 69998, 69999]  # 53687 * 40000 passes 2^31
+    want, err = ref.product(xv[rows], wv[0], ref.f8_terms(k))
+    check(f64(y[rows]), want, ref.rounded(want, err, "bf16"), "rows")
+
+
+@pytest.mark.parametrize("kind", ["f8", "bf16"])
+def test_mm_grouped_weights_beyond_2_31_elements(qm, kind):
+    """A stack of 2.4e9 elements: only the last group's matrix is not zero."""
+    import torch
+    e, n, k, m = 36, 8192, 8192, 72
+    g = np.random.default_rng(62)
+    off = np.arange(0, 2 * e + 1, 2).astype(np.int32)
+    y = out_tensor(m, n, torch.float32)
+    if kind == "f8":
+        xq, xs, wq, ws, xv, wv = f8_operands(g, m, 256, k)
+        W = torch.zeros(e, n, k, dtype=torch.uint8, device="cuda")
+        S = torch.ones(e, n // 128, k // 128, device="cuda")
+        W[-1, -256:] = dev(wq[0])
+        S[-1, -2:] = dev(ws[0])
+        qm.mm_grouped(qm.E4M3, W, S, e, n, k, dev(xq), dev(xs), m, dev(off), qm.F32, y)
+        terms, w = ref.f8_terms(k), wv[0]
+    else:
+        x, w16, xv, wv = wide_operands(g, m, 256, k, 1, "bf16")
+        W = torch.zeros(e, n, k, dtype=torch.bfloat16, device="cuda")
+        W[-1, -256:] = w16[0].cuda()
+        qm.mm_grouped(qm.BF16, W, None, e, n, k, x.cuda(), None, m, dev(off), qm.F32, y)
+        terms, w = ref.wide_terms(k), wv[0]
+    assert qm.device_status() == qm.OK
+    assert (y[:-2] == 0).all() and (y[-2:, :-256] == 0).all()
+    want, err = ref.product(xv[-2:], w, terms)
+    check(f64(y[-2:, -256:]), want, ref.rounded(want, err, "f32"), "last group")
+
+
+def test_moe_many_tokens_repeat_the_first(qm):
+    """140,000 tokens (the activations' rows pass 2^31 bytes) that repeat 64
+    tokens: every repeat has the bits of the first."""
+    import torch
+    dims = (64, 2048, 128, 8, 8)
+    g, x, residual, idx, w, stacks = moe_case(63, *dims, "bf16")
+    reps = 2188
+    T = 64 * reps
+    st = dev_stacks(stacks)
+    X, I, W, R = (t.repeat(reps, 1) for t in (x.cuda(), dev(idx), dev(w), residual.cuda()))
+    out = run_moe(qm, (T,) + dims[1:], "bf16", X, I, W, st, R)
+    assert qm.device_status() == qm.OK
+    first = out[:64]
+    assert (out.view(reps, 64, -1) == first).all()
+    want, err = moe_reference(x.double().numpy()[:8], idx[:8], w[:8], [s[2] for s in stacks],
+                              residual.double().numpy()[:8], "bf16")
+    check(f64(first[:8]), want, ref.rounded(want, err, "bf16"), "moe")
+
+
+def test_first_call_may_be_captured():
+    """A process whose first call of each function is inside a capture."""
+    import subprocess
+    import sys
+    code = """
+import torch, moe_ffn_gb300 as qm
+x = torch.randn(4, 256, device="cuda", dtype=torch.bfloat16)
+q = torch.empty(4, 256, dtype=torch.uint8, device="cuda"); s = torch.empty(4, 2, device="cuda")
+W = torch.full((128, 256), 0x38, dtype=torch.uint8, device="cuda"); S = torch.ones(1, 2, device="cuda")
+y = torch.empty(4, 128, device="cuda")
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    qm.f8_quantize(qm.BF16, x, 4, 256, q, s)
+    qm.f8_mm(W, S, 128, 256, q, s, 4, qm.F32, y)
+g.replay()
+torch.cuda.synchronize()
+want = (q.view(torch.float8_e4m3fn).float() * s.repeat_interleave(128, 1)).sum(1)
+assert torch.allclose(y, want[:, None].expand(4, 128), rtol=1e-4, atol=1e-4)
+assert qm.device_status() == qm.OK
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
