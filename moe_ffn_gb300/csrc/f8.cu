@@ -78,7 +78,7 @@ static qmoe_status launch_gmm(Kern kern, int threads, bool shaped, const Gmm& g,
                               int clusters, const DevInfo& d, cudaStream_t st) {
     const int smem = C::smem(g.p.E);
     constexpr int most = C::smem(C::GU ? MAX_F8_EXPERTS : MAX_GROUPS);
-    static_assert(most <= 232448, "shared memory of one CTA");
+    static_assert(most + 512 <= 232448, "shared memory of one CTA, static arrays included");
     static std::atomic<int> configured[64];
     if (smem > configured[d.dev].load()) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,

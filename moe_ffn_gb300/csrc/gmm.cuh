@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int step = ranks > 1 ? max(tiles, 1) : gridDim.x;
     const int kbeg = (rank * p.kb) >> lg, kend = ((rank + 1) * p.kb) >> lg;
     Tile w0 = {};  // the first tile, for every role and the sum over the cluster
-    if (first < tiles) w0 = tile_at(first, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+    if (first < tiles) w0 = tile_at_warp(first, C::NT, 16, t_lo, t_hi, t_pre, p.E);
 
     if (warp == 0) {
         // ---------------------------------------------------------- loads
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ph = 1;  // parity of the wait for a free stage
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
-            const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const Tile w = t == first ? w0 : tile_at_warp(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             const int boxes = (w.np + C::BOX - 1) / C::BOX;
             for (int kb = kbeg; kb < kend; ++kb, ++it) {
                 // (before any use of a stage the wait passes at once)
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t hi = static_cast<uint32_t>(da0 >> 32), lo0 = static_cast<uint32_t>(da0);
         uint32_t lo = lo0;  // the stage's descriptor, low word
         for (int t = first; t < tiles && ok; t += step) {
-            const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const Tile w = t == first ? w0 : tile_at_warp(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
 #pragma unroll 1
             for (int kb = kbeg; kb < kend; ++kb) {
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int ch = 0;
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
-                const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+                const Tile w = t == first ? w0 : tile_at_warp(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + w.nbi) * p.kb;
                 for (int k0 = kbeg; k0 < kend; k0 += SC_BLK, ++ch) {
                     float v[RPT][SC_BLK], g[C::NA][SC_BLK];
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ab = 0, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step, par ^= 1) {
-            const Tile w = t == first ? w0 : tile_at(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
+            const Tile w = t == first ? w0 : tile_at_warp(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             float acc[C::NA][C::CH];
 #pragma unroll
             for (int a = 0; a < C::NA; ++a)

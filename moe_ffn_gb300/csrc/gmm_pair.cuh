@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     int* t_hi = t_lo + p.E;
     int* t_pre = t_hi + p.E;
 
+    __shared__ int notes[C::EPI][3];  // an epilogue warp's tile
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t rank = cluster_rank();
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
             bool ok = true;
             const uint32_t full0 = cluster_addr(full, 0);
             for (int t = first; t < tiles && ok; t += step) {
-                const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
+                const Tile w = tile_at_warp(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const int half = w.np >> 1;
                 const int boxes = (half + C::BOX - 1) / C::BOX;
                 const uint32_t bytes = 2 * (C::NA * C::A_BYTES + boxes * C::BOX * KBLK);
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
             const uint32_t hi = static_cast<uint32_t>(da0 >> 32), lo0 = static_cast<uint32_t>(da0);
             uint32_t lo = lo0;  // the stage's descriptor, low word
             for (int t = first; t < tiles && ok; t += step) {
-                const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
+                const Tile w = tile_at_warp(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
                 if constexpr (!C::F8) ab = (ab + 1) % C::NBUF;
 #pragma unroll 1
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
             uint32_t ph = 1;
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
-                const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
+                const Tile w = tile_at_warp(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const int nbi = 2 * w.nbi + static_cast<int>(rank);
                 const bool rows_in = nbi < p.nb;  // the last weight tile's second half may be empty
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + nbi) * p.kb;
@@ -401,11 +402,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
         // column distance of the two runs, in the buffer and in the ring
         constexpr int R2 = C::GU ? C::NT : C::CG * P_CH;
         uint8_t* stage = base + C::O_OUT + (warp - 4) * C::OUT_BYTES;
+        volatile int* note = notes[warp - 4];
         uint32_t ab = C::NBUF - 1, aph = 0, cs = 0, cph = 0, par = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step, par ^= 1) {
             if constexpr (!C::F8) {
-                const Tile w = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
+                const Tile w = tile_at_warp(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const int n0 = (2 * w.nbi + static_cast<int>(rank)) * TILE_W + quad * 32;
                 ab = (ab + 1) % C::NBUF;
                 ok = mbar_wait_spin(&acc_full[ab], (aph >> ab) & 1, p.err, DEV_GMM_TIMEOUT);
@@ -437,7 +439,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
                 float acc[RUNS][2][16];
 #pragma unroll
                 for (int c = 0; c < RUNS * 32; ++c) acc[c >> 5][(c >> 4) & 1][c & 15] = 0.f;
-                const int np = tile_at(t, C::NT, 32, t_lo, t_hi, t_pre, p.E).np;
+                // (the tile's fields wait in shared memory: they would take registers
+                // through the K loop)
+                int np;
+                {
+                    const Tile w = tile_at_warp(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
+                    np = w.np;
+                    if (lane == 0) {
+                        note[0] = w.nbi;
+                        note[1] = w.row0;
+                        note[2] = w.nv;
+                    }
+                }
                 const int runs = C::GU ? (run_col < np ? 2 : 0)
                                        : (run_col < np) + (RUNS > 1 && run_col + R2 < np);
                 const float* run = ring + run_col + lc * 8;
@@ -489,11 +502,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
                 if (!ok) break;
-                // the tile, from an index the compiler cannot trace: its fields would
-                // take registers through the K loop
-                int t_again = t;
-                asm volatile("" : "+r"(t_again));
-                const Tile w = tile_at(t_again, C::NT, 32, t_lo, t_hi, t_pre, p.E);
+                __syncwarp();
+                const Tile w = {0, note[0], note[1], note[2], 0};
                 const int nbi = 2 * w.nbi + static_cast<int>(rank);
                 const int n0 = nbi * TILE_W + quad * 32;  // first of this warp's weight rows
                 if constexpr (!C::GU) {
