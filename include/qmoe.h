@@ -348,7 +348,7 @@ qmoe_status f8_quantize(int xtype, const void* x, int64_t rows, int64_t cols, in
  *            between rows are left as they were
  * y must not overlap an input.
  * Errors as f8_quantize; QMOE_ERR_TIMEOUT from qmoe_device_status if a device
- * wait ran out. */
+ * wait ran out (the output is then not valid: tiles are missing or NaN). */
 qmoe_status f8_mm(const void* W, const float* w_scale, int64_t rows, int64_t cols, const void* x,
                   const float* x_scale, int64_t n_tokens, int64_t ldx, int ytype, void* y,
                   int64_t ldy, void* stream);
@@ -430,7 +430,9 @@ qmoe_status qmoe_set_exec_mode(int mode);
  * and, if skip_arrive_cta >= 0, that CTA of the cooperative layer kernels
  * never arrives at their grid barriers, so the other CTAs' waits run out:
  * the kernels then record QMOE_ERR_TIMEOUT (qmoe_device_status) and return
- * without writing the layer's output.  (-1, 0) restores normal operation.
+ * without writing the layer's output.  In f8_mm, mm_grouped and
+ * moe_experts_f8 that CTA loads nothing, so the waits for its operands run
+ * out.  (-1, 0) restores normal operation.
  * Synchronises the device before writing the setting.  Errors: CUDA,
  * UNSUPPORTED (not sm_103), INVALID_ARGUMENT (skip_arrive_cta < -1).  The
  * pages have no counterpart; their CudaError model ("refuse, never compute

@@ -24,6 +24,11 @@
 // distributed shared memory, in rank order.  gmm_pair.cuh has the kernel for
 // many rows.
 //
+// Measured: 1 x 4096 x 4096 e4m3 6.5 us (fixed latency: about 2,500 clocks to
+// the first copy, 1,300 for its data, 3,000 from the last MMA to the end); eight
+// bf16 experts of one row, 768 x 2048: 8.4 us, 3.0 TB/s; 128 rows in 64 groups,
+// 2048 x 2048 bf16: 82 us, 6.5 TB/s.
+//
 // Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs,
 // warps 2-3 stage the scale products, warps 4-11 are the epilogue: warp w
 // reads TMEM lanes 32 (w % 4) .. +31, and the two groups of four warps take
@@ -90,7 +95,7 @@ struct Cfg {
     static constexpr int O_PART = O_SC + (F8 ? SC_RING * SC_STAGE * 4 : 0);
     static constexpr int O_AMAX = O_PART + NA * NT * TILE_W * 4;
     static constexpr int O_BAR = O_AMAX + (GU ? 2 * 4 * NT * 4 : 0);
-    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1;
+    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1 + (GU ? 2 : 0);
     static constexpr int O_TAB = O_BAR + (N_BAR + 1) * 8;
     // tables: first row, end row and first tile of each group, total last
     static constexpr int smem(int E) { return 1024 + O_TAB + (3 * E + 4) * 4; }
@@ -208,6 +213,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* acc_full = sc_empty + SC_RING;
     uint64_t* acc_empty = acc_full + C::NBUF;
     uint64_t* mma_done = acc_empty + C::NBUF;
+    uint64_t* am_full = mma_done + 1;  // [2] SwiGLU form: four warps' maxima are there
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BAR);
     int* t_lo = reinterpret_cast<int*>(base + C::O_TAB);
     int* t_hi = t_lo + p.E;
@@ -230,11 +236,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&acc_empty[i], EPI_WARPS);
         }
         mbar_init(mma_done, 1);
+        if constexpr (C::GU)
+            for (int i = 0; i < 2; ++i) mbar_init(&am_full[i], 4);
         fence_barrier_init();
         prefetch_tensormap(&tm_w);
         prefetch_tensormap(&tm_x);
         if constexpr (C::GU) prefetch_tensormap(&tm_w2);
     }
+    // failure-path tests: this CTA's load warp issues nothing, so that every wait
+    // that depends on it runs out
+    const bool skip = __ldcg(&p.err->skip_arrive_cta) == static_cast<int>(blockIdx.x);
     // Every operand may be an earlier launch's output (weights quantised on
     // this stream too), so nothing is read before the dependency wait.
     pdl_wait();
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ---------------------------------------------------------- loads
         int it = 0, s = 0;
         uint32_t ph = 1;  // parity of the wait for a free stage
-        bool ok = true;
+        bool ok = !skip;
         for (int t = first; t < tiles && ok; t += step) {
             const Tile w = t == first ? w0 : tile_at_warp(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             const int boxes = (w.np + C::BOX - 1) / C::BOX;
@@ -500,7 +511,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     if (lane < C::CH) am[quad * C::NT + col + lane] = mine;
                 }
-                named_bar(1 + half, 128);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&am_full[half]);
+                ok = mbar_wait_spin(&am_full[half], par, p.err, DEV_GMM_TIMEOUT);
+                if (!ok) break;
                 if (col < w.np) {
                     float s = 1.f, inv = 1.f;
                     if (lane < C::CH) {

@@ -26,12 +26,18 @@
 //
 // So a wide tile with few epilogue warps is for many rows per group; where
 // groups fill at most 128 columns, four buffers and sixteen warps are faster
-// (64 groups of 64 rows, 1024 x 2048: 34 against 39 us).
+// (64 groups of 64 rows, 1024 x 2048: 34 against 39 us).  The 16-bit form is
+// bound by shared memory too: 80 KB per 128 bytes of K are 625 clocks, 650
+// measured, against 513 of MMA.
 //
-// Roles: warps 0 and 2 load, warp 1 (of the first CTA)
-// issues the MMAs, warp 3 stages scale products, the warps from 4 on are the epilogue: warp w reads
-// lanes 32 (w % 4) .. + 31 and up to two runs of 32 columns (SwiGLU form:
-// the same run of gate and of up).
+// Measured: f16, 16,384 rows in 8 groups, 4096 x 4096: 335 us, 1640 TFLOP/s;
+// e4m3, 4096 x 14336 x 4096: 301 us, 1600 TFLOP/s; 64 groups of about 64 rows,
+// 1024 x 2048 e4m3: 32 us, 4.3 TB/s.
+//
+// Roles: warps 0 and 2 load, warp 1 (of the first CTA) issues the MMAs, warp 3
+// stages scale products, the warps from 4 on are the epilogue: warp w reads
+// lanes 32 (w % 4) .. + 31 and up to two runs of 32 columns (SwiGLU form: the
+// same run of gate and of up).
 #pragma once
 #include "gmm.cuh"
 
@@ -62,14 +68,14 @@ struct PairCfg {
     static constexpr int TM_BUF = NA * NT;
     static constexpr int TM_COLS = 512;
     static constexpr int NBUF = TM_COLS / TM_BUF;  // accumulator buffers
-        static constexpr int SC_STAGE = SC_BLK * NA * NT;  // floats: sx sw of every column
+    static constexpr int SC_STAGE = SC_BLK * NA * NT;  // floats: sx sw of every column
     // staging per epilogue warp: 32 tokens of 32 values
     static constexpr int OUT_BYTES = GU ? 1024 : 2048;
     static constexpr int O_SC = NST * STAGE;
     static constexpr int O_OUT = O_SC + (F8 ? SC_RING * SC_STAGE * 4 : 0);
     static constexpr int O_AMAX = O_OUT + EPI * OUT_BYTES;
     static constexpr int O_BAR = O_AMAX + (GU ? 2 * 4 * NT * 4 : 0);
-    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1;
+    static constexpr int N_BAR = 2 * NST + 2 * SC_RING + 2 * NBUF + 1 + (GU ? CG : 0);
     static constexpr int O_TAB = O_BAR + (N_BAR + 1) * 8;
     static constexpr int smem(int E) { return 1024 + O_TAB + (3 * E + 4) * 4; }
     static_assert(TM_BUF * NBUF <= TM_COLS && STAGE % 1024 == 0, "tile shape");
@@ -179,6 +185,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t* acc_full = sc_empty + SC_RING;  // [NBUF] each CTA's
     uint64_t* acc_empty = acc_full + C::NBUF; // [NBUF] first CTA's: both epilogues have read it
     uint64_t* mma_done = acc_empty + C::NBUF;
+    uint64_t* am_full = mma_done + 1;  // [CG] SwiGLU form: four warps' maxima are there
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BAR);
     int* t_lo = reinterpret_cast<int*>(base + C::O_TAB);
     int* t_hi = t_lo + p.E;
@@ -203,11 +210,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&acc_empty[i], 2 * C::EPI);
         }
         mbar_init(mma_done, 1);
+        if constexpr (C::GU)
+            for (int i = 0; i < C::CG; ++i) mbar_init(&am_full[i], 4);
         fence_barrier_init();
         prefetch_tensormap(&tm_w);
         prefetch_tensormap(&tm_x);
         if constexpr (C::GU) prefetch_tensormap(&tm_w2);
     }
+    // (failure-path tests, as in gmm_kernel)
+    const bool skip = __ldcg(&p.err->skip_arrive_cta) == static_cast<int>(blockIdx.x);
     pdl_wait();
     pdl_trigger();
     umma::fence_before_sync();
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
             const bool wgt = warp == 0;
             int it = 0, s = 0;
             uint32_t ph = 1;  // parity of the wait for a free stage
-            bool ok = true;
+            bool ok = !skip;
             const uint32_t full0 = cluster_addr(full, 0);
             for (int t = first; t < tiles && ok; t += step) {
                 const Tile w = tile_at_warp(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
@@ -533,7 +544,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
                             if (lr == 0) am[quad * C::NT + run_col + 4 * i + lc] = m;
                         }
                     }
-                    named_bar(1 + cg, 128);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&am_full[cg]);
+                    ok = mbar_wait_spin(&am_full[cg], par, p.err, DEV_GMM_TIMEOUT);
+                    if (!ok) break;
                     if (runs > 0) {
                         uint32_t* codes = reinterpret_cast<uint32_t*>(stage);
 #pragma unroll

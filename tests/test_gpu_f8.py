@@ -677,3 +677,46 @@ print("captured")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("cta", [0, 1])
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (32, 20000, 256), (600, 1024, 512),
+                                   (900, 700, 1600)],
+                         ids=["shared_k", "few_rows", "pairs", "pairs_ragged"])
+def test_wait_that_runs_out_is_reported(qm, m, n, k, cta):
+    """One CTA loads nothing and every device wait gives up after 5 ms: the call
+    returns, the status says so, and the next call is right."""
+    import torch
+    g = np.random.default_rng(71)
+    xq, xs, wq, ws, xv, wv = f8_operands(g, m, n, k)
+    args = (dev(wq[0]), dev(ws[0]), n, k, dev(xq), dev(xs), m, qm.F32)
+    y = out_tensor(m, n, torch.float32)
+    torch.cuda.synchronize()
+    qm.set_fault_injection(5_000_000, cta)
+    try:
+        qm.f8_mm(*args, y)
+        assert qm.device_status() == qm.ERR_TIMEOUT
+        assert "wait" in qm.last_error()
+    finally:
+        qm.set_fault_injection(0, -1)
+    qm.f8_mm(*args, y)
+    assert qm.device_status() == qm.OK
+    want, err = ref.product(xv, wv[0], ref.f8_terms(k))
+    check(f64(y), want, ref.rounded(want, err, "f32"), "after the timeout")
+
+
+@pytest.mark.parametrize("tokens", [1, 300])
+def test_moe_wait_that_runs_out_is_reported(qm, tokens):
+    dims = (tokens, 256, 256, 4, 2)
+    g, x, residual, idx, w, stacks = moe_case(72, *dims, "bf16")
+    args = (x.cuda(), dev(idx), dev(w), dev_stacks(stacks), residual.cuda())
+    good = run_moe(qm, dims, "bf16", *args)
+    assert qm.device_status() == qm.OK
+    qm.set_fault_injection(5_000_000, 0)
+    try:
+        run_moe(qm, dims, "bf16", *args)
+        assert qm.device_status() == qm.ERR_TIMEOUT
+    finally:
+        qm.set_fault_injection(0, -1)
+    assert (run_moe(qm, dims, "bf16", *args) == good).all()
+    assert qm.device_status() == qm.OK
