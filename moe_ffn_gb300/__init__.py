@@ -288,13 +288,25 @@ def _context(stream):
     return dev, stream
 
 
-def _arg(fn: str, name: str, t, kind, need: int, dev: int):
+def _rows_apart(t, ld) -> bool:
+    """Whether a tensor's rows are consecutive elements, `ld` apart."""
+    if ld is None or t.dim() < 2 or (t.size(-1) > 1 and t.stride(-1) != 1):
+        return False
+    for i in range(t.dim() - 2, -1, -1):
+        if t.size(i) > 1 and t.stride(i) != ld:
+            return False
+        ld *= t.size(i)
+    return True
+
+
+def _arg(fn: str, name: str, t, kind, need: int, dev: int, ld=None):
     """Address of a device array of at least `need` elements of type `kind`
     (None: any type).
 
     Integers (addresses) and None pass through unchecked; a tensor must live
     on the current CUDA device, have the element type the call names (one-byte
-    types for E4M3) and reach `need` elements from its first one."""
+    types for E4M3) and reach `need` elements from its first one.  It must be
+    contiguous; rows of a strided argument may lie `ld` apart."""
     if t is None or isinstance(t, int):
         return t
     if not t.is_cuda or t.get_device() != dev:
@@ -304,7 +316,12 @@ def _arg(fn: str, name: str, t, kind, need: int, dev: int):
     if kind in _DTYPES and t.dtype not in _DTYPES[kind]:
         raise QmoeError(ERR_INVALID_ARGUMENT,
                         f"{fn}: {name} has dtype {t.dtype}, not {_DTYPES[kind][0]}")
-    if not (t.is_contiguous() and t.numel() >= need):
+    dense = t.is_contiguous()
+    if not (dense or _rows_apart(t, ld)):
+        raise QmoeError(ERR_INVALID_ARGUMENT,
+                        f"{fn}: {name} has strides {tuple(t.stride())}, which are not those of "
+                        + ("a contiguous array" if ld is None else f"rows {ld} apart"))
+    if not (dense and t.numel() >= need):
         have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
         if have < need:
             raise QmoeError(ERR_INVALID_ARGUMENT,
@@ -326,7 +343,7 @@ def f8_quantize(xtype: int, x, rows: int, cols: int, q, scale, ldx=None, stream=
     fn, ldx = "f8_quantize", cols if ldx is None else ldx
     dev, st = _context(stream)
     _check((_libh or lib()).f8_quantize(
-        xtype, _arg(fn, "x", x, xtype, _span(rows, cols, ldx), dev), rows, cols, ldx,
+        xtype, _arg(fn, "x", x, xtype, _span(rows, cols, ldx), dev, ldx), rows, cols, ldx,
         _arg(fn, "q", q, E4M3, rows * cols, dev),
         _arg(fn, "scale", scale, F32, rows * f8_blocks(cols), dev), st))
 
@@ -340,9 +357,9 @@ def f8_mm(W, w_scale, rows: int, cols: int, x, x_scale, n_tokens: int, ytype: in
     _check((_libh or lib()).f8_mm(
         _arg(fn, "W", W, E4M3, rows * cols, dev),
         _arg(fn, "w_scale", w_scale, F32, f8_blocks(rows) * kb, dev), rows, cols,
-        _arg(fn, "x", x, E4M3, _span(n_tokens, cols, ldx), dev),
+        _arg(fn, "x", x, E4M3, _span(n_tokens, cols, ldx), dev, ldx),
         _arg(fn, "x_scale", x_scale, F32, n_tokens * kb, dev), n_tokens, ldx, ytype,
-        _arg(fn, "y", y, ytype, _span(n_tokens, rows, ldy), dev), ldy, st))
+        _arg(fn, "y", y, ytype, _span(n_tokens, rows, ldy), dev, ldy), ldy, st))
 
 
 def mm_grouped(wtype: int, W, w_scale, num_groups: int, rows: int, cols: int, x, x_scale,
@@ -354,10 +371,10 @@ def mm_grouped(wtype: int, W, w_scale, num_groups: int, rows: int, cols: int, x,
     _check((_libh or lib()).mm_grouped(
         wtype, _arg(fn, "W", W, wtype, num_groups * rows * cols, dev),
         _arg(fn, "w_scale", w_scale, F32, num_groups * f8_blocks(rows) * kb, dev), num_groups,
-        rows, cols, _arg(fn, "x", x, wtype, _span(n_rows, cols, ldx), dev),
+        rows, cols, _arg(fn, "x", x, wtype, _span(n_rows, cols, ldx), dev, ldx),
         _arg(fn, "x_scale", x_scale, F32, n_rows * kb, dev), n_rows, ldx,
         _arg(fn, "offsets", offsets, _I32, num_groups + 1, dev), ytype,
-        _arg(fn, "y", y, ytype, _span(n_rows, rows, ldy), dev), ldy, st))
+        _arg(fn, "y", y, ytype, _span(n_rows, rows, ldy), dev, ldy), ldy, st))
 
 
 def moe_experts_f8_workspace_size(shape: _Shape) -> int:
@@ -402,8 +419,9 @@ def set_exec_mode(mode: int) -> None:
 
 def set_fault_injection(wait_limit_ns: int = 0, skip_arrive_cta: int = -1) -> None:
     """Failure-path tests only: shorten every bounded device wait and make one
-    CTA of the cooperative kernels skip its grid-barrier arrivals; (0, -1)
-    restores normal operation (see include/qmoe.h)."""
+    CTA of the cooperative kernels skip its grid-barrier arrivals, or one of the
+    e4m3, bf16 and f16 products load nothing; (0, -1) restores normal operation
+    (see include/qmoe.h)."""
     _check(lib().qmoe_set_fault_injection(wait_limit_ns, skip_arrive_cta))
 
 

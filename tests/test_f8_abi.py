@@ -146,6 +146,63 @@ def test_binding_refuses_host_and_mistyped_tensors(lib):
     assert ei.value.status == INV and "current CUDA device" in str(ei.value)
 
 
+class OnDevice:
+    """A host tensor that says it is on the current CUDA device: for refusals
+    that come before anything is launched."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def get_device(self):
+        import torch
+        return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_binding_refuses_layouts_it_would_misread(lib):
+    """Arrays are read by address, row after row: a transposed tensor, rows
+    with gaps where no stride is given, or another stride than the one given
+    would be read in the wrong order."""
+    torch = pytest.importorskip("torch")
+    d = OnDevice
+    n, k, m = 64, 128, 4
+    w = torch.zeros(n, k, dtype=torch.uint8)
+    ws, xs, y = torch.zeros(1, 1), torch.zeros(m, 1), torch.zeros(m, n)
+    x = torch.zeros(m, k, dtype=torch.uint8)
+    gaps = torch.zeros(2 * m, 2 * k, dtype=torch.uint8)
+
+    def f8(w=w, ws=ws, x=x, xs=xs, y=y, **kw):
+        qm.f8_mm(d(w), d(ws), n, k, d(x), d(xs), m, qm.F32, d(y), stream=0, **kw)
+
+    wide = torch.zeros(n, 2 * k, dtype=torch.uint8)
+    for name, call in [
+            ("W", lambda: f8(w=torch.zeros(k, n, dtype=torch.uint8).t())),
+            ("W", lambda: f8(w=wide[:, :k])),
+            ("x", lambda: f8(x=torch.zeros(k, m, dtype=torch.uint8).t())),
+            ("x", lambda: f8(x=gaps[:m, :k])),
+            ("x", lambda: f8(x=gaps[::2, :k], ldx=2 * k)),
+            ("x_scale", lambda: f8(xs=torch.zeros(m, 2)[:, :1])),
+            ("y", lambda: f8(y=torch.zeros(m, 2 * n)[:, :n])),
+            ("y", lambda: f8(y=torch.zeros(n, m).t()))]:
+        with pytest.raises(qm.QmoeError) as ei:
+            call()
+        assert ei.value.status == INV and f"f8_mm: {name} " in str(ei.value)
+        assert "stride" in str(ei.value)
+
+
+def test_binding_takes_rows_with_the_given_stride(lib):
+    torch = pytest.importorskip("torch")
+    qm._context(0)
+    big = torch.zeros(3, 4, 256)
+    dev = OnDevice(big).get_device()
+    for t, ld in [(big[0, :, :128], 256), (big[0, ::2, :128], 512), (big[:, :, :128], 256),
+                  (big[0], 256), (big[0], 128), (big.view(-1), 256), (big[1, 2:3, 5:133], 128)]:
+        assert qm._arg("f", "x", OnDevice(t), qm.F32, 1, dev, ld) == t.data_ptr()
+
+
 def test_type_numbers_match_header():
     text = open(qm.HEADER).read()
     for name in ("BF16", "F16", "E4M3"):
