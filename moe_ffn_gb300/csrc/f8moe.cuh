@@ -22,8 +22,8 @@ __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 // one or two 16-byte loads, a four-step maximum, one 8-byte store.  They take
 // RUN neighbouring blocks of a row, all loaded before the first is reduced.
 // Bound by HBM, (size + 1) bytes per element: RUN = 4 keeps 64 bytes per thread
-// in flight (4096 x 14336 bf16: 46 us, with RUN = 1 58 us); RUN = 1 spreads few
-// rows over more threads (1 x 2048: 1.9 against 2.7 us).  VEC needs 16-byte aligned
+// in flight (4096 x 14336 bf16: 34 us, 5.3 TB/s; with RUN = 1 48 us); RUN = 1
+// spreads few rows over more threads (1 x 2048: 1.7 against 2.6 us).  VEC needs 16-byte aligned
 // rows and whole groups of eight columns; the other form loads element by
 // element.
 //
@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const QuantParams p
 // the counts are summed over (expert, CTA, warp), the CTAs' totals read from
 // each other's shared memory, and a second pass over the run gives every pair
 // its row.  Pairs whose expert lies outside [0, E) get row -1.  Bound by
-// latency: G_AHEAD loads of a run are in flight at a time (one CTA with one
-// load in flight took 59 us for 32,768 pairs).
+// latency: G_AHEAD loads of a run are in flight at a time (32,768 pairs in 14 us;
+// one CTA with one load in flight took 59).
 //   offsets[E+1]  first row of each expert, total last
 //   pos[P]        row of each pair, or -1
 constexpr int G_THREADS = 1024;

@@ -25,8 +25,9 @@
 // take 512 threads (any spill in these loops cost 15 to 30 percent).
 //
 // So a wide tile with few epilogue warps is for many rows per group; where
-// groups fill at most 128 columns, four buffers and sixteen warps are faster
-// (64 groups of 64 rows, 1024 x 2048: 34 against 39 us).  The 16-bit form is
+// groups fill at most 128 columns, or wide tiles leave pairs idle, four buffers
+// and sixteen warps are faster (the rule and both sides' times stand where the
+// kernel is launched).  The 16-bit form is
 // bound by shared memory too: 80 KB per 128 bytes of K are 625 clocks, 650
 // measured, against 513 of MMA.
 //

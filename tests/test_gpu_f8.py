@@ -247,6 +247,58 @@ def test_mm_grouped(qm, kind, out, name, sizes, n, k):
         check(got[r], want, ref.rounded(want, err, out), f"{name} group {i}")
 
 
+@pytest.mark.parametrize("kind,m,n", [
+    # one group: narrow tiles in one pass, wide in one against narrow in two,
+    # narrow in two against wide in two (152 SMs)
+    ("f8", 260, 4096), ("f8", 640, 4096), ("f8", 1000, 4096), ("f8", 129, 14336),
+    ("bf16", 260, 4096), ("bf16", 640, 4096), ("f16", 384, 4096), ("f16", 1030, 4096)])
+def test_one_group_of_every_tile_width(qm, kind, m, n):
+    import torch
+    k = 400 if kind == "f8" else 200
+    g = np.random.default_rng(m)
+    y = out_tensor(m, n, torch.float32)
+    off = dev(np.array([0, m], dtype=np.int32))
+    if kind == "f8":
+        xq, xs, wq, ws, xv, wv = f8_operands(g, m, n, k)
+        qm.mm_grouped(qm.E4M3, dev(wq), dev(ws), 1, n, k, dev(xq), dev(xs), m, off, qm.F32, y)
+        z = out_tensor(m, n, torch.float32)
+        qm.f8_mm(dev(wq[0]), dev(ws[0]), n, k, dev(xq), dev(xs), m, qm.F32, z)
+        assert torch.equal(y, z)
+        terms = ref.f8_terms(k)
+    else:
+        x, w, xv, wv = wide_operands(g, m, n, k, 1, kind)
+        qm.mm_grouped(kinds(qm)[kind][0], w.cuda(), None, 1, n, k, x.cuda(), None, m, off, qm.F32,
+                      y)
+        terms = ref.wide_terms(k)
+    assert qm.device_status() == qm.OK
+    want, err = ref.product(xv, wv[0], terms)
+    check(f64(y), want, ref.rounded(want, err, "f32"), f"{kind} {m}x{n}")
+
+
+@pytest.mark.parametrize("kind", ["f8", "bf16"])
+@pytest.mark.parametrize("sizes", [[300, 90], [600, 0, 700, 1, 260, 129]])
+def test_few_groups_of_every_tile_width(qm, kind, sizes):
+    import torch
+    e, n, k, m = len(sizes), 2048, 272, sum(sizes)
+    g = np.random.default_rng(m)
+    off = np.cumsum([0] + sizes).astype(np.int32)
+    y = out_tensor(m, n, torch.float32)
+    if kind == "f8":
+        xq, xs, wq, ws, xv, wv = f8_operands(g, m, n, k, e)
+        qm.mm_grouped(qm.E4M3, dev(wq), dev(ws), e, n, k, dev(xq), dev(xs), m, dev(off), qm.F32, y)
+        terms = ref.f8_terms(k)
+    else:
+        x, w, xv, wv = wide_operands(g, m, n, k, e, kind)
+        qm.mm_grouped(qm.BF16, w.cuda(), None, e, n, k, x.cuda(), None, m, dev(off), qm.F32, y)
+        terms = ref.wide_terms(k)
+    assert qm.device_status() == qm.OK
+    got = f64(y)
+    for i in range(e):
+        r = slice(off[i], off[i + 1])
+        want, err = ref.product(xv[r], wv[i], terms)
+        check(got[r], want, ref.rounded(want, err, "f32"), f"group {i}")
+
+
 @pytest.mark.parametrize("kind", ["f8", "bf16"])
 def test_mm_grouped_larger(qm, kind):
     """Several token tiles a group and more tiles than SMs, K over many blocks."""
