@@ -354,8 +354,9 @@ __global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
 // out[t] = residual[t] + sum_s w[t][s] y[pos[t][s]], summed in f32 in slot
 // order and rounded once.  A thread takes eight columns of one token and loads
 // four slots' values before it adds them.  Bound by reading y: for bf16
-// activations y is bf16 (the layer rounds each expert's output once: 2^-9 of
-// it, below out's own rounding; y is the layer's largest traffic), else f32.
+// activations y is bf16 (the layer rounds each expert's output once, by at most
+// 2^-8 of it, as out's own rounding is of out; y is the layer's largest traffic),
+// else f32.
 constexpr int C_THREADS = 128;
 constexpr int C_AHEAD = 4;
 

@@ -55,18 +55,9 @@ QMOE_HD Tile tile_in(int a, int t, int nt, int step, const int* lo, const int* h
     r.np = (r.nv + step - 1) & ~(step - 1);
     return r;
 }
-// The group of tile t by bisection: pre[a] <= t < pre[a + 1].
-QMOE_HD Tile tile_at(int t, int nt, int step, const int* lo, const int* hi, const int* pre, int E) {
-    int a = 0, b = E;
-    while (b - a > 1) {
-        const int m = (a + b) >> 1;
-        if (pre[m] <= t) a = m; else b = m;
-    }
-    return tile_in(a, t, nt, step, lo, hi, pre);
-}
 #if defined(__CUDACC__)
-// The same by a whole warp, 32 groups at a step: the last a with pre[a] <= t (a
-// bisection's seven dependent loads took a tenth of a short tile's time).
+// Tile t, its group found by a whole warp, 32 groups at a step: the last a with
+// pre[a] <= t (a bisection's seven dependent loads took a tenth of a short tile's time).
 __device__ __forceinline__ Tile tile_at_warp(int t, int nt, int step, const int* lo,
                                              const int* hi, const int* pre, int E) {
     const int lane = static_cast<int>(threadIdx.x) & 31;
@@ -77,6 +68,16 @@ __device__ __forceinline__ Tile tile_at_warp(int t, int nt, int step, const int*
         if (n < 32) break;
     }
     return tile_in(a - 1, t, nt, step, lo, hi, pre);
+}
+#else
+// The same for the host, by bisection: pre[a] <= t < pre[a + 1].
+QMOE_HD Tile tile_at(int t, int nt, int step, const int* lo, const int* hi, const int* pre, int E) {
+    int a = 0, b = E;
+    while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (pre[m] <= t) a = m; else b = m;
+    }
+    return tile_in(a, t, nt, step, lo, hi, pre);
 }
 #endif
 

@@ -285,22 +285,6 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* tmap, in
         : "memory");
 }
 
-// 4-byte asynchronous copy global -> shared; zeros instead if !valid (the
-// source must be readable all the same).  cp_async_arrive arrives on `bar`
-// once this thread's earlier copies have landed.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(valid ? 4 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_drain() {
-    asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
 // Brings a tensor map (a __grid_constant__ parameter) to the copy engine.
 __device__ __forceinline__ void prefetch_tensormap(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
