@@ -31,8 +31,10 @@
 // bound by shared memory too: 80 KB per 128 bytes of K are 625 clocks, 650
 // measured, against 513 of MMA.
 //
-// Measured: f16, 16,384 rows in 8 groups, 4096 x 4096: 335 us, 1640 TFLOP/s;
-// e4m3, 4096 x 14336 x 4096: 301 us, 1600 TFLOP/s; 64 groups of about 64 rows,
+// Measured: f16, 16,384 rows in 8 groups, 4096 x 4096: 334 to 344 us, 1600 to
+// 1650 TFLOP/s, in short runs; 379 us in long ones, where the power limit lowers
+// the clock to 1.4 GHz; e4m3, 4096 x 14336 x 4096: 300 us, 1600 TFLOP/s, at full
+// clock in either; 64 groups of about 64 rows,
 // 1024 x 2048 e4m3: 32 us, 4.3 TB/s.
 //
 // Roles: warps 0 and 2 load, warp 1 (of the first CTA) issues the MMAs, warp 3
