@@ -194,6 +194,17 @@ __device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, in
     __syncthreads();
 }
 
+// Waits until the MMAs have handed back the stages of the last `it` loads, a lane
+// per stage; true if they have, and then the copies have landed and the commits'
+// arrivals too.  False at once where the loads had given up (`ok` false).
+template <int NST>
+__device__ __forceinline__ bool drain_stages(uint64_t* empty, int it, bool ok, DevCtl* err) {
+    const int k = it - 1 - (static_cast<int>(threadIdx.x) & 31);
+    if (ok && k >= 0 && k >= it - NST)
+        ok = mbar_wait_spin(&empty[k % NST], (k / NST) & 1, err, DEV_GMM_TIMEOUT);
+    return __all_sync(0xffffffffu, ok);
+}
+
 template <class C>
 __global__ void __launch_bounds__(THREADS, 1)
     gmm_kernel(const Params p, const __grid_constant__ CUtensorMap tm_w,
@@ -304,9 +315,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
-        // never leave with copies in flight
-        for (int k = max(it - C::NST, 0); k < it; ++k)
-            mbar_wait_spin(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
+        // never leave with copies or a commit's arrival in flight
+        if (!drain_stages<C::NST>(empty, it, ok, p.err))
+            for (int k = max(it - C::NST, 0); k < it; ++k)
+                mbar_wait_spin(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
         int s = 0;

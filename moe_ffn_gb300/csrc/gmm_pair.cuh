@@ -282,9 +282,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
             }
-            // never leave with copies in flight (the pair's: the other CTA
-            // leaves only after the cluster barrier at the end)
-            if (wgt && rank == 0)
+            // never leave with copies or a commit's arrival in flight: the MMA warp
+            // signals both CTAs' stages, and no barrier between threads orders the
+            // tensor core's arrivals
+            if (wgt && !drain_stages<C::NST>(empty, it, ok, p.err) && rank == 0)
                 for (int k = max(it - C::NST, 0); k < it; ++k)
                     mbar_wait_spin(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
         } else if (warp == 1 && rank == 0) {
@@ -604,10 +605,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
     umma::fence_before_sync();
     __syncthreads();
-    // neither CTA leaves while the other may still signal it or read its copies
+    // neither CTA leaves while the other's threads may still signal it or its copies
+    // are read
     cluster_sync();
     umma::fence_after_sync();
-    if (warp == 1) umma::tmem_dealloc_pair(tmem, C::TM_COLS);
+    if (warp == 1) {
+        // The last commit arrives in both CTAs; the first has seen its own copy before
+        // the barrier above, so the second's is due now.  (Waited for here, for a
+        // wait from the start of a long launch would run out.)
+        if (rank != 0) mbar_wait_spin(mma_done, 0, p.err, DEV_GMM_TIMEOUT);
+        __syncwarp();
+        umma::tmem_dealloc_pair(tmem, C::TM_COLS);
+    }
 }
 
 }  // namespace gmm
