@@ -33,7 +33,7 @@ constexpr int64_t MAX_COLS = 1 << 20;    // K of a product, columns of a quantis
 constexpr int64_t MAX_ROWS = 0x7fffff00; // token rows and weight rows
 constexpr int MAX_GROUPS = 1024;
 constexpr int MAX_F8_EXPERTS = 256;
-constexpr int MAX_F8_TOPK = 16;
+constexpr int MAX_F8_TOPK = 16;  // the kernels hold a token's slots in 16 lanes
 
 // ------------------------------------------------------------ tensor maps
 // [outer][rows][inner] elements of `size` bytes, 128-byte swizzled boxes of

@@ -1,5 +1,9 @@
 // f8moe.cuh — the kernels around the e4m3 products: quantising rows, sorting
 // a layer's (token, slot) pairs by expert, and adding the experts' outputs.
+//
+// Under programmatic dependent launch these grids may be resident while their
+// inputs are still being written, so inputs are never read as data that is
+// constant for the kernel's life (ld.global.nc): __ldcg, behind the wait.
 #pragma once
 #include <type_traits>
 
@@ -159,6 +163,9 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const QuantParams p
             }
         }
     }
+    // the rows of a token's slots: one load, a slot per lane (k <= 16)
+    const unsigned half = 0xffffu << (threadIdx.x & 16);
+    const int slot_row = p.pos && live && sub < p.k ? __ldcg(p.pos + row * p.k + sub) : -1;
 #pragma unroll
     for (int b = 0; b < RUN; ++b) {
         float s;
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const QuantParams p
         const int c = c0 + b * F8_BLOCK;
         const int nslot = p.pos ? p.k : 1;
         for (int i = 0; i < nslot; ++i) {
-            const int64_t r = p.pos ? __ldg(p.pos + row * p.k + i) : row;
+            const int64_t r = p.pos ? __shfl_sync(half, slot_row, i, 16) : row;
             if (r < 0) continue;
             uint8_t* dst = p.q + r * p.cols + c;
             if constexpr (VEC) {
@@ -198,9 +205,8 @@ constexpr int G_WARPS = G_THREADS / 32;
 constexpr int G_AHEAD = 4;
 constexpr int G_CLUSTER = 8;
 
-__global__ void __launch_bounds__(G_THREADS) group_kernel(const int32_t* __restrict__ idx, int P,
-                                                          int E, int32_t* __restrict__ offsets,
-                                                          int32_t* __restrict__ pos) {
+__global__ void __launch_bounds__(G_THREADS) group_kernel(const int32_t* idx, int P, int E,
+                                                          int32_t* offsets, int32_t* pos) {
     extern __shared__ int hist[];  // [G_WARPS][E], then this CTA's totals [E]
     __shared__ int wsum[G_WARPS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(G_THREADS) group_kernel(const int32_t* __restr
 #pragma unroll
         for (int a = 0; a < G_AHEAD; ++a) {
             const int j = i + 32 * a + lane;
-            const int v = j < end ? __ldg(idx + j) : -1;
+            const int v = j < end ? __ldcg(idx + j) : -1;
             e[a] = v >= 0 && v < E ? v : -1;
         }
     };
@@ -296,15 +302,14 @@ constexpr int GQ_PAIRS = 256;
 
 template <class T>
 __global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
-    const QuantParams p, const int32_t* __restrict__ idx, int P, int E,
-    int32_t* __restrict__ offsets, int32_t* __restrict__ pos_out) {
+    const QuantParams p, const int32_t* idx, int P, int E, int32_t* offsets, int32_t* pos_out) {
     __shared__ int s_idx[GQ_PAIRS];
     __shared__ int s_pos[32];
     const int tid = threadIdx.x, t = blockIdx.x;
     pdl_wait();
     pdl_trigger();
     for (int i = tid; i < P; i += Q_THREADS) {
-        const int e = __ldg(idx + i);
+        const int e = __ldcg(idx + i);
         s_idx[i] = e >= 0 && e < E ? e : -1;
     }
     if (tid < 32) s_pos[tid] = 0;
@@ -385,13 +390,16 @@ __device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
 
 template <class T, class Y>
 __global__ void __launch_bounds__(C_THREADS) combine_kernel(
-    const Y* __restrict__ y, const int32_t* __restrict__ pos, const float* __restrict__ w,
-    const T* residual, T* out, int H, int k) {
+    const Y* y, const int32_t* pos, const float* w, const T* residual, T* out, int H, int k) {
     const int64_t t = blockIdx.x;
     const int c = (blockIdx.y * C_THREADS + threadIdx.x) * 8;
+    const int lane = threadIdx.x & 31;
+    const bool in = c < H;
     pdl_wait();
     pdl_trigger();
-    if (c >= H) return;
+    // a token's slots: one load, a slot per lane (k <= 16)
+    const int slot_row = lane < k ? __ldcg(pos + t * k + lane) : -1;
+    const float slot_w = lane < k ? __ldcg(w + t * k + lane) : 0.f;
     float a[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = 0.f;
@@ -399,17 +407,19 @@ __global__ void __launch_bounds__(C_THREADS) combine_kernel(
         float v[C_AHEAD][8], ws[C_AHEAD];
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s) {
-            const int r = s0 + s < k ? __ldg(pos + t * k + s0 + s) : -1;
-            ws[s] = r >= 0 ? __ldg(w + t * k + s0 + s) : 0.f;
+            const int r = __shfl_sync(0xffffffffu, slot_row, s0 + s);  // -1 past the slots
+            ws[s] = __shfl_sync(0xffffffffu, slot_w, s0 + s);
+            if (r < 0) ws[s] = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
-            if (r >= 0) load8(y + static_cast<int64_t>(r) * H + c, v[s]);
+            if (in && r >= 0) load8(y + static_cast<int64_t>(r) * H + c, v[s]);
         }
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s)
 #pragma unroll
             for (int i = 0; i < 8; ++i) a[i] = fmaf(ws[s], v[s][i], a[i]);
     }
+    if (!in) return;
     if (residual) {
         float r[8];
         load8(residual + t * H + c, r);

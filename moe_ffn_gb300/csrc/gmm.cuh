@@ -392,9 +392,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     float v[RPT][SC_BLK], g[C::NA][SC_BLK];
 #pragma unroll
                     for (int b = 0; b < SC_BLK; ++b) {
-                        g[0][b] = k0 + b < kend ? __ldg(p.ws + wo + k0 + b) : 0.f;
+                        g[0][b] = k0 + b < kend ? __ldcg(p.ws + wo + k0 + b) : 0.f;
                         if constexpr (C::GU)
-                            g[1][b] = k0 + b < kend ? __ldg(p.ws2 + wo + k0 + b) : 0.f;
+                            g[1][b] = k0 + b < kend ? __ldcg(p.ws2 + wo + k0 + b) : 0.f;
                     }
 #pragma unroll
                     for (int i = 0; i < RPT; ++i) {

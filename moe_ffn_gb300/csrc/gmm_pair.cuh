@@ -364,7 +364,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
                 const bool rows_in = nbi < p.nb;  // the last weight tile's second half may be empty
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + nbi) * p.kb;
                 const float* xs = p.xs + (static_cast<int64_t>(w.row0) + lane) * p.kb;
+                float ws[C::NA];  // weight scales of 32 k-blocks, one per lane
                 for (int k0 = 0; k0 < p.kb; k0 += SC_BLK) {
+                    if ((k0 & 31) == 0)
+#pragma unroll
+                        for (int a = 0; a < C::NA; ++a)
+                            ws[a] = rows_in && k0 + lane < p.kb
+                                        ? __ldcg((a ? p.ws2 : p.ws) + wo + k0 + lane)
+                                        : 0.f;
                     if (!mbar_wait_spin(&sc_empty[s], ph, p.err, DEV_GMM_TIMEOUT)) {
                         ok = false;
                         break;
@@ -388,9 +395,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
                     for (int b = 0; b < SC_BLK; ++b)
 #pragma unroll
                         for (int a = 0; a < C::NA; ++a) {
-                            const float g = rows_in && k0 + b < p.kb
-                                                ? __ldg((a ? p.ws2 : p.ws) + wo + k0 + b)
-                                                : 0.f;
+                            const float g = __shfl_sync(0xffffffffu, ws[a], (k0 & 31) + b);
 #pragma unroll
                             for (int i = 0; i < C::NT / 32; ++i)
                                 dst[(b * C::NA + a) * C::NT + sc_slot(lane + 32 * i)] =

@@ -50,3 +50,18 @@ def test_no_cta_leaves_with_a_commit_in_flight():
     body = between(one, "bool drain_stages(", "__global__")
     assert "mbar_wait_spin(&empty[k % NST], (k / NST) & 1" in body and "__all_sync" in body
     assert one.index("commit(mma_done)") < one.index("mbar_wait_spin(mma_done")
+
+
+def test_no_read_only_loads_of_stream_ordered_data():
+    """These grids may start before the launch that writes their inputs has
+    ended (weight scales included: every operand is ordered by the stream).
+    Loads that promise read-only data for the kernel's whole life, written out
+    or allowed to the compiler by __restrict__, are not theirs to use."""
+    for name in ("f8.cuh", "f8.cu", "f8moe.cuh", "gmm.cuh", "gmm_pair.cuh", "gmm_tiles.cuh"):
+        text = code(name)
+        for word in ("__ldg(", "ld.global.nc", "__restrict__"):
+            assert word not in text, (name, word)
+        # nothing is read before the dependency wait but the kernel's own control block
+        for kernel in re.findall(r"__global__ void.*?pdl_wait\(\);", text):
+            reads = set(re.findall(r"__ldcg\(([^)]*)\)", kernel))
+            assert reads <= {"&p.err->skip_arrive_cta"}, (name, reads)
