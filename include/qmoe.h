@@ -361,9 +361,9 @@ qmoe_status f8_mm(const void* W, const float* w_scale, int64_t rows, int64_t col
  *   n_rows   rows of x and y
  *   offsets  [num_groups + 1] int32 on the device, not decreasing, within
  *            [0, n_rows]; groups may be empty, and rows of y before offsets[0]
- *            or from offsets[num_groups] on are left as they were.  Offsets
- *            that break this are clamped (no access leaves the arrays), and
- *            qmoe_device_status reports INVALID_ARGUMENT.
+ *            or from offsets[num_groups] on are left as they were.  If any
+ *            offset breaks this the call computes nothing, y is left as it
+ *            was, and qmoe_device_status reports INVALID_ARGUMENT.
  * Other arguments, rules and errors as f8_mm. */
 qmoe_status mm_grouped(int wtype, const void* W, const float* w_scale, int32_t num_groups,
                        int64_t rows, int64_t cols, const void* x, const float* x_scale,

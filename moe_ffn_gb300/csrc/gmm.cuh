@@ -151,22 +151,26 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // The groups' tables, by the whole CTA (ends with a barrier): rows [lo, hi) of
-// each group and the tiles before it, the total last.  Offsets are clamped into
-// [0, M], so that no value of theirs forms an address outside x or y.  A thread
-// per group; the time is one load latency and one scan.
+// each group and the tiles before it, the total last.  If any group's offsets
+// decrease or leave [0, M] the total is 0 and the call computes nothing: clamped
+// groups may overlap, so two would write the same rows, and their tiles may be
+// more than an int counts.  A thread per group; the time is one load latency and
+// one scan.
 __device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, int* t_lo,
                                              int* t_hi, int* t_pre) {
     __shared__ int wsum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int total = 0;
+    int total = 0, bad = 0;
     for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
         const int e = e0 + tid;
         int n = 0;
         if (e < p.E) {
             int lo = 0, hi = p.M;
             if (p.offsets &&
-                !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M, &lo, &hi))
+                !group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M, &lo, &hi)) {
                 record_error(p.err, DEV_GMM_OFFSETS);
+                bad = 1;
+            }
             t_lo[e] = lo;
             t_hi[e] = hi;
             n = group_tiles(hi - lo, nt, nb);
@@ -178,7 +182,7 @@ __device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, in
             if (lane >= o) s += v;
         }
         if (lane == 31) wsum[warp] = s;
-        __syncthreads();
+        bad = __syncthreads_or(bad);
         const int nw = static_cast<int>(blockDim.x >> 5);
         int before = 0, all = 0;
         for (int w = 0; w < nw; ++w) {
@@ -190,7 +194,7 @@ __device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, in
         total += all;
         if (e0 + static_cast<int>(blockDim.x) < p.E) __syncthreads();  // wsum is used again
     }
-    if (tid == 0) t_pre[p.E] = total;
+    if (tid == 0) t_pre[p.E] = bad ? 0 : total;
     __syncthreads();
 }
 

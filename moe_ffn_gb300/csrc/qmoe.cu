@@ -1140,7 +1140,7 @@ qmoe_status qmoe_device_status(void* stream) {
         if (v == DEV_GMM_OFFSETS)
             return fail(QMOE_ERR_INVALID_ARGUMENT,
                         "mm_grouped: group offsets decrease or lie outside [0, n_rows] (code %u); "
-                        "they were clamped, and the output is not valid", v);
+                        "y was not written", v);
         return fail(QMOE_ERR_TIMEOUT, "a bounded device wait expired (code %u: %s)", v,
                     v == DEV_TIMEOUT_FULL    ? "stage never filled"
                     : v == DEV_TIMEOUT_EMPTY ? "stage never released"
