@@ -392,8 +392,11 @@ def moe_experts_f8(gate_stack, gate_scale, up_stack, up_scale, down_stack, down_
     H, F, E, T = shape.hidden, shape.expert_dim, shape.num_experts, shape.n_tokens
     P, EFH, TH = T * shape.top_k, E * F * H, T * H
     blocks = E * f8_blocks(F) * f8_blocks(H)
+    ws_need = 0
     if ws_bytes is None:
         ws_bytes = ws.numel() * ws.element_size()
+    elif ws is not None and not isinstance(ws, int):
+        ws_need = -(-ws_bytes // ws.element_size())
     dev, st = _context(stream)
     _check((_libh or lib()).moe_experts_f8(
         _arg(fn, "gate_stack", gate_stack, E4M3, EFH, dev),
@@ -404,7 +407,7 @@ def moe_experts_f8(gate_stack, gate_scale, up_stack, up_scale, down_stack, down_
         _arg(fn, "down_scale", down_scale, F32, blocks, dev), ctypes.byref(shape), xtype,
         _arg(fn, "x", x, xtype, TH, dev), _arg(fn, "topk_idx", topk_idx, _I32, P, dev),
         _arg(fn, "topk_w", topk_w, F32, P, dev), _arg(fn, "residual", residual, xtype, TH, dev),
-        _arg(fn, "out", out, xtype, TH, dev), _arg(fn, "ws", ws, None, 0, dev), ws_bytes, st))
+        _arg(fn, "out", out, xtype, TH, dev), _arg(fn, "ws", ws, None, ws_need, dev), ws_bytes, st))
 
 
 # qmoe_set_exec_mode
