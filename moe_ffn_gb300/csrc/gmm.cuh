@@ -122,9 +122,15 @@ __device__ __forceinline__ void store_out(void* y, int64_t i, int type, float v)
         static_cast<float*>(y)[i] = v;
 }
 
-// silu(g) u with the fast f32 exponential and division (2^-20 or better).
+// silu(g) u.  With e = exp(-|g|) <= 1 the quotient's divisor lies in [1, 2]: no
+// overflow for any g, where 1 + exp(-g) passed the divisor's range of the fast
+// division at g = -87.3 and gave 0.  Roundings: e 2 ulp and 1 + e half (at most
+// 1.5 in the divisor), g e half, the fast division 2, the product half: within 7
+// ulp or 2^-20 (below g = -87 e is subnormal and its last bits go).  The fast
+// exponential is off by up to 1.2 |g| ulp.
 __device__ __forceinline__ float swiglu(float g, float u) {
-    return __fdividef(g, 1.0f + __expf(-g)) * u;
+    const float e = expf(-fabsf(g));
+    return __fdividef(g < 0.f ? g * e : g, 1.0f + e) * u;
 }
 
 // The cluster's values at this CTA's address `src`, added in rank order; all

@@ -68,3 +68,48 @@ def test_bad_offsets_past_the_first_scan(qm):
     assert qm.device_status() == qm.OK
     want, err = ref.product(xv, wv[0], ref.wide_terms(k))
     check(f64(y), want, ref.rounded(want, err, "f32"), "1024 groups")
+
+
+# SwiGLU alone: with x = 1, one code per weight row and a down matrix that copies
+# one 128-block of the activations into the output, out is the activation after its
+# e4m3 rounding.  Every product is exact (powers of two times a four-bit
+# significand), so |out - a| is at most half a step of a: 2^-4 |a|, or 2^-10 of the
+# block's scale where that is more, and SwiGLU's own error, stated as 2^-20 |a|.
+def swiglu_case(qm, tokens, blocks, probe, gates, up):
+    import torch
+    H, F = 128, 128 * blocks
+    table = np.abs(ref.TABLE[:127])
+    codes = np.array([int(np.argmin(np.abs(table - abs(v)))) for v in gates], np.uint8)
+    gq = np.repeat(codes[:, None], H, axis=1)
+    G = np.zeros((1, F, H), np.uint8)
+    G[0, probe * 128:probe * 128 + 128] = gq
+    U = np.full((1, F, H), 0x38, np.uint8)  # 1.0
+    D = np.zeros((1, H, F), np.uint8)
+    D[0, np.arange(H), probe * 128 + np.arange(H)] = 0x38
+    one = lambda v, *s: dev(np.full((1,) + s, v, np.float32))
+    sign = np.float32(np.sign(gates[0]))
+    shape = qm.moe_shape(H, F, 1, 1, tokens, qm.E4M3, qm.E4M3, qm.E4M3)
+    ws = torch.empty(qm.moe_experts_f8_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    out = out_tensor(tokens, H, torch.float32)
+    qm.moe_experts_f8(dev(G), one(sign / 128, blocks, 1), dev(U), one(up / 128, blocks, 1), dev(D),
+                      one(1.0, 1, blocks), shape, qm.F32, torch.ones(tokens, H, device="cuda"),
+                      torch.zeros(tokens, 1, dtype=torch.int32, device="cuda"),
+                      torch.ones(tokens, 1, device="cuda"), None, out, ws)
+    assert qm.device_status() == qm.OK
+    g = float(sign) * table[codes]
+    a = g / (1.0 + np.exp(-g)) * up
+    scale = float(ref.block_scale(np.abs(a).max()))
+    tol = np.maximum(2.0 ** -4 * np.abs(a), 2.0 ** -10 * scale) + 2.0 ** -20 * np.abs(a)
+    check(f64(out), np.broadcast_to(a, (tokens, H)), tol, f"SwiGLU of {gates[0]}..{gates[-1]}")
+
+
+@pytest.mark.parametrize("tokens,blocks,probe", [(1, 1, 0), (20, 3, 1), (600, 10, 3), (600, 11, 10)],
+                         ids=["one", "few_rows", "pairs", "pairs_odd"])
+@pytest.mark.parametrize("gates,up", [
+    (np.linspace(0.01, 20.0, 128), 1.0), (-np.linspace(0.01, 20.0, 128), 1.0),
+    (np.linspace(20.0, 448.0, 128), 2.0 ** -3), (-np.linspace(20.0, 87.0, 128), 2.0 ** 20),
+    # far below zero: silu is 2^-120 and smaller, and up brings it back
+    (-np.full(128, 88.0), 2.0 ** 100), (-np.linspace(80.0, 88.0, 128), 2.0 ** 90)],
+    ids=["positive", "negative", "large", "small", "far", "far_mixed"])
+def test_swiglu_over_its_range(qm, tokens, blocks, probe, gates, up):
+    swiglu_case(qm, tokens, blocks, probe, gates, up)
