@@ -133,61 +133,12 @@ static qmoe_status launch_few(const Gmm& g, const DevInfo& d, cudaStream_t st) {
     return launch_gmm<C>(gmm::gmm_kernel<C>, gmm::THREADS, true, g, ranks, clusters, d, st);
 }
 
-// Whether that kernel is used: up to 16 rows per group, where its tile of 32
-// columns holds most groups (32 without groups), and beyond that as long as its
-// small tiles still fit the SMs at once, for the other kernel's 256-row tiles
-// then leave most of them idle.  e4m3, this kernel against the pair kernel:
-// 2048 x 2048, 33 / 256 rows 6.2 / 8.2 us against 9.5 / 12.2; 4096 x 4096 (32 row
-// tiles), 128 rows 12.5 against 16.4; 64 groups, 1024 x 2048, 16 rows each 28.7
-// against 30.5, 64 rows each 41.7 against 32.4.
-static bool few_rows(const gmm::Params& p, int sms) {
-    const int64_t groups = p.M < p.E ? p.M : p.E;
-    return p.M <= (p.offsets ? 16 * groups : 32) ||
-           gmm::max_tiles(p.M, p.E, 32, p.nb) <= sms;
-}
 // One CTA pair per two SMs, or as many as there can be tiles.
 template <class C>
 static qmoe_status launch_pairs(const Gmm& g, const DevInfo& d, cudaStream_t st) {
     const int64_t tiles = gmm::max_tiles(g.p.M, g.p.E, C::NT, (g.p.nb + 1) / 2);
     const int pairs = static_cast<int>(tiles < d.sms / 2 ? tiles : d.sms / 2);
     return launch_gmm<C>(gmm::gmm_pair_kernel<C>, C::THREADS, false, g, 2, pairs, d, st);
-}
-
-// Whether the pair kernel takes its narrow tiles (128 columns) or the wide ones
-// (192 for e4m3, 256 for 16-bit types), which do more work per byte but may leave
-// pairs idle.
-//   Narrow tiles that all fit the pairs at once: always (one pass either way).
-//     4096 x 4096, e4m3, 256 / 512 rows: 16.8 / 17.5 us against 19.2 / 21.6; bf16
-//     20.8 / 21.6 against 24.9 / 25.1.
-//   e4m3, one group: a pass of narrow tiles takes 3/4 of one of wide tiles.
-//     4096 x 4096, 640 / 1024 rows (2 passes against 1 / 2 against 2): 30.0 / 30.4
-//     against 20.6 / 39.4; 14336 x 4096, 1024 / 1536 rows (6 against 5 / 9 against
-//     6): 82.6 / 121 against 92 / 110.
-//   e4m3, more groups, whose sizes only the device knows: up to 128 rows per
-//     group on average.  64 groups, 1024 x 2048, 64 / 128 / 192 rows each: 32.4 /
-//     37.0 / 51.5 against 33.5 / 41.4 / 47.2.
-static bool narrow_tiles(const gmm::Params& p, bool f8, int sms) {
-    const int nb = (p.nb + 1) / 2, pairs = sms / 2;
-    const int64_t narrow = gmm::max_tiles(p.M, p.E, 128, nb);
-    if (narrow <= pairs) return true;
-    if (!f8) return false;
-    if (p.E > 1) return p.M <= int64_t{128} * (p.M < p.E ? p.M : p.E);
-    const int64_t wide = gmm::max_tiles(p.M, 1, 192, nb);
-    return 3 * ((narrow + pairs - 1) / pairs) < 4 * ((wide + pairs - 1) / pairs);
-}
-
-template <bool F8>
-static qmoe_status run_gmm_kind(Gmm& g, const DevInfo& d, cudaStream_t st) {
-    if (few_rows(g.p, d.sms)) return launch_few<gmm::Cfg<F8, 8, false>>(g, d, st);
-    g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
-    const bool narrow = narrow_tiles(g.p, F8, d.sms);
-    if constexpr (F8) {
-        return narrow ? launch_pairs<gmm::PairCfg<true, 128, 7, false, 4>>(g, d, st)
-                      : launch_pairs<gmm::PairCfg<true, 192, 6, false, 3>>(g, d, st);
-    } else {
-        return narrow ? launch_pairs<gmm::PairCfg<false, 128, 7, false, 4>>(g, d, st)
-                      : launch_pairs<gmm::PairCfg<false, 256, 5, false, 3>>(g, d, st);
-    }
 }
 
 static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
@@ -201,15 +152,21 @@ static qmoe_status run_gmm(Gmm g, const DevInfo& d, cudaStream_t st) {
     const uint32_t fmt = g.type == QMOE_BF16 ? 1u : 0u;
     g.p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) |
                 (static_cast<uint32_t>(gmm::TILE_W >> 4) << 24);
-    if (g.type == QMOE_E4M3) {
-        if (g.W2) {
-            if (few_rows(g.p, d.sms)) return launch_few<gmm::Cfg<true, 5, true>>(g, d, st);
-            g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
-            return launch_pairs<gmm::PairCfg<true, 96, 5, true, 3>>(g, d, st);
-        }
-        return run_gmm_kind<true>(g, d, st);
+    const bool f8 = g.type == QMOE_E4M3;
+    const int nt = gmm::token_tile(g.p.M, g.p.E, g.p.offsets != nullptr, g.p.nb, f8,
+                                   g.W2 != nullptr, d.sms);
+    if (nt == gmm::FEW_ROWS) {
+        if (g.W2) return launch_few<gmm::Cfg<true, 5, true>>(g, d, st);
+        return f8 ? launch_few<gmm::Cfg<true, 8, false>>(g, d, st)
+                  : launch_few<gmm::Cfg<false, 8, false>>(g, d, st);
     }
-    return run_gmm_kind<false>(g, d, st);
+    g.p.idesc += static_cast<uint32_t>(gmm::TILE_W >> 4) << 24;  // M = 256
+    if (g.W2) return launch_pairs<gmm::PairCfg<true, 96, 5, true, 3>>(g, d, st);
+    if (f8)
+        return nt == 128 ? launch_pairs<gmm::PairCfg<true, 128, 7, false, 4>>(g, d, st)
+                         : launch_pairs<gmm::PairCfg<true, 192, 6, false, 3>>(g, d, st);
+    return nt == 128 ? launch_pairs<gmm::PairCfg<false, 128, 7, false, 4>>(g, d, st)
+                     : launch_pairs<gmm::PairCfg<false, 256, 5, false, 3>>(g, d, st);
 }
 
 // --------------------------------------------------------------- quantise

@@ -80,7 +80,7 @@ struct Params {
 template <bool F8_, int NST_, bool GU_>
 struct Cfg {
     static constexpr bool F8 = F8_, GU = GU_;
-    static constexpr int NT = 32, NST = NST_;  // token tile
+    static constexpr int NT = FEW_ROWS, NST = NST_;  // token tile
     static constexpr int NA = GU ? 2 : 1;
     static constexpr int BOX = NT;  // token rows per TMA box
     static constexpr int A_BYTES = TILE_W * KBLK;
