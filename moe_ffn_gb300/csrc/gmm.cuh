@@ -29,10 +29,10 @@
 // bf16 experts of one row, 768 x 2048: 8.4 us, 3.0 TB/s; 128 rows in 64 groups,
 // 2048 x 2048 bf16: 82 us, 6.5 TB/s.
 //
-// Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs,
-// warps 2-3 stage the scale products, warps 4-11 are the epilogue: warp w
-// reads TMEM lanes 32 (w % 4) .. +31, and the two groups of four warps take
-// sixteen columns each.
+// Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs, warp 2
+// stages the scale products (warp 3 has no part: the epilogue's warps start at a
+// multiple of four), warps 4-11 are the epilogue: warp w reads TMEM lanes
+// 32 (w % 4) .. +31, and the two groups of four warps take sixteen columns each.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -82,7 +82,7 @@ struct Cfg {
     static constexpr bool F8 = F8_, GU = GU_;
     static constexpr int NT = FEW_ROWS, NST = NST_;  // token tile
     static constexpr int NA = GU ? 2 : 1;
-    static constexpr int BOX = NT;  // token rows per TMA box
+    static constexpr int BOX = NT;  // a stage's token rows are one TMA box
     static constexpr int A_BYTES = TILE_W * KBLK;
     static constexpr int STAGE = NA * A_BYTES + NT * KBLK;
     static constexpr int CH = 16;  // columns per epilogue warp
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < SC_RING; ++i) {
-            mbar_init(&sc_full[i], 2);
+            mbar_init(&sc_full[i], 1);
             mbar_init(&sc_empty[i], EPI_WARPS);
         }
         for (int i = 0; i < C::NBUF; ++i) {
@@ -295,7 +295,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = !skip;
         for (int t = first; t < tiles && ok; t += step) {
             const Tile w = t == first ? w0 : tile_at_warp(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
-            const int boxes = (w.np + C::BOX - 1) / C::BOX;
             for (int kb = kbeg; kb < kend; ++kb, ++it) {
                 // (before any use of a stage the wait passes at once)
                 if (!mbar_wait_spin(&empty[s], ph, p.err, DEV_GMM_TIMEOUT)) {
@@ -304,19 +303,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (elect_one()) {
                     uint8_t* st = base + s * C::STAGE;
-                    mbar_arrive_expect_tx(&full[s],
-                                          C::NA * C::A_BYTES + boxes * C::BOX * KBLK);
+                    mbar_arrive_expect_tx(&full[s], C::STAGE);
                     // x coordinates are multiples of 128 bytes; rows past the
                     // matrix or past x arrive as zeros
                     const int kx = C::F8 ? kb * KBLK : kb * (KBLK / 2);
                     tma_load_3d(st, &tm_w, kx, w.nbi * TILE_W, w.e, &full[s]);
                     if constexpr (C::GU)
                         tma_load_3d(st + C::A_BYTES, &tm_w2, kx, w.nbi * TILE_W, w.e, &full[s]);
-#pragma unroll
-                    for (int b = 0; b < C::NT / C::BOX; ++b)
-                        if (b < boxes)
-                            tma_load_2d(st + C::NA * C::A_BYTES + b * C::BOX * KBLK, &tm_x, kx,
-                                        w.row0 + b * C::BOX, &full[s]);
+                    tma_load_2d(st + C::NA * C::A_BYTES, &tm_x, kx, w.row0, &full[s]);
                 }
                 __syncwarp();
                 if (++s == C::NST) {
@@ -385,11 +379,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) umma::commit(mma_done);
         __syncwarp();
         mbar_wait_spin(mma_done, 0, p.err, DEV_GMM_TIMEOUT);
-    } else if (warp < 4) {
+    } else if (warp == 2) {
         // --------------------------------------------------------- scales
         if constexpr (C::F8) {
-            const int lt = tid - 64;  // 0..63: token rows lt, lt + 64, ...
-            constexpr int RPT = (C::NT + 63) / 64;
+            static_assert(C::NT == 32, "a token row per lane");
             // rows of scales are read four at a time where they are aligned
             const bool vec = (p.kb & 3) == 0 && (kbeg & 3) == 0 &&
                              (reinterpret_cast<uintptr_t>(p.xs) & 15) == 0;
@@ -398,26 +391,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int t = first; t < tiles && ok; t += step) {
                 const Tile w = t == first ? w0 : tile_at_warp(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
                 const int64_t wo = (static_cast<int64_t>(w.e) * p.nb + w.nbi) * p.kb;
+                const float* xs = p.xs + (static_cast<int64_t>(w.row0) + lane) * p.kb;
                 for (int k0 = kbeg; k0 < kend; k0 += SC_BLK, ++ch) {
-                    float v[RPT][SC_BLK], g[C::NA][SC_BLK];
+                    float v[SC_BLK], g[C::NA][SC_BLK];
 #pragma unroll
                     for (int b = 0; b < SC_BLK; ++b) {
                         g[0][b] = k0 + b < kend ? __ldcg(p.ws + wo + k0 + b) : 0.f;
                         if constexpr (C::GU)
                             g[1][b] = k0 + b < kend ? __ldcg(p.ws2 + wo + k0 + b) : 0.f;
                     }
+                    if (vec && lane < w.nv && k0 + SC_BLK <= kend) {
+                        const float4 q = __ldcg(reinterpret_cast<const float4*>(xs + k0));
+                        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const int j = lt + 64 * i;
-                        const float* src = p.xs + static_cast<int64_t>(w.row0 + j) * p.kb + k0;
-                        if (vec && j < w.nv && k0 + SC_BLK <= kend) {
-                            const float4 q = __ldcg(reinterpret_cast<const float4*>(src));
-                            v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < SC_BLK; ++b)
-                                v[i][b] = j < w.nv && k0 + b < kend ? __ldcg(src + b) : 0.f;
-                        }
+                        for (int b = 0; b < SC_BLK; ++b)
+                            v[b] = lane < w.nv && k0 + b < kend ? __ldcg(xs + k0 + b) : 0.f;
                     }
                     const int s = ch % SC_RING, round = ch / SC_RING;
                     if (round > 0 && !mbar_wait_spin(&sc_empty[s], (round - 1) & 1, p.err,
@@ -427,21 +416,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     float* dst = ring + s * C::SC_STAGE;
 #pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const int j = lt + 64 * i;
-                        if (j < C::NT)
+                    for (int b = 0; b < SC_BLK; ++b)
 #pragma unroll
-                            for (int b = 0; b < SC_BLK; ++b)
-#pragma unroll
-                                for (int a = 0; a < C::NA; ++a)
-                                    dst[(b * C::NA + a) * C::NT + j] = v[i][b] * g[a][b];
-                    }
+                        for (int a = 0; a < C::NA; ++a)
+                            dst[(b * C::NA + a) * C::NT + lane] = v[b] * g[a][b];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_full[s]);
                 }
             }
         }
-    } else {
+    } else if (warp >= 4) {
         // ------------------------------------------------------- epilogue
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const int col = half * C::CH;  // this warp's columns
