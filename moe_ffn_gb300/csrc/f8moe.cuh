@@ -361,7 +361,11 @@ __global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
 // four slots' values before it adds them.  Bound by reading y: for bf16
 // activations y is bf16 (the layer rounds each expert's output once, by at most
 // 2^-8 of it, as out's own rounding is of out; y is the layer's largest traffic),
-// else f32.
+// else f32.  Both sides for bf16 activations, 4096 tokens, hidden 2048, 128
+// experts, top-8, F 768: y in bf16 364 us and 1.77e-3 root mean square error
+// against 64 bits, in f32 459 us and 1.66e-3 (the rounding of out alone); 512
+// tokens, 64 experts, F 1024: 109 us and 1.80e-3 against 125 and 1.66e-3.  A
+// caller who wants f32 sums throughout passes f32 activations.
 constexpr int C_THREADS = 128;
 constexpr int C_AHEAD = 4;
 
@@ -404,15 +408,20 @@ __global__ void __launch_bounds__(C_THREADS) combine_kernel(
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = 0.f;
     for (int s0 = 0; s0 < k; s0 += C_AHEAD) {
+        // (all shuffles before the first load: between loads they kept those apart)
         float v[C_AHEAD][8], ws[C_AHEAD];
+        int r[C_AHEAD];
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s) {
-            const int r = __shfl_sync(0xffffffffu, slot_row, s0 + s);  // -1 past the slots
+            r[s] = __shfl_sync(0xffffffffu, slot_row, s0 + s);  // -1 past the slots
             ws[s] = __shfl_sync(0xffffffffu, slot_w, s0 + s);
-            if (r < 0) ws[s] = 0.f;
+            if (r[s] < 0) ws[s] = 0.f;
+        }
+#pragma unroll
+        for (int s = 0; s < C_AHEAD; ++s) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
-            if (in && r >= 0) load8(y + static_cast<int64_t>(r) * H + c, v[s]);
+            if (in && r[s] >= 0) load8(y + static_cast<int64_t>(r[s]) * H + c, v[s]);
         }
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s)
