@@ -204,15 +204,14 @@ __device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, in
     __syncthreads();
 }
 
-// Waits until the MMAs have handed back the stages of the last `it` loads, a lane
-// per stage; true if they have, and then the copies have landed and the commits'
-// arrivals too.  False at once where the loads had given up (`ok` false).
+// k-blocks of a tile, counted from its end, whose stages no later load takes: the
+// last NST steps of a CTA, `after` of them in tiles to come.  Such a stage is not
+// handed back by a commit, so that every arrival of one is waited for: an arrival
+// comes from the tensor core, no barrier between threads orders it, and the CTA's
+// shared memory may be another launch's as soon as it ends.
 template <int NST>
-__device__ __forceinline__ bool drain_stages(uint64_t* empty, int it, bool ok, DevCtl* err) {
-    const int k = it - 1 - (static_cast<int>(threadIdx.x) & 31);
-    if (ok && k >= 0 && k >= it - NST)
-        ok = mbar_wait_spin(&empty[k % NST], (k / NST) & 1, err, DEV_GMM_TIMEOUT);
-    return __all_sync(0xffffffffu, ok);
+__device__ __forceinline__ int unreturned(int64_t after) {
+    return after < NST ? NST - static_cast<int>(after) : 0;
 }
 
 template <class C>
@@ -319,10 +318,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
-        // never leave with copies or a commit's arrival in flight
-        if (!drain_stages<C::NST>(empty, it, ok, p.err))
-            for (int k = max(it - C::NST, 0); k < it; ++k)
-                mbar_wait_spin(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
+        // never leave with copies in flight
+        for (int k = max(it - C::NST, 0); k < it; ++k)
+            mbar_wait_spin(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
         int s = 0;
@@ -334,6 +332,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int t = first; t < tiles && ok; t += step) {
             const Tile w = t == first ? w0 : tile_at_warp(t, C::NT, 16, t_lo, t_hi, t_pre, p.E);
             const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
+            const int ret = kend - unreturned<C::NST>(
+                                       static_cast<int64_t>((tiles - 1 - t) / step) * (kend - kbeg));
 #pragma unroll 1
             for (int kb = kbeg; kb < kend; ++kb) {
                 const bool fresh = C::F8 || kb == kbeg;  // a new accumulator buffer
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                                  lo + a * (C::A_BYTES >> 4) + 2 * j,
                                                  lo + C::NA * (C::A_BYTES >> 4) + 2 * j, hi, idesc,
                                                  (!fresh || j > 0) ? 1u : 0u);
-                    umma::commit(&empty[s]);
+                    if (kb < ret) umma::commit(&empty[s]);
                     if (last) umma::commit(&acc_full[ab]);
                 }
                 __syncwarp();

@@ -281,10 +281,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
             }
-            // never leave with copies or a commit's arrival in flight: the MMA warp
-            // signals both CTAs' stages, and no barrier between threads orders the
-            // tensor core's arrivals
-            if (wgt && !drain_stages<C::NST>(empty, it, ok, p.err) && rank == 0)
+            // never leave with copies in flight (the pair's: the other CTA
+            // leaves only after the cluster barrier at the end)
+            if (wgt && rank == 0)
                 for (int k = max(it - C::NST, 0); k < it; ++k)
                     mbar_wait_spin(&full[k % C::NST], (k / C::NST) & 1, p.err, DEV_GMM_TIMEOUT);
         } else if (warp == 1 && rank == 0) {
@@ -299,6 +298,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
             for (int t = first; t < tiles && ok; t += step) {
                 const Tile w = tile_at_warp(t, C::NT, 32, t_lo, t_hi, t_pre, p.E);
                 const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.np >> 3) << 17);
+                const int ret = p.kb - unreturned<C::NST>(
+                                           static_cast<int64_t>((tiles - 1 - t) / step) * p.kb);
                 if constexpr (!C::F8) ab = (ab + 1) % C::NBUF;
 #pragma unroll 1
                 for (int k0 = 0; k0 < p.kb && ok; k0 += C::NBUF) {
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
                                     const uint32_t bj = lo + C::NA * (C::A_BYTES >> 4) + 2 * j;
                                     umma::mma_pair<C::F8>(d + a * C::NT, aj, bj, hi, idesc, acc);
                                 }
-                            umma::commit_pair(&empty[s]);
+                            if (k0 + k < ret) umma::commit_pair(&empty[s]);
                             if (last) umma::commit_pair(&acc_full[ab]);
                         }
                         __syncwarp();

@@ -20,9 +20,6 @@ def between(text, a, b):
     return text[i:text.index(b, i)]
 
 
-DRAIN = "drain_stages<C::NST>(empty, it, ok, p.err)"
-
-
 def test_no_cta_leaves_with_a_commit_in_flight():
     """A commit's arrival comes from the tensor core, so no barrier between
     threads orders it: every barrier that a commit signals is waited for, in
@@ -31,9 +28,9 @@ def test_no_cta_leaves_with_a_commit_in_flight():
     pair = code("gmm_pair.cuh")
     signalled = set(re.findall(r"umma::commit_pair\(&?(\w+)", pair))
     assert signalled == {"empty", "acc_full", "mma_done"}
-    # stages: the weight-load warp of either CTA, at the end of its loop
-    loads = between(pair, "if (warp == 0 || warp == 2) {", "else if (warp == 1 && rank == 0)")
-    assert f"if (wgt && !{DRAIN}" in loads
+    # stages: handed back only where a later load waits for them
+    assert pair.count("commit_pair(&empty") == pair.count(
+        "if (k0 + k < ret) umma::commit_pair(&empty[s])") == 1
     # accumulators: every epilogue warp of either CTA, before each use
     epilogue = pair[pair.index("regs_inc<C::REGS_EPI>()"):]
     assert epilogue.count("mbar_wait_spin(&acc_full[ab]") == 2  # one per form
@@ -46,10 +43,31 @@ def test_no_cta_leaves_with_a_commit_in_flight():
 
     one = code("gmm.cuh")
     assert set(re.findall(r"umma::commit\(&?(\w+)", one)) == {"empty", "acc_full", "mma_done"}
-    assert DRAIN in between(one, "if (warp == 0) {", "else if (warp == 1)")
-    body = between(one, "bool drain_stages(", "__global__")
-    assert "mbar_wait_spin(&empty[k % NST], (k / NST) & 1" in body and "__all_sync" in body
+    assert one.count("commit(&empty") == one.count("if (kb < ret) umma::commit(&empty[s])") == 1
     assert one.index("commit(mma_done)") < one.index("mbar_wait_spin(mma_done")
+
+
+def test_stages_are_handed_back_exactly_where_a_load_waits():
+    """The arithmetic of unreturned() over whole runs of a CTA: step i of n hands
+    its stage back exactly if a load i + NST follows, which waits for it."""
+    text = code("gmm.cuh")
+    assert "return after < NST ? NST - static_cast<int>(after) : 0;" in text
+    for name, first, last in (("gmm.cuh", "kend", "kend - kbeg"), ("gmm_pair.cuh", "p.kb", "p.kb")):
+        expr = (f"const int ret = {first} - unreturned<C::NST>( "
+                f"static_cast<int64_t>((tiles - 1 - t) / step) * ")
+        assert expr + (f"({last}))" if "-" in last else f"{last})") in code(name)
+    for nst in (5, 6, 7, 8):
+        for kb in (1, 2, 3, nst - 1, nst, nst + 1, 2 * nst + 1):
+            for first, step, tiles in ((0, 1, 1), (0, 1, 2), (1, 3, 2), (2, 3, 12), (0, 5, 26)):
+                own = range(first, tiles, step)
+                n = len(own) * kb
+                i = 0
+                for t in own:
+                    after = (tiles - 1 - t) // step * kb
+                    ret = kb - (nst - after if after < nst else 0)
+                    for k in range(kb):
+                        assert (k < ret) == (i + nst < n), (nst, kb, t, k)
+                        i += 1
 
 
 def test_no_read_only_loads_of_stream_ordered_data():
