@@ -336,9 +336,10 @@ qmoe_status f8_quantize(int xtype, const void* x, int64_t rows, int64_t cols, in
  *   b of the codes' products)
  * The inner sums run on the tensor cores, products exact and sums in f32; the
  * outer sum is f32, and y is rounded once.  The product of two scales is
- * formed in f32 first, so it has to be finite there.  For
- * a few tokens the CTAs of a cluster share a row tile's K range and their
- * parts are added in a fixed order.
+ * formed in f32 first: it has to be finite there, and below 2^-126 it is a
+ * subnormal with fewer bits (0 below 2^-150), whatever the inner sum makes of
+ * it.  For a few tokens the CTAs of a cluster share a row tile's K range and
+ * their parts are added in a fixed order.
  *   W        [rows][cols] e4m3, contiguous, 16-byte aligned;  w_scale f32
  *   rows     1..2^31-257;  cols  1..2^20, a multiple of 16 (else UNSUPPORTED)
  *   x        [n_tokens][cols] e4m3, rows ldx apart (ldx >= cols, a multiple of
@@ -379,8 +380,10 @@ size_t moe_experts_f8_workspace_size(const qmoe_moe_shape* shape);
  *   a = silu(G_e xq) * (U_e xq) in f32,  aq = f8_quantize(a),
  *   out_t = residual_t + sum_s topk_w[t][s] * (D_e aq)
  * with sums in f32 and one rounding into out; for QMOE_BF16, D_e aq is rounded
- * to bf16 before its weight multiplies it.  topk_idx and topk_w are as moe_ffn
- * returns them; any other routing rule may supply them.
+ * to bf16 before its weight multiplies it (QMOE_F32 and QMOE_F16 keep it in
+ * f32).  The library has no router for these stacks: the caller supplies
+ * topk_idx and topk_w, in the layout in which moe_ffn writes its own, by any
+ * routing rule.
  *   gate_stack, up_stack  [E][F][H] e4m3;  scales [E][F/128][H/128]
  *   down_stack            [E][H][F] e4m3;  scales [E][H/128][F/128]
  *   shape       hidden and expert_dim multiples of 128, num_experts <= 256,

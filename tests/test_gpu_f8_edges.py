@@ -113,3 +113,28 @@ def swiglu_case(qm, tokens, blocks, probe, gates, up):
     ids=["positive", "negative", "large", "small", "far", "far_mixed"])
 def test_swiglu_over_its_range(qm, tokens, blocks, probe, gates, up):
     swiglu_case(qm, tokens, blocks, probe, gates, up)
+
+
+@pytest.mark.parametrize("m,n", [(3, 200), (300, 2100)], ids=["few_rows", "pairs"])
+def test_scale_products_below_the_normal_range(qm, m, n):
+    """The product of two scales is an f32 of its own: below 2^-126 it is a
+    subnormal with fewer bits, and 0 below 2^-150.  y is the sum with that product,
+    not with the exact one.  One block of K, so the inner sum times one product."""
+    import torch
+    g = np.random.default_rng(83)
+    k = 128
+    xq, _, wq, _, _, _ = f8_operands(g, m, n, k)
+    xs = np.exp2(g.uniform(-90, -60, (m, 1))).astype(np.float32)
+    ws = np.exp2(g.uniform(-75, -40, (1, -(-n // 128), 1))).astype(np.float32)
+    xs[0], xs[1] = np.float32(2.0 ** -80), np.float32(2.0 ** -126)
+    ws[0, 0] = np.float32(1.7 * 2.0 ** -60)  # row 0: 1.7 x 2^-140; row 1: 0
+    y = out_tensor(m, n, torch.float32)
+    qm.f8_mm(dev(wq[0]), dev(ws[0]), n, k, dev(xq), dev(xs), m, qm.F32, y)
+    assert qm.device_status() == qm.OK
+    with np.errstate(under="ignore"):
+        sp = (xs * np.repeat(ws[0], 128, axis=0)[:n, 0][None, :]).astype(np.float32)
+    sp = sp.astype(np.float64)
+    assert (sp[1, :128] == 0).all() and ((sp > 0) & (sp < 2.0 ** -126)).any()
+    xv, wv = ref.TABLE[xq], ref.TABLE[wq[0]]
+    s, err = ref.product(xv, wv, ref.f8_terms(k))
+    check(f64(y), s * sp, ref.rounded(s * sp, err * sp, "f32"), "subnormal scale products")
