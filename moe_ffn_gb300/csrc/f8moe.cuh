@@ -357,8 +357,10 @@ __global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
 
 // ----------------------------------------------------------------- combine
 // out[t] = residual[t] + sum_s w[t][s] y[pos[t][s]], summed in f32 in slot
-// order and rounded once.  A thread takes eight columns of one token and loads
-// four slots' values before it adds them.  Bound by reading y: for bf16
+// order and rounded once.  A thread takes eight columns of one token and eight
+// slots at a step (1 / 512 / 4096 tokens of top-8, cold: 5.7 / 7.4 / 28 us; four at
+// a step 6.3 / 7.9 / 29; rows and weights of the slots loaded by every thread
+// instead of once per warp 7.6 / 9.2 / 39).  Bound by reading y: for bf16
 // activations y is bf16 (the layer rounds each expert's output once, by at most
 // 2^-8 of it, as out's own rounding is of out; y is the layer's largest traffic),
 // else f32.  Both sides for bf16 activations, 4096 tokens, hidden 2048, 128
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
 // tokens, 64 experts, F 1024: 109 us and 1.80e-3 against 125 and 1.66e-3.  A
 // caller who wants f32 sums throughout passes f32 activations.
 constexpr int C_THREADS = 128;
-constexpr int C_AHEAD = 4;
+constexpr int C_AHEAD = 8;
 
 template <class T>
 __device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
@@ -408,8 +410,8 @@ __global__ void __launch_bounds__(C_THREADS) combine_kernel(
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = 0.f;
     for (int s0 = 0; s0 < k; s0 += C_AHEAD) {
-        // (all shuffles before the first load: between loads they kept those apart)
-        float v[C_AHEAD][8], ws[C_AHEAD];
+        Raw8<Y> v[C_AHEAD];
+        float ws[C_AHEAD];
         int r[C_AHEAD];
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s) {
@@ -419,14 +421,13 @@ __global__ void __launch_bounds__(C_THREADS) combine_kernel(
         }
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
-            if (in && r[s] >= 0) load8(y + static_cast<int64_t>(r[s]) * H + c, v[s]);
+            v[s].zero();
+            if (in && r[s] >= 0) v[s].load(y + static_cast<int64_t>(r[s]) * H + c);
         }
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = fmaf(ws[s], v[s][i], a[i]);
+            for (int i = 0; i < 8; ++i) a[i] = fmaf(ws[s], v[s].get(i), a[i]);
     }
     if (!in) return;
     if (residual) {
