@@ -4,8 +4,9 @@
 // max|x| <= 448 s (448 is the largest e4m3 value).  A power of two, because
 // x / s is then exact and e4m3's own exponent loses nothing by it: a normal
 // code keeps the same four significant bits whatever the power; only values
-// below 2^-6 s (the subnormal codes, at most 2^-14 of the block's largest)
-// are coarser than with s = max|x| / 448, by at most one bit.
+// below 2^-6 s (the subnormal codes; the block's largest exceeds 224 s unless k
+// is -126, so at most 2^-13.8 of it) are coarser than with s = max|x| / 448, by
+// at most one bit.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>

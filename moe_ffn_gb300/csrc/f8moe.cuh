@@ -26,7 +26,7 @@ __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 // one or two 16-byte loads, a four-step maximum, one 8-byte store.  They take
 // RUN neighbouring blocks of a row, all loaded before the first is reduced.
 // Bound by HBM, (size + 1) bytes per element: RUN = 4 keeps 64 bytes per thread
-// in flight (4096 x 14336 bf16: 34 us, 5.3 TB/s; with RUN = 1 48 us); RUN = 1
+// in flight (4096 x 14336 bf16: 29 us, 6.2 TB/s; with RUN = 1 42 us); RUN = 1
 // spreads few rows over more threads (1 x 2048: 1.7 against 2.6 us).  VEC needs 16-byte aligned
 // rows and whole groups of eight columns; the other form loads element by
 // element.

@@ -24,10 +24,10 @@
 // distributed shared memory, in rank order.  gmm_pair.cuh has the kernel for
 // many rows.
 //
-// Measured: 1 x 4096 x 4096 e4m3 6.5 us (fixed latency: about 2,500 clocks to
+// Measured: 1 x 4096 x 4096 e4m3 6.6 us (fixed latency: about 2,500 clocks to
 // the first copy, 1,300 for its data, 3,000 from the last MMA to the end); eight
-// bf16 experts of one row, 768 x 2048: 8.4 us, 3.0 TB/s; 128 rows in 64 groups,
-// 2048 x 2048 bf16: 82 us, 6.5 TB/s.
+// bf16 experts of one row, 768 x 2048: 8.6 us, 2.9 TB/s; 128 rows in 64 groups,
+// 2048 x 2048 bf16: 81 us, 6.7 TB/s.
 //
 // Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs, warp 2
 // stages the scale products (warp 3 has no part: the epilogue's warps start at a

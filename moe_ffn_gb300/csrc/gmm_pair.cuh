@@ -16,25 +16,31 @@
 // 256-column k-block of 512 clocks).  Measured over 12 warps: 32x32b 439,
 // 16x128b 431, 16x256b 255 bytes per clock.
 //
-// What bounds the e4m3 form is shared memory: per k-block the MMAs read both
-// operands, the copies write them and the epilogue reads scales, 92 KB for 192
-// columns (720 clocks at 128 bytes per clock, against 384 of MMA).  Narrower
-// tiles read the weight rows more often: four buffers of 128 columns took 760
-// clocks per 128.  256 columns do not leave the epilogue's threads the
-// registers: 64 sums, a fragment of 32 values and its scales without spilling
-// take 512 threads (any spill in these loops cost 15 to 30 percent).
+// No pipe bounds the e4m3 form; what is left is the epilogue's chain from one
+// accumulator buffer to the next (wait, TMEM read, scales, 64 FMAs per thread,
+// arrival).  2048 x 4096 x 4096, the busiest SM: 1,155 clocks per k-block of 192 columns, of
+// which the tensor pipe is busy 43%, the issue slots 66%.  Shared memory could
+// serve it: by the counters the MMAs read 221 wavefronts per k-block (this CTA's
+// weight rows and its half of the token rows), scales and staging take 296, and
+// the copies write 28 KB, 744 clocks even if they took turns.  Narrower tiles read
+// the weight rows more often: four buffers of 128 columns took 760 clocks per 128.
+// 256 columns do not leave the epilogue's threads the registers: 64 sums, a
+// fragment of 32 values and its scales without spilling take 512 threads (any
+// spill in these loops cost 15 to 30 percent).
 //
 // So a wide tile with few epilogue warps is for many rows per group; where
 // groups fill at most 128 columns, or wide tiles leave pairs idle, four buffers
-// and sixteen warps are faster (the rule and both sides' times: gmm_tiles.cuh).  The 16-bit form is
-// bound by shared memory too: 80 KB per 128 bytes of K are 625 clocks, 650
-// measured, against 513 of MMA.
+// and sixteen warps are faster (the rule and both sides' times: gmm_tiles.cuh).
 //
-// Measured: f16, 16,384 rows in 8 groups, 4096 x 4096: 334 to 344 us, 1600 to
-// 1650 TFLOP/s, in short runs; 379 us in long ones, where the power limit lowers
-// the clock to 1.4 GHz; e4m3, 4096 x 14336 x 4096: 300 us, 1600 TFLOP/s, at full
-// clock in either; 64 groups of about 64 rows,
-// 1024 x 2048 e4m3: 32 us, 4.3 TB/s.
+// The 16-bit form is bound by the tensor pipe: busy 81% of a launch of 16,384 rows
+// and 87% on the busiest SM of 2048 x 4096 x 4096, the fill of the pipeline and the
+// last stores included.
+//
+// Measured: f16, 16,384 rows in 8 groups, 4096 x 4096: 327 to 345 us, 1590 to
+// 1680 TFLOP/s, in short runs; 370 to 399 us in long ones, where the power limit
+// lowers the clock to 1.36-1.46 GHz; e4m3, 4096 x 14336 x 4096: 301 us, 1600
+// TFLOP/s, at full clock in either; 64 groups of about 64 rows, 1024 x 2048 e4m3:
+// 32 us, 4.3 TB/s.
 //
 // Roles: warps 0 and 2 load, warp 1 (of the first CTA) issues the MMAs, warp 3
 // stages scale products, the warps from 4 on are the epilogue: warp w reads
