@@ -405,13 +405,137 @@ qmoe_status moe_experts_f8(const void* gate_stack, const float* gate_scale, cons
                            const int32_t* topk_idx, const float* topk_w, const void* residual,
                            void* out, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The steps of an MoE layer around its experts' products, with their gradients,
+ * and products with 4-bit weights.  The pages have no counterpart of these
+ * calls; the conventions are those of the section above.  With them
+ *   moe_route -> moe_permute -> mm_grouped or w4_mm_grouped (gate, up; down)
+ *   -> moe_combine
+ * is a layer for weights that moe_ffn does not take; moe_route also makes the
+ * routes that moe_experts_f8 asks for.  Limits common to the steps: num_experts
+ * <= 1024, top_k <= 16, n_tokens * top_k <= 2^25, cols <= 2^20. */
+
+/* Routes from the router's logits, by moe_ffn's rule (see there for ties and
+ * logits that are not finite): p = softmax over the experts, the top_k largest,
+ * ties to the lower index, weights p_e renormalised over those, or p_e itself
+ * with QMOE_ROUTE_NO_RENORM.  An expert masked by a logit of -inf is taken only
+ * when too few others are left, with weight 0.
+ *   ltype       QMOE_F32, QMOE_BF16 or QMOE_F16
+ *   logits      [n_tokens][num_experts], rows ldl elements apart, aligned to its
+ *               element
+ *   top_k       1..num_experts
+ *   topk_idx    [n_tokens][top_k] int32, experts in rank order
+ *   topk_w      [n_tokens][top_k] f32
+ * Errors: INVALID_ARGUMENT (null, sizes, alignment, flags), UNSUPPORTED (ltype,
+ * limits, device), CUDA. */
+qmoe_status moe_route(int ltype, const void* logits, int64_t n_tokens, int32_t num_experts,
+                      int64_t ldl, int32_t top_k, int32_t route_flags, int32_t* topk_idx,
+                      float* topk_w, void* stream);
+
+/* Gradient of the logits from that of the weights, topk_idx and topk_w as
+ * moe_route wrote them.  With c = sum_s w_s grad_w_s over the token's slots:
+ *   renormalised   grad_logits[e_s] = w_s (grad_w_s - c), 0 elsewhere
+ *   NO_RENORM      grad_logits[e] = p_e (grad_w_s [e = e_s] - c), p formed again
+ *                  from the logits (which the renormalised form does not read)
+ * in f32, rounded once to ltype.  Every element of the [n_tokens][num_experts]
+ * gradient (rows ldg apart) is written.  A slot whose expert lies outside
+ * [0, num_experts) adds nothing; an expert that two slots name takes both. */
+qmoe_status moe_route_backward(int ltype, const void* logits, int64_t n_tokens,
+                               int32_t num_experts, int64_t ldl, int32_t top_k,
+                               int32_t route_flags, const int32_t* topk_idx, const float* topk_w,
+                               const float* grad_w, void* grad_logits, int64_t ldg, void* stream);
+
+/* Bytes of workspace moe_permute needs; 0 (with a message) for sizes it
+ * refuses. */
+size_t moe_permute_workspace_size(int64_t n_tokens, int32_t num_experts, int32_t top_k);
+
+/* The tokens' rows sorted by expert: the (token, slot) pairs in order of their
+ * experts, equal experts in order of the pairs (t * top_k + s), and
+ *   rows[pos[t][s]] = x[t]
+ *   topk_idx    [n_tokens][top_k] int32; a slot outside [0, num_experts) has no
+ *               row (padding); an expert may appear twice in a token, and top_k
+ *               may exceed num_experts
+ *   xtype       QMOE_F32, QMOE_BF16 or QMOE_F16
+ *   x           [n_tokens][cols], rows ldx elements apart
+ *   rows        [n_tokens * top_k][cols], rows ldr apart; rows behind the last
+ *               pair's, and elements between rows, are left as they were
+ *   offsets     [num_experts + 1] int32: the rows of expert e are offsets[e] to
+ *               offsets[e + 1] (mm_grouped's offsets); all 0 without tokens
+ *   pos         [n_tokens][top_k] int32: each pair's row, or -1
+ *   ws          >= moe_permute_workspace_size bytes, 16-byte aligned scratch;
+ *               calls that overlap on the GPU must not share one (nor may two
+ *               graphs that are replayed at the same time)
+ * No output may overlap an input.  The gradient of x is moe_combine of the rows'
+ * gradient with topk_w and residual null.  Errors as moe_route. */
+qmoe_status moe_permute(int xtype, const void* x, int64_t n_tokens, int64_t cols, int64_t ldx,
+                        const int32_t* topk_idx, int32_t num_experts, int32_t top_k, void* rows,
+                        int64_t ldr, int32_t* offsets, int32_t* pos, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* out[t] = residual[t] + sum_s topk_w[t][s] y[pos[t][s]], summed in f32 in slot
+ * order, the residual last, and rounded once.
+ *   ytype, otype  QMOE_F32, QMOE_BF16 or QMOE_F16, of y and of residual and out
+ *   y           [n_rows][cols], rows ldy elements apart
+ *   pos         [n_tokens][top_k] int32; a slot whose row lies outside
+ *               [0, n_rows) adds nothing, whatever its weight
+ *   topk_w      [n_tokens][top_k] f32, used as given, or NULL for ones
+ *   residual    [n_tokens][cols], or NULL for zeros;  out, may be residual
+ *               itself; rows of both ldo apart
+ * out must not overlap y.  Errors as moe_route. */
+qmoe_status moe_combine(int ytype, const void* y, int64_t n_rows, int64_t cols, int64_t ldy,
+                        const int32_t* pos, const float* topk_w, int64_t n_tokens, int32_t top_k,
+                        int otype, const void* residual, void* out, int64_t ldo, void* stream);
+
+/* Gradients of moe_combine (that of the residual is grad_out itself):
+ *   grad_y[pos[t][s]] = topk_w[t][s] grad_out[t]         (ytype, rounded once)
+ *   grad_w[t][s] = sum_c y[pos[t][s]][c] grad_out[t][c]  (f32; 0 without a row)
+ *   grad_out    [n_tokens][cols] of otype, rows ldo apart
+ *   grad_y      [n_rows][cols], rows ldg apart, or NULL; rows that no slot names
+ *               are left as they were
+ *   grad_w      [n_tokens][top_k] f32, or NULL (y is then not read and may be
+ *               NULL)
+ * A row may be named by one slot only, as moe_permute leaves it: of several, one
+ * gives the row's gradient, and which is not said.  No gradient may overlap an
+ * input.  Other arguments as moe_combine; errors as moe_route. */
+qmoe_status moe_combine_backward(int ytype, const void* y, int64_t n_rows, int64_t cols,
+                                 int64_t ldy, const int32_t* pos, const float* topk_w,
+                                 int64_t n_tokens, int32_t top_k, int otype, const void* grad_out,
+                                 int64_t ldo, void* grad_y, int64_t ldg, float* grad_w,
+                                 void* stream);
+
+/* y[t][i] = sum_j W[i][j] x[t][j] with 4-bit weights,
+ *   W[i][j] = scale[i][j / scale_cols] (code[i][j] - zero[i][j / scale_cols])
+ *   W           [rows][cols / 2] bytes, contiguous, 16-byte aligned: code j in the
+ *               low half of byte j / 2 if j is even, else in the high half
+ *   scale_cols  32, 64 or 128;  cols  a multiple of it, <= 2^20
+ *   scale       [rows][cols / scale_cols] of stype: QMOE_F32, QMOE_BF16, QMOE_F16
+ *   zero        [rows][cols / scale_cols] bytes of 0..15 (the low four bits are
+ *               taken), or NULL: 8 everywhere
+ *   xtype       QMOE_F32, QMOE_BF16 or QMOE_F16
+ *   x           [n_tokens][cols], rows ldx elements apart, aligned to its element
+ *   ytype, y    as f8_mm
+ * Products of (code - zero) and x are exact, sums and scales f32, and y is
+ * rounded once.  For few tokens (one to some tens: the weights are read once for
+ * every 64).  Errors as f8_quantize. */
+qmoe_status w4_mm(const void* W, int stype, const void* scale, const uint8_t* zero,
+                  int32_t scale_cols, int64_t rows, int64_t cols, int xtype, const void* x,
+                  int64_t n_tokens, int64_t ldx, int ytype, void* y, int64_t ldy, void* stream);
+
+/* The same for a stack of num_groups matrices (W, scale and zero one after
+ * another) and ragged groups of rows: y[r] = W_g x[r], offsets[g] <= r <
+ * offsets[g+1].  num_groups, n_rows, offsets and bad offsets as mm_grouped. */
+qmoe_status w4_mm_grouped(const void* W, int stype, const void* scale, const uint8_t* zero,
+                          int32_t scale_cols, int32_t num_groups, int64_t rows, int64_t cols,
+                          int xtype, const void* x, int64_t n_rows, int64_t ldx,
+                          const int32_t* offsets, int ytype, void* y, int64_t ldy, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word: QMOE_ERR_TIMEOUT if a bounded device wait expired since the last
  * read (a pipeline stage, or a grid barrier that not every CTA reached);
  * QMOE_ERR_UNSUPPORTED if the many-token MoE path met a decoded gate/up
  * weight outside f16 range, or a quantized product met an activation of
  * magnitude 2^106 or more (the output is then not valid);
- * QMOE_ERR_INVALID_ARGUMENT if mm_grouped met bad offsets; QMOE_ERR_CUDA if
+ * QMOE_ERR_INVALID_ARGUMENT if mm_grouped or w4_mm_grouped met bad offsets; QMOE_ERR_CUDA if
  * the stream reported an error, or if an internal invariant of the routing
  * failed (an expert index outside [0, E) was clamped to 0); else QMOE_OK. */
 qmoe_status qmoe_device_status(void* stream);

@@ -37,7 +37,7 @@ STATUS_NAMES = {0: "OK", 1: "INVALID_ARGUMENT", 2: "UNSUPPORTED", 3: "CUDA", 4: 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-ftz=false",
               "-std=c++17", "-Xcompiler", "-fPIC"]
 # Translation units of libqmoe.so, compiled in parallel and linked together.
-UNITS = ("qmoe.cu", "batch.cu", "f8.cu")
+UNITS = ("qmoe.cu", "batch.cu", "f8.cu", "moe_steps.cu", "w4.cu")
 
 
 class QmoeError(RuntimeError):
@@ -124,6 +124,24 @@ SIGNATURES = {
     "moe_experts_f8_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(_Shape)]),
     "moe_experts_f8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.POINTER(_Shape),
                                       ctypes.c_int, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_route": (ctypes.c_int, [ctypes.c_int, _P, _I64, ctypes.c_int32, _I64, ctypes.c_int32,
+                                 ctypes.c_int32, _P, _P, _P]),
+    "moe_route_backward": (ctypes.c_int, [ctypes.c_int, _P, _I64, ctypes.c_int32, _I64,
+                                          ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _I64,
+                                          _P]),
+    "moe_permute_workspace_size": (ctypes.c_size_t, [_I64, ctypes.c_int32, ctypes.c_int32]),
+    "moe_permute": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, _P, ctypes.c_int32,
+                                   ctypes.c_int32, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_combine": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, _P, _P, _I64,
+                                   ctypes.c_int32, ctypes.c_int, _P, _P, _I64, _P]),
+    "moe_combine_backward": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, _P, _P, _I64,
+                                            ctypes.c_int32, ctypes.c_int, _P, _I64, _P, _I64, _P,
+                                            _P]),
+    "w4_mm": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, ctypes.c_int32, _I64, _I64, ctypes.c_int,
+                             _P, _I64, _I64, ctypes.c_int, _P, _I64, _P]),
+    "w4_mm_grouped": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, ctypes.c_int32, ctypes.c_int32,
+                                     _I64, _I64, ctypes.c_int, _P, _I64, _I64, _P, ctypes.c_int,
+                                     _P, _I64, _P]),
     "qmoe_device_status": (ctypes.c_int, [_P]),
     "qmoe_set_exec_mode": (ctypes.c_int, [ctypes.c_int]),
     "qmoe_set_fault_injection": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_int]),
@@ -269,7 +287,7 @@ def moe_ffn_noalloc(router_W, gate_stack, up_stack, down_stack, shape: _Shape, x
 # One-token calls take a few microseconds on the GPU, so these functions keep
 # their own cost low: cheap tensor checks, and the current device and stream
 # asked of torch once per call.
-_I32 = -1
+_I32, _U8 = -1, -2
 _DTYPES = {}
 
 
@@ -279,7 +297,7 @@ def _context(stream):
     if not _DTYPES:
         _DTYPES.update({F32: (torch.float32,), BF16: (torch.bfloat16,), F16: (torch.float16,),
                         E4M3: (torch.float8_e4m3fn, torch.uint8, torch.int8),
-                        _I32: (torch.int32,)})
+                        _I32: (torch.int32,), _U8: (torch.uint8,)})
     dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
@@ -408,6 +426,132 @@ def moe_experts_f8(gate_stack, gate_scale, up_stack, up_scale, down_stack, down_
         _arg(fn, "x", x, xtype, TH, dev), _arg(fn, "topk_idx", topk_idx, _I32, P, dev),
         _arg(fn, "topk_w", topk_w, F32, P, dev), _arg(fn, "residual", residual, xtype, TH, dev),
         _arg(fn, "out", out, xtype, TH, dev), _arg(fn, "ws", ws, None, ws_need, dev), ws_bytes, st))
+
+
+# ------------------- steps around the experts' products (include/qmoe.h)
+def moe_route(ltype: int, logits, n_tokens: int, num_experts: int, top_k: int, topk_idx, topk_w,
+              renormalize: bool = True, ldl=None, stream=None) -> None:
+    """topk_idx, topk_w = the top-k experts of each token's logits and their softmax
+    weights (see include/qmoe.h)."""
+    fn, ldl = "moe_route", num_experts if ldl is None else ldl
+    dev, st = _context(stream)
+    P = n_tokens * top_k
+    _check((_libh or lib()).moe_route(
+        ltype, _arg(fn, "logits", logits, ltype, _span(n_tokens, num_experts, ldl), dev, ldl),
+        n_tokens, num_experts, ldl, top_k, 0 if renormalize else ROUTE_NO_RENORM,
+        _arg(fn, "topk_idx", topk_idx, _I32, P, dev), _arg(fn, "topk_w", topk_w, F32, P, dev), st))
+
+
+def moe_route_backward(ltype: int, logits, n_tokens: int, num_experts: int, top_k: int, topk_idx,
+                       topk_w, grad_w, grad_logits, renormalize: bool = True, ldl=None, ldg=None,
+                       stream=None) -> None:
+    """grad_logits from the gradient of moe_route's weights (see include/qmoe.h)."""
+    fn = "moe_route_backward"
+    ldl, ldg = num_experts if ldl is None else ldl, num_experts if ldg is None else ldg
+    dev, st = _context(stream)
+    P = n_tokens * top_k
+    _check((_libh or lib()).moe_route_backward(
+        ltype, _arg(fn, "logits", logits, ltype, _span(n_tokens, num_experts, ldl), dev, ldl),
+        n_tokens, num_experts, ldl, top_k, 0 if renormalize else ROUTE_NO_RENORM,
+        _arg(fn, "topk_idx", topk_idx, _I32, P, dev), _arg(fn, "topk_w", topk_w, F32, P, dev),
+        _arg(fn, "grad_w", grad_w, F32, P, dev),
+        _arg(fn, "grad_logits", grad_logits, ltype, _span(n_tokens, num_experts, ldg), dev, ldg),
+        ldg, st))
+
+
+def moe_permute_workspace_size(n_tokens: int, num_experts: int, top_k: int) -> int:
+    n = int(lib().moe_permute_workspace_size(n_tokens, num_experts, top_k))
+    if n == 0:
+        raise QmoeError(ERR_INVALID_ARGUMENT, last_error())
+    return n
+
+
+def moe_permute(xtype: int, x, n_tokens: int, cols: int, topk_idx, num_experts: int, top_k: int,
+                rows, offsets, pos, ws, ldx=None, ldr=None, ws_bytes=None, stream=None) -> None:
+    """rows[pos[t][s]] = x[t], the rows sorted by expert (see include/qmoe.h)."""
+    fn = "moe_permute"
+    ldx, ldr = cols if ldx is None else ldx, cols if ldr is None else ldr
+    ws_need = 0
+    if ws_bytes is None:
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    elif ws is not None and not isinstance(ws, int):
+        ws_need = -(-ws_bytes // ws.element_size())
+    dev, st = _context(stream)
+    P = n_tokens * top_k
+    _check((_libh or lib()).moe_permute(
+        xtype, _arg(fn, "x", x, xtype, _span(n_tokens, cols, ldx), dev, ldx), n_tokens, cols, ldx,
+        _arg(fn, "topk_idx", topk_idx, _I32, P, dev), num_experts, top_k,
+        _arg(fn, "rows", rows, xtype, _span(P, cols, ldr), dev, ldr), ldr,
+        _arg(fn, "offsets", offsets, _I32, num_experts + 1, dev),
+        _arg(fn, "pos", pos, _I32, P, dev), _arg(fn, "ws", ws, None, ws_need, dev), ws_bytes, st))
+
+
+def moe_combine(ytype: int, y, n_rows: int, cols: int, pos, topk_w, n_tokens: int, top_k: int,
+                otype: int, residual, out, ldy=None, ldo=None, stream=None) -> None:
+    """out[t] = residual[t] + sum_s topk_w[t][s] y[pos[t][s]] (see include/qmoe.h)."""
+    fn = "moe_combine"
+    ldy, ldo = cols if ldy is None else ldy, cols if ldo is None else ldo
+    dev, st = _context(stream)
+    P, TH = n_tokens * top_k, _span(n_tokens, cols, ldo)
+    _check((_libh or lib()).moe_combine(
+        ytype, _arg(fn, "y", y, ytype, _span(n_rows, cols, ldy), dev, ldy), n_rows, cols, ldy,
+        _arg(fn, "pos", pos, _I32, P, dev), _arg(fn, "topk_w", topk_w, F32, P, dev), n_tokens,
+        top_k, otype, _arg(fn, "residual", residual, otype, TH, dev, ldo),
+        _arg(fn, "out", out, otype, TH, dev, ldo), ldo, st))
+
+
+def moe_combine_backward(ytype: int, y, n_rows: int, cols: int, pos, topk_w, n_tokens: int,
+                         top_k: int, otype: int, grad_out, grad_y, grad_w, ldy=None, ldo=None,
+                         ldg=None, stream=None) -> None:
+    """grad_y and grad_w (either may be None) of moe_combine (see include/qmoe.h)."""
+    fn = "moe_combine_backward"
+    ldy, ldo = cols if ldy is None else ldy, cols if ldo is None else ldo
+    ldg = cols if ldg is None else ldg
+    dev, st = _context(stream)
+    P = n_tokens * top_k
+    _check((_libh or lib()).moe_combine_backward(
+        ytype, _arg(fn, "y", y, ytype, _span(n_rows, cols, ldy), dev, ldy), n_rows, cols, ldy,
+        _arg(fn, "pos", pos, _I32, P, dev), _arg(fn, "topk_w", topk_w, F32, P, dev), n_tokens,
+        top_k, otype,
+        _arg(fn, "grad_out", grad_out, otype, _span(n_tokens, cols, ldo), dev, ldo), ldo,
+        _arg(fn, "grad_y", grad_y, ytype, _span(n_rows, cols, ldg), dev, ldg), ldg,
+        _arg(fn, "grad_w", grad_w, F32, P, dev), st))
+
+
+# --------------------------- products with 4-bit weights (include/qmoe.h)
+def w4_mm(W, stype: int, scale, zero, scale_cols: int, rows: int, cols: int, xtype: int, x,
+          n_tokens: int, ytype: int, y, ldx=None, ldy=None, stream=None) -> None:
+    """y = x W^T with 4-bit weights, a scale and zero point per scale_cols columns (see
+    include/qmoe.h)."""
+    fn = "w4_mm"
+    ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
+    dev, st = _context(stream)
+    blocks = rows * (cols // scale_cols) if scale_cols > 0 else 0
+    _check((_libh or lib()).w4_mm(
+        _arg(fn, "W", W, _U8, rows * cols // 2, dev), stype,
+        _arg(fn, "scale", scale, stype, blocks, dev), _arg(fn, "zero", zero, _U8, blocks, dev),
+        scale_cols, rows, cols, xtype,
+        _arg(fn, "x", x, xtype, _span(n_tokens, cols, ldx), dev, ldx), n_tokens, ldx, ytype,
+        _arg(fn, "y", y, ytype, _span(n_tokens, rows, ldy), dev, ldy), ldy, st))
+
+
+def w4_mm_grouped(W, stype: int, scale, zero, scale_cols: int, num_groups: int, rows: int,
+                  cols: int, xtype: int, x, n_rows: int, offsets, ytype: int, y, ldx=None,
+                  ldy=None, stream=None) -> None:
+    """y[r] = W_g x[r] for the rows of every group, with 4-bit weights (see
+    include/qmoe.h)."""
+    fn = "w4_mm_grouped"
+    ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
+    dev, st = _context(stream)
+    n = num_groups * rows
+    blocks = n * (cols // scale_cols) if scale_cols > 0 else 0
+    _check((_libh or lib()).w4_mm_grouped(
+        _arg(fn, "W", W, _U8, n * cols // 2, dev), stype,
+        _arg(fn, "scale", scale, stype, blocks, dev), _arg(fn, "zero", zero, _U8, blocks, dev),
+        scale_cols, num_groups, rows, cols, xtype,
+        _arg(fn, "x", x, xtype, _span(n_rows, cols, ldx), dev, ldx), n_rows, ldx,
+        _arg(fn, "offsets", offsets, _I32, num_groups + 1, dev), ytype,
+        _arg(fn, "y", y, ytype, _span(n_rows, rows, ldy), dev, ldy), ldy, st))
 
 
 # qmoe_set_exec_mode

@@ -5,21 +5,13 @@
 // inputs are still being written, so inputs are never read as data that is
 // constant for the kernel's life (ld.global.nc): __ldcg, behind the wait.
 #pragma once
-#include <type_traits>
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "f8.cuh"
 #include "gmm.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace qmoe {
 namespace f8 {
-
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
 // ---------------------------------------------------------------- quantise
 // Sixteen lanes share a 128-column block, eight consecutive columns each:
@@ -45,57 +37,6 @@ struct QuantParams {
     int nrun;         // runs of RUN blocks per row
 };
 constexpr int Q_THREADS = 256;
-
-// Eight consecutive values as they lie in memory.
-template <class T>
-struct Raw8 {
-    uint32_t w[sizeof(T) * 2];
-    __device__ __forceinline__ void load(const T* src) {
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
-            const uint4 a = __ldcg(reinterpret_cast<const uint4*>(src) + i);
-            w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
-        }
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) * 2; ++i) w[i] = 0u;
-    }
-    __device__ __forceinline__ float get(int i) const {
-        if constexpr (sizeof(T) == 4)
-            return __uint_as_float(w[i]);
-        else
-            return to_f32(reinterpret_cast<const T*>(w)[i]);
-    }
-    // The largest magnitude as its type's bits (16-bit values two at a time):
-    // magnitudes order as their bits do, infinities and NaN above the rest.
-    __device__ __forceinline__ uint32_t amax() const {
-        if constexpr (sizeof(T) == 4) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
-            return m;
-        } else {
-            uint32_t m = w[0] & 0x7FFF7FFFu;
-#pragma unroll
-            for (int i = 1; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-            return max(m & 0xFFFFu, m >> 16);
-        }
-    }
-    static __device__ __forceinline__ uint32_t inf() {
-        return sizeof(T) == 4 ? 0x7F800000u : std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-    }
-    // f32 bits of a magnitude from its type's
-    static __device__ __forceinline__ uint32_t f32_bits(uint32_t m) {
-        if constexpr (sizeof(T) == 4)
-            return m;
-        else if constexpr (std::is_same<T, __half>::value)
-            return __float_as_uint(
-                __half2float(__ushort_as_half(static_cast<unsigned short>(m))));
-        else
-            return m << 16;
-    }
-};
 
 // Quantises a block held by sixteen lanes, eight values each: this lane's codes
 // and the block's scale.  By a whole warp.
@@ -370,29 +311,6 @@ __global__ void __launch_bounds__(Q_THREADS) group_quantize_kernel(
 // caller who wants f32 sums throughout passes f32 activations.
 constexpr int C_THREADS = 128;
 constexpr int C_AHEAD = 8;
-
-template <class T>
-__device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
-    Raw8<T> r;
-    r.load(src);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = r.get(i);
-}
-template <class T>
-__device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint4 q;
-        uint32_t* u = reinterpret_cast<uint32_t*>(&q);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = std::is_same<T, __half>::value ? gmm::pack_f16(v[2 * i], v[2 * i + 1])
-                                                  : gmm::pack_bf16(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<uint4*>(dst) = q;
-    }
-}
 
 template <class T, class Y>
 __global__ void __launch_bounds__(C_THREADS) combine_kernel(

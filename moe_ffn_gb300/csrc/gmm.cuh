@@ -41,6 +41,7 @@
 #include "f8.cuh"
 #include "gmm_tiles.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 #include "umma.cuh"
 
 namespace qmoe {
@@ -145,15 +146,6 @@ __device__ __forceinline__ float cluster_sum(const float* src, int ranks) {
     for (int q = 1; q < MAX_RANKS; ++q)
         if (q < ranks) s += v[q];
     return s;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // The groups' tables, by the whole CTA (ends with a barrier): rows [lo, hi) of

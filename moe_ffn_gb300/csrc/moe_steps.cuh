@@ -1,0 +1,565 @@
+// moe_steps.cuh — the steps of a mixture-of-experts layer around its experts'
+// products: routing, the sort of the tokens by expert, and the weighted sum of the
+// experts' outputs, each with its gradient.
+//
+// Under programmatic dependent launch these grids may be resident while their
+// inputs are still being written: every load of them lies behind the wait and goes
+// through __ldcg.
+#pragma once
+#include "ptx.cuh"
+#include "route.cuh"
+#include "rows.cuh"
+
+namespace qmoe {
+namespace steps {
+
+constexpr int MAX_EXPERTS = 1024;
+constexpr int MAX_TOPK = 16;  // a token's slots lie in the lanes of one warp
+
+// ------------------------------------------------------------------ routing
+// A warp per token; lane i holds the logits i V .. i V + V - 1 as ranking keys
+// (route.cuh), so the lowest lane with the largest key also has the lowest index
+// among equals.  Each of the k rounds takes the largest key left.
+constexpr int R_WARPS = 4;
+
+struct RouteParams {
+    const void* logits;
+    int64_t ldl;
+    int64_t n_tokens;
+    int E, k;
+    bool vec;       // whole aligned runs of V logits
+    bool renorm;
+    int32_t* idx;
+    float* w;
+    // backward
+    const float* grad_w;
+    void* grad;     // logits' type
+    int64_t ldg;
+    bool vec_g;
+};
+
+// V values of a row from element c on, as f32; `fill` past the row's end.
+template <class T, int V>
+__device__ __forceinline__ void load_run(const T* row, int c, int E, bool vec, float fill,
+                                         float (&v)[V]) {
+    constexpr int BYTES = V * static_cast<int>(sizeof(T));
+    if constexpr (BYTES >= 4) {
+        if (vec) {  // E is a multiple of V: a lane's run is whole or empty
+            uint32_t w[BYTES / 4];
+            if (c < E) {
+                const T* p = row + c;
+                if constexpr (BYTES >= 16) {
+#pragma unroll
+                    for (int i = 0; i < BYTES / 16; ++i) {
+                        const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p) + i);
+                        w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+                    }
+                } else if constexpr (BYTES == 8) {
+                    const uint2 a = __ldcg(reinterpret_cast<const uint2*>(p));
+                    w[0] = a.x; w[1] = a.y;
+                } else {
+                    w[0] = __ldcg(reinterpret_cast<const uint32_t*>(p));
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+                    else v[i] = to_f32(reinterpret_cast<const T*>(w)[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = fill;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = c + i < E ? to_f32(ldcg_value(row + c + i)) : fill;
+}
+
+// The softmax's largest logit and the sum of exponentials around it, over a warp.
+template <int V>
+__device__ __forceinline__ float warp_expsum(const float (&v)[V], int c, int E, float top) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (c + i < E) z += expf(v[i] - top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    return z;
+}
+
+template <class T, int V>
+__global__ void __launch_bounds__(R_WARPS * 32) route_kernel(const RouteParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * R_WARPS + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    if (t >= p.n_tokens) return;
+    const int c = lane * V;
+    float v[V];
+    load_run<T, V>(static_cast<const T*>(p.logits) + t * p.ldl, c, p.E, p.vec, 0.f, v);
+    uint32_t key[V];
+    uint32_t best = 0;  // 0: none left (no key is 0)
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        key[i] = c + i < p.E ? route_key(v[i]) : 0u;
+        if (key[i] > best) { best = key[i]; at = i; }
+    }
+    uint32_t my_key = 0;
+    int my_idx = 0;
+    uint32_t top_key = 0;
+    for (int s = 0; s < p.k; ++s) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        const int who = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
+        const int e = __shfl_sync(0xffffffffu, c + at, who);
+        if (s == 0) top_key = m;
+        if (lane == s) { my_key = m; my_idx = e; }
+        if (lane == who) {
+            best = 0;
+            const int gone = at;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (i == gone) key[i] = 0u;
+                if (key[i] > best) { best = key[i]; at = i; }
+            }
+        }
+    }
+    const float top = route_key_value(top_key);
+    float w;
+    if (route_degenerate(top)) {
+        my_idx = lane;
+        w = __int_as_float(0x7FC00000);
+    } else {
+        const float x = lane < p.k ? expf(route_key_value(my_key) - top) : 0.f;
+        float z = x;
+        if (p.renorm) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        } else {
+            z = warp_expsum<V>(v, c, p.E, top);
+        }
+        w = x / z;
+    }
+    if (lane < p.k) {
+        p.idx[t * p.k + lane] = my_idx;
+        p.w[t * p.k + lane] = w;
+    }
+}
+
+// Gradient of the logits, a warp per token, with c = sum_s w_s dw_s over the slots
+// that name an expert:
+//   renormalised      dl_e = sum over slots s of e: w_s (dw_s - c)
+//   not renormalised  dl_e = p_e ((sum over slots s of e: dw_s) - c), p the softmax
+//                     over all experts, formed again from the logits
+template <class T, int V>
+__global__ void __launch_bounds__(R_WARPS * 32) route_backward_kernel(const RouteParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * R_WARPS + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    if (t >= p.n_tokens) return;
+    const int c = lane * V;
+    int idx = lane < p.k ? __ldcg(p.idx + t * p.k + lane) : -1;
+    const bool live = idx >= 0 && idx < p.E;
+    if (!live) idx = -1;
+    const float w = live ? __ldcg(p.w + t * p.k + lane) : 0.f;
+    const float d = live ? __ldcg(p.grad_w + t * p.k + lane) : 0.f;
+    float v[V], g[V];
+    if (!p.renorm)
+        load_run<T, V>(static_cast<const T*>(p.logits) + t * p.ldl, c, p.E, p.vec,
+                       -__int_as_float(0x7F800000), v);
+    float dot = w * d;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    const float mine = p.renorm ? w * (d - dot) : d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = 0.f;
+    for (int s = 0; s < p.k; ++s) {
+        const int e = __shfl_sync(0xffffffffu, idx, s);
+        const float m = __shfl_sync(0xffffffffu, mine, s);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e == c + i) g[i] += m;
+    }
+    if (!p.renorm) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) best = max(best, c + i < p.E ? route_key(v[i]) : 0u);
+        const float top = route_key_value(__reduce_max_sync(0xffffffffu, best));
+        const float inv = 1.f / warp_expsum<V>(v, c, p.E, top);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            g[i] = route_degenerate(top) ? __int_as_float(0x7FC00000)
+                                         : expf(v[i] - top) * inv * (g[i] - dot);
+    }
+    T* row = static_cast<T*>(p.grad) + t * p.ldg + c;
+    constexpr int BYTES = V * static_cast<int>(sizeof(T));
+    if constexpr (BYTES >= 4) {
+        if (p.vec_g) {
+            if (c >= p.E) return;
+            uint32_t q[BYTES / 4];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if constexpr (sizeof(T) == 4) q[i] = __float_as_uint(g[i]);
+                else reinterpret_cast<T*>(q)[i] = from_f32<T>(g[i]);
+            }
+            if constexpr (BYTES >= 16) {
+#pragma unroll
+                for (int i = 0; i < BYTES / 16; ++i)
+                    reinterpret_cast<uint4*>(row)[i] =
+                        make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+            } else if constexpr (BYTES == 8) {
+                *reinterpret_cast<uint2*>(row) = make_uint2(q[0], q[1]);
+            } else {
+                *reinterpret_cast<uint32_t*>(row) = q[0];
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (c + i < p.E) row[i] = from_f32<T>(g[i]);
+}
+
+// ------------------------------------------------------------------ permute
+// Stable counting sort of the P = T k (token, slot) pairs by expert, and the copy
+// of each token's row to its pairs' rows, read once and written k times.
+//
+// A CTA takes a run of tokens.  A pair's row is the number of pairs of smaller
+// experts, plus the pairs of its expert in earlier runs, plus those before it in
+// its own run.  The first two come from all the indices, counted by every CTA
+// for itself, while they are few (up to P_ALONE pairs: one launch), else from a
+// table of counts [runs][E] that count_kernel makes.
+constexpr int P_THREADS = 256;
+constexpr int P_WARPS = P_THREADS / 32;
+constexpr int P_ALONE = 8192;
+constexpr int P_POS = 1024;   // positions of a run kept in shared memory
+
+struct PermuteParams {
+    const uint8_t* x;
+    int64_t ldx;            // bytes
+    uint8_t* rows;
+    int64_t ldr;            // bytes
+    int nvec;               // units of VB bytes in a row
+    const int32_t* idx;
+    int32_t* offsets;
+    int32_t* pos;
+    int P, E, k;
+    int run;                // tokens of a run
+    int runs;
+    uint16_t* counts;       // [runs][E], or null
+};
+
+// The expert of pair i, or -1.
+__device__ __forceinline__ int expert_of(const int32_t* idx, int i, int E) {
+    const int e = __ldcg(idx + i);
+    return e >= 0 && e < E ? e : -1;
+}
+
+__global__ void __launch_bounds__(P_THREADS) count_kernel(const PermuteParams p) {
+    extern __shared__ int hist[];
+    const int tid = threadIdx.x;
+    for (int e = tid; e < p.E; e += P_THREADS) hist[e] = 0;
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+    const int beg = blockIdx.x * p.run * p.k, end = min(beg + p.run * p.k, p.P);
+    for (int i = beg + tid; i < end; i += P_THREADS) {
+        const int e = expert_of(p.idx, i, p.E);
+        if (e >= 0) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    uint16_t* out = p.counts + static_cast<int64_t>(blockIdx.x) * p.E;
+    for (int e = tid; e < p.E; e += P_THREADS) out[e] = static_cast<uint16_t>(hist[e]);
+}
+
+template <int VB>
+struct Unit;
+template <> struct Unit<16> { using type = uint4; };
+template <> struct Unit<4> { using type = uint32_t; };
+template <> struct Unit<2> { using type = uint16_t; };
+
+template <int VB>
+__global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams p) {
+    using U = typename Unit<VB>::type;
+    extern __shared__ int sm[];
+    __shared__ int s_pos[P_POS];
+    __shared__ int s_wsum[P_WARPS];
+    int* whist = sm;                    // [P_WARPS][E] this run's counts, then next rows
+    int* total = sm + P_WARPS * p.E;    // [E]
+    int* before = total + p.E;          // [E]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = blockIdx.x;
+    for (int i = tid; i < (P_WARPS + 2) * p.E; i += P_THREADS) sm[i] = 0;
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+    const int beg = r * p.run * p.k, end = min(beg + p.run * p.k, p.P);
+    if (p.counts) {
+        for (int e = tid; e < p.E; e += P_THREADS) {
+            int all = 0, ahead = 0;
+            for (int j = 0; j < p.runs; ++j) {
+                const int c = __ldcg(p.counts + static_cast<int64_t>(j) * p.E + e);
+                all += c;
+                if (j < r) ahead += c;
+            }
+            total[e] = all;
+            before[e] = ahead;
+        }
+    } else {
+        for (int i = tid; i < p.P; i += P_THREADS) {
+            const int e = expert_of(p.idx, i, p.E);
+            if (e >= 0) {
+                atomicAdd(&total[e], 1);
+                if (i < beg) atomicAdd(&before[e], 1);
+            }
+        }
+    }
+    // this run's pairs, a part to each warp
+    const int part = ((end - beg + P_WARPS - 1) / P_WARPS + 31) & ~31;
+    const int wbeg = min(beg + warp * part, end), wend = min(wbeg + part, end);
+    int* h = whist + warp * p.E;
+    for (int i = wbeg; i < wend; i += 32) {
+        const int e = i + lane < wend ? expert_of(p.idx, i + lane, p.E) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(same) - 1) h[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // exclusive sum over the experts, a run of experts to each thread
+    const int per = (p.E + P_THREADS - 1) / P_THREADS;
+    const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) mine += total[e];
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_wsum[warp] = incl;
+    __syncthreads();
+    int first = incl - mine;
+    for (int w = 0; w < warp; ++w) first += s_wsum[w];
+    const bool tell = r == 0 && blockIdx.y == 0;
+    for (int e = e0; e < e1; ++e) {
+        if (tell) p.offsets[e] = first;
+        int at = first + before[e];
+        first += total[e];
+        for (int w = 0; w < P_WARPS; ++w) {
+            const int c = whist[w * p.E + e];
+            whist[w * p.E + e] = at;
+            at += c;
+        }
+        if (tell && e == p.E - 1) p.offsets[p.E] = first;
+    }
+    __syncthreads();
+    for (int i = wbeg; i < wend; i += 32) {
+        const int e = i + lane < wend ? expert_of(p.idx, i + lane, p.E) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        int row = -1;
+        if (e >= 0) row = h[e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) h[e] += __popc(same);
+        __syncwarp();
+        if (i + lane < wend) {
+            p.pos[i + lane] = row;  // (the same value from every blockIdx.y)
+            if (i + lane - beg < P_POS) s_pos[i + lane - beg] = row;
+        }
+    }
+    __syncthreads();
+    constexpr int AHEAD = 4;
+    const int ntok = (end - beg) / p.k;
+    const int nseg = (p.nvec + 32 * AHEAD - 1) / (32 * AHEAD);
+    const int64_t items = static_cast<int64_t>(ntok) * nseg;
+    for (int64_t it = blockIdx.y * P_WARPS + warp; it < items; it += gridDim.y * P_WARPS) {
+        const int tok = static_cast<int>(it / nseg);
+        const int v0 = static_cast<int>(it - static_cast<int64_t>(tok) * nseg) * 32 * AHEAD + lane;
+        const int64_t t = static_cast<int64_t>(r) * p.run + tok;
+        const U* src = reinterpret_cast<const U*>(p.x + t * p.ldx);
+        U u[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (v0 + 32 * a < p.nvec) u[a] = __ldcg(src + v0 + 32 * a);
+        for (int s = 0; s < p.k; ++s) {
+            const int i = tok * p.k + s;
+            const int row = i < P_POS ? s_pos[i] : __ldcg(p.pos + beg + i);
+            if (row < 0) continue;
+            U* dst = reinterpret_cast<U*>(p.rows + static_cast<int64_t>(row) * p.ldr);
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a)
+                if (v0 + 32 * a < p.nvec) dst[v0 + 32 * a] = u[a];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ combine
+// out[t] = residual[t] + sum_s w[t][s] y[pos[t][s]], summed in f32 in slot order and
+// rounded once.  A thread takes N columns of one token (N = 8 where every row is
+// whole aligned 16-byte units, else 1), eight slots at a step.
+constexpr int C_THREADS = 128;
+constexpr int C_AHEAD = 8;
+
+struct CombineParams {
+    const void* y;
+    int64_t n_rows, ldy;
+    int cols;
+    const int32_t* pos;
+    const float* w;         // null: ones
+    int k;
+    const void* residual;   // null: zeros
+    void* out;
+    int64_t ldo;
+    // backward
+    const void* grad_out;   // rows ldo apart
+    void* grad_y;           // null: not wanted
+    int64_t ldg;
+    float* grad_w;          // null: not wanted
+};
+
+// One value, with the interface of Raw8.
+template <class T>
+struct Raw1 {
+    T v;
+    __device__ __forceinline__ void load(const T* p) { v = ldcg_value(p); }
+    __device__ __forceinline__ void zero() { v = from_f32<T>(0.f); }
+    __device__ __forceinline__ float get(int) const { return to_f32(v); }
+};
+// N consecutive values of a row.
+template <class T, int N>
+using Run = typename std::conditional<N == 8, Raw8<T>, Raw1<T>>::type;
+template <class T, int N>
+__device__ __forceinline__ void store_run(T* p, const float (&v)[N]) {
+    if constexpr (N == 8) store8(p, v);
+    else p[0] = from_f32<T>(v[0]);
+}
+
+// A token's slots: one load, a slot per lane (k <= 16); a row outside [0, n_rows)
+// adds nothing.
+__device__ __forceinline__ void load_slots(const CombineParams& p, int64_t t, int lane, int* row,
+                                           float* w) {
+    int r = lane < p.k ? __ldcg(p.pos + t * p.k + lane) : -1;
+    if (r >= p.n_rows) r = -1;
+    *row = r;
+    *w = r >= 0 ? (p.w ? __ldcg(p.w + t * p.k + lane) : 1.f) : 0.f;
+}
+
+template <class Y, class O, int N>
+__global__ void __launch_bounds__(C_THREADS) combine_kernel(const CombineParams p) {
+    const int64_t t = blockIdx.x;
+    const int c = (blockIdx.y * C_THREADS + threadIdx.x) * N;
+    const int lane = threadIdx.x & 31;
+    const bool in = c < p.cols;
+    pdl_wait();
+    pdl_trigger();
+    int slot_row;
+    float slot_w;
+    load_slots(p, t, lane, &slot_row, &slot_w);
+    float a[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = 0.f;
+    for (int s0 = 0; s0 < p.k; s0 += C_AHEAD) {
+        Run<Y, N> v[C_AHEAD];
+        float w[C_AHEAD];
+        int r[C_AHEAD];
+#pragma unroll
+        for (int s = 0; s < C_AHEAD; ++s) {
+            r[s] = __shfl_sync(0xffffffffu, slot_row, s0 + s);  // -1 past the slots
+            w[s] = __shfl_sync(0xffffffffu, slot_w, s0 + s);
+        }
+#pragma unroll
+        for (int s = 0; s < C_AHEAD; ++s) {
+            v[s].zero();
+            if (in && r[s] >= 0)
+                v[s].load(static_cast<const Y*>(p.y) + static_cast<int64_t>(r[s]) * p.ldy + c);
+        }
+#pragma unroll
+        for (int s = 0; s < C_AHEAD; ++s)
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] = fmaf(w[s], v[s].get(i), a[i]);
+    }
+    if (!in) return;
+    if (p.residual) {
+        Run<O, N> q;
+        q.load(static_cast<const O*>(p.residual) + t * p.ldo + c);
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] += q.get(i);
+    }
+    store_run<O, N>(static_cast<O*>(p.out) + t * p.ldo + c, a);
+}
+
+// Gradients: of a row, grad_y[pos[t][s]] = w[t][s] grad_out[t], rounded once; of a
+// weight, grad_w[t][s] = sum_c y[pos[t][s]][c] grad_out[t][c] in f32 (0 for a slot
+// without a row).  A CTA per token reads grad_out and the token's rows once.
+template <class Y, class O, int N>
+__global__ void __launch_bounds__(C_THREADS) combine_backward_kernel(const CombineParams p) {
+    __shared__ float s_sum[C_THREADS / 32][MAX_TOPK];
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
+    pdl_wait();
+    pdl_trigger();
+    int slot_row;
+    float slot_w;
+    load_slots(p, t, lane, &slot_row, &slot_w);
+    const O* g_row = static_cast<const O*>(p.grad_out) + t * p.ldo;
+    for (int s0 = 0; s0 < p.k; s0 += C_AHEAD) {
+        float w[C_AHEAD], sum[C_AHEAD];
+        int r[C_AHEAD];
+#pragma unroll
+        for (int s = 0; s < C_AHEAD; ++s) {
+            r[s] = __shfl_sync(0xffffffffu, slot_row, s0 + s);
+            w[s] = __shfl_sync(0xffffffffu, slot_w, s0 + s);
+            sum[s] = 0.f;
+        }
+        for (int c = tid * N; c < p.cols; c += C_THREADS * N) {
+            Run<O, N> g;
+            Run<Y, N> v[C_AHEAD];
+            g.load(g_row + c);
+            if (p.grad_w) {
+#pragma unroll
+                for (int s = 0; s < C_AHEAD; ++s) {
+                    v[s].zero();
+                    if (r[s] >= 0)
+                        v[s].load(static_cast<const Y*>(p.y) + static_cast<int64_t>(r[s]) * p.ldy +
+                                  c);
+                }
+#pragma unroll
+                for (int s = 0; s < C_AHEAD; ++s)
+                    if (r[s] >= 0)
+#pragma unroll
+                        for (int i = 0; i < N; ++i) sum[s] = fmaf(v[s].get(i), g.get(i), sum[s]);
+            }
+            if (p.grad_y) {
+#pragma unroll
+                for (int s = 0; s < C_AHEAD; ++s)
+                    if (r[s] >= 0) {
+                        float d[N];
+#pragma unroll
+                        for (int i = 0; i < N; ++i) d[i] = w[s] * g.get(i);
+                        store_run<Y, N>(static_cast<Y*>(p.grad_y) +
+                                            static_cast<int64_t>(r[s]) * p.ldg + c, d);
+                    }
+            }
+        }
+        if (p.grad_w) {
+#pragma unroll
+            for (int s = 0; s < C_AHEAD; ++s) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    sum[s] += __shfl_xor_sync(0xffffffffu, sum[s], o);
+                if (lane == 0) s_sum[tid >> 5][s0 + s] = sum[s];
+            }
+        }
+    }
+    if (!p.grad_w) return;
+    __syncthreads();
+    if (tid < p.k) {
+        float a = 0.f;
+        for (int i = 0; i < C_THREADS / 32; ++i) a += s_sum[i][tid];
+        p.grad_w[t * p.k + tid] = a;
+    }
+}
+
+}  // namespace steps
+}  // namespace qmoe

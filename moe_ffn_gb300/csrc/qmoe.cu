@@ -1139,7 +1139,7 @@ qmoe_status qmoe_device_status(void* stream) {
                         "(code %u); it was clamped, and the layer's output is not valid", v);
         if (v == DEV_GMM_OFFSETS)
             return fail(QMOE_ERR_INVALID_ARGUMENT,
-                        "mm_grouped: group offsets decrease or lie outside [0, n_rows] (code %u); "
+                        "mm_grouped or w4_mm_grouped: group offsets decrease or lie outside [0, n_rows] (code %u); "
                         "y was not written", v);
         return fail(QMOE_ERR_TIMEOUT, "a bounded device wait expired (code %u: %s)", v,
                     v == DEV_TIMEOUT_FULL    ? "stage never filled"

@@ -1,0 +1,286 @@
+"""GPU tests of w4_mm and w4_mm_grouped against the 64-bit forms of
+tests/steps_ref.py, whose header derives the tolerances."""
+import numpy as np
+import pytest
+
+from tests import steps_ref as ref
+from tests.test_gpu_f8 import check, dev, f64, kinds
+from tests.test_gpu_steps import strided
+
+pytestmark = pytest.mark.gpu
+TYPES = ["f32", "bf16", "f16"]
+
+
+def weights(qm, g, e, n, k, S, stype, zeros):
+    """Random codes, scales of wide range, zero points with their high bits set."""
+    import torch
+    q = g.integers(0, 256, (e, n, k // 2), dtype=np.uint8)
+    s = torch.from_numpy(np.exp(g.uniform(-4, 0, (e, n, k // S))).astype(np.float32))
+    s = s.to(kinds(qm)[stype][1]).cuda()
+    z = g.integers(0, 256, (e, n, k // S), dtype=np.uint8) if zeros else None
+    return dev(q), s, (None if z is None else dev(z)), ref.w4_values(q, f64(s), z, S)
+
+
+def run_mm(qm, m, n, k, S, kind="bf16", okind=None, stype="f16", zeros=True, ldx=None, ldy=None,
+           offset=0, x=None, sparse=False):
+    import torch
+    okind = okind or kind
+    g = np.random.default_rng(m + 3 * n + 5 * k + S)
+    q, s, z, wv = weights(qm, g, 1, n, k, S, stype, zeros)
+    if x is None:
+        x = g.standard_normal((m, k)) * (0.01 if "f16" in (kind, okind) else 1.0)
+    xt, _ = strided(x, kind, qm, ldx, offset)
+    y, store = strided(np.full((m, n), 55.0), okind, qm, ldy, offset)
+    qm.w4_mm(q, kinds(qm)[stype][0], s, z, S, n, k, kinds(qm)[kind][0], xt, m, kinds(qm)[okind][0],
+             y, ldx=ldx, ldy=ldy)
+    assert qm.device_status() == qm.OK
+    want, err = ref.w4_product(f64(xt[:, :k]), wv[0], S)
+    check(f64(y[:, :n]), want, ref.rounded(want, err, okind), f"w4 {m}x{n}x{k}")
+    if ldy:
+        assert (y[:, n:] == 77.0).all()
+    assert (store[:offset] == 77.0).all() and (store[offset + y.numel():] == 77.0).all()
+
+
+SHAPES = [  # tokens, rows, cols, scale_cols
+    (1, 1, 32, 32), (1, 4096, 4096, 128), (2, 100, 64, 64), (3, 130, 160, 32), (7, 33, 1280, 128),
+    (8, 257, 192, 64), (9, 640, 1024, 128), (16, 15, 2048, 128), (17, 128, 96, 32),
+    (33, 300, 512, 64), (64, 16, 4096, 128), (65, 200, 256, 32), (150, 129, 384, 128),
+    (1, 5000, 128, 128), (5, 48, 14336, 128), (2, 20, 14400, 64), (1, 17, 40000, 32),
+]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("m,n,k,S", SHAPES)
+def test_w4_mm(qm, kind, m, n, k, S):
+    run_mm(qm, m, n, k, S, kind)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("okind", TYPES)
+@pytest.mark.parametrize("stype", TYPES)
+@pytest.mark.parametrize("zeros", [True, False])
+def test_w4_mm_types(qm, kind, okind, stype, zeros):
+    run_mm(qm, 11, 70, 256, 64, kind, okind, stype, zeros)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("ldx,ldy,offset", [(264, 72, 0), (257, 65, 0), (256, 64, 1), (258, 67, 2),
+                                            (256, 64, 4), (272, 80, 8)])
+@pytest.mark.parametrize("m", [1, 12])
+def test_w4_mm_strides(qm, kind, ldx, ldy, offset, m):
+    run_mm(qm, m, 64, 256, 32, kind, ldx=ldx, ldy=ldy, offset=offset)
+
+
+def test_w4_mm_f32_keeps_all_bits_of_x(qm):
+    """f32 values with 24 significant bits, of sizes from 2^-100 to 2^100: the error stays
+    within the bound of the sums (one bit lost would be 2^-23 of single terms)."""
+    g = np.random.default_rng(5)
+    k = 64
+    for p in (-100, -20, 0, 20, 100):
+        x = np.zeros((3, k), np.float32)
+        x[0, 5] = np.float32(2.0 ** p) * np.float32(1 + 2.0 ** -23)
+        x[1, 63] = np.float32(2.0 ** p) * np.float32(2 - 2.0 ** -23)
+        x[2] = (g.standard_normal(k) * 2.0 ** p).astype(np.float32)
+        run_mm(qm, 3, 40, k, 32, "f32", x=x)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("m", [1, 5, 40])
+def test_w4_mm_nan_and_infinities_stay_in_their_rows(qm, kind, m):
+    """A NaN or infinite x makes its own row's outputs so (an infinity NaN where its
+    weight is 0) and no other's; a NaN scale its own column's."""
+    import torch
+    n, k, S = 50, 128, 64
+    g = np.random.default_rng(m)
+    q, s, z, wv = weights(qm, g, 1, n, k, S, "f32", True)
+    s[0, 7, 1] = float("nan")
+    wv[0, 7, 64:] = np.nan
+    x = (g.standard_normal((m, k)) * 0.01)
+    x[0, 3] = np.inf
+    if m > 1:
+        x[m - 1, 100] = np.nan
+    xt, _ = strided(x, kind, qm)
+    y = torch.full((m, n), 55.0, device="cuda")
+    qm.w4_mm(q, qm.F32, s, z, S, n, k, kinds(qm)[kind][0], xt, m, qm.F32, y)
+    got = y.cpu().numpy()
+    w3 = wv[0, :, 3]
+    other = np.arange(n) != 7
+    assert np.isnan(got[:, 7]).all()
+    assert np.array_equal(np.isnan(got[0, other]), w3[other] == 0)
+    live = other & (w3 != 0)
+    assert np.array_equal(got[0, live], np.sign(w3[live]) * np.inf)
+    if m > 1:
+        assert np.isnan(got[m - 1]).all()
+        rest = slice(1, m - 1)
+        want, err = ref.w4_product(f64(xt)[rest], wv[0][other], S)
+        check(got[rest][:, other], want, ref.rounded(want, err, "f32"), "the other rows")
+
+
+GROUPS = {  # rows of each group
+    "one each": [1] * 9, "ragged": [0, 3, 17, 0, 1, 40, 0], "first empty": [0, 0, 5],
+    "large": [70, 1, 130, 0, 64], "none": [0, 0, 0], "one": [20],
+}
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("name", GROUPS)
+@pytest.mark.parametrize("n,k,S,zeros", [(100, 256, 128, True), (33, 96, 32, False),
+                                         (768, 2048, 64, True)])
+def test_w4_mm_grouped(qm, kind, name, n, k, S, zeros):
+    """Groups by offsets, with rows before the first and behind the last: left as they
+    were."""
+    import torch
+    sizes = GROUPS[name]
+    e = len(sizes)
+    g = np.random.default_rng(n + e)
+    q, s, z, wv = weights(qm, g, e, n, k, S, "bf16", zeros)
+    head, tail = 3, 4
+    off = np.cumsum([head] + sizes).astype(np.int32)
+    m = int(off[-1]) + tail
+    xt, _ = strided(g.standard_normal((m, k)) * 0.01, kind, qm)
+    y, _ = strided(np.full((m, n), 55.0), kind, qm)
+    code = kinds(qm)[kind][0]
+    qm.w4_mm_grouped(q, qm.BF16, s, z, S, e, n, k, code, xt, m, dev(off), code, y)
+    assert qm.device_status() == qm.OK
+    assert (y[:head] == 55.0).all() and (y[int(off[-1]):] == 55.0).all()
+    xv, got = f64(xt), f64(y)
+    for i in range(e):
+        r = slice(off[i], off[i + 1])
+        want, err = ref.w4_product(xv[r], wv[i], S)
+        check(got[r], want, ref.rounded(want, err, kind), f"group {i}")
+
+
+@pytest.mark.parametrize("e", [1, 33, 300, 1024])
+def test_w4_mm_grouped_many_groups(qm, e):
+    import torch
+    n, k, S, m = 40, 64, 32, 200
+    g = np.random.default_rng(e)
+    q, s, z, wv = weights(qm, g, e, n, k, S, "f32", True)
+    group = np.sort(g.integers(0, e, m))
+    off = np.searchsorted(group, np.arange(e + 1)).astype(np.int32)
+    xt, _ = strided(g.standard_normal((m, k)), "f32", qm)
+    y = torch.zeros(m, n, device="cuda")
+    qm.w4_mm_grouped(q, qm.F32, s, z, S, e, n, k, qm.F32, xt, m, dev(off), qm.F32, y)
+    assert qm.device_status() == qm.OK
+    xv = f64(xt)
+    for i in range(m):
+        want, err = ref.w4_product(xv[i:i + 1], wv[group[i]], S)
+        check(f64(y[i:i + 1]), want, ref.rounded(want, err, "f32"), f"row {i}")
+
+
+@pytest.mark.parametrize("off", [[0, 5, 3, 8], [-1, 2, 4, 8], [0, 2, 4, 9], [3, 2, 1, 0]])
+def test_w4_mm_grouped_bad_offsets_are_reported(qm, off):
+    import torch
+    n, k = 40, 64
+    g = np.random.default_rng(0)
+    q, s, z, _ = weights(qm, g, 3, n, k, 32, "f32", True)
+    y = torch.full((8, n), 55.0, device="cuda")
+    x = torch.ones(8, k, device="cuda")
+    qm.w4_mm_grouped(q, qm.F32, s, z, 32, 3, n, k, qm.F32, x, 8, dev(np.array(off, np.int32)),
+                     qm.F32, y)
+    assert qm.device_status() == qm.ERR_INVALID_ARGUMENT and "w4_mm_grouped" in qm.last_error()
+    assert (y == 55.0).all()
+    qm.w4_mm_grouped(q, qm.F32, s, z, 32, 3, n, k, qm.F32, x, 8,
+                     dev(np.array([0, 2, 4, 8], np.int32)), qm.F32, y)
+    assert qm.device_status() == qm.OK and (y != 55.0).all()
+
+
+def test_same_inputs_same_bits(qm):
+    import torch
+    g = np.random.default_rng(1)
+    for m, n, k in ((1, 4096, 4096), (5, 1000, 2048), (200, 300, 512)):
+        q, s, z, _ = weights(qm, g, 1, n, k, 128, "f16", True)
+        x = torch.randn(m, k, device="cuda").to(torch.bfloat16)
+        ys = [torch.empty(m, n, device="cuda") for _ in range(4)]
+        for y in ys:
+            qm.w4_mm(q, qm.F16, s, z, 128, n, k, qm.BF16, x, m, qm.F32, y)
+        assert all(torch.equal(ys[0], y) for y in ys[1:])
+
+
+def test_a_row_does_not_depend_on_the_others(qm):
+    """A token's outputs are the same bits alone, and within the bound in any batch."""
+    import torch
+    g = np.random.default_rng(2)
+    n, k, S = 200, 512, 64
+    q, s, z, wv = weights(qm, g, 1, n, k, S, "f16", True)
+    x = torch.randn(70, k, device="cuda").to(torch.bfloat16)
+    want, err = ref.w4_product(f64(x), wv[0], S)
+    for m in (1, 2, 8, 9, 16, 31, 64, 70):
+        y = torch.empty(m, n, device="cuda")
+        qm.w4_mm(q, qm.F16, s, z, S, n, k, qm.BF16, x[:m], m, qm.F32, y)
+        check(f64(y), want[:m], ref.rounded(want[:m], err[:m], "f32"), f"{m} tokens")
+
+
+def test_weights_beyond_2_31_codes(qm):
+    """A matrix of 2^32 codes: offsets of weights and scales that pass 32 bits."""
+    import torch
+    n, k, S = (1 << 20) + 3, 4096, 128
+    q = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device="cuda")
+    s = torch.rand(n, k // S, device="cuda").to(torch.float16)
+    z = torch.randint(0, 16, (n, k // S), dtype=torch.uint8, device="cuda")
+    x = torch.randn(2, k, device="cuda").to(torch.bfloat16)
+    y = torch.zeros(2, n, device="cuda")
+    qm.w4_mm(q, qm.F16, s, z, S, n, k, qm.BF16, x, 2, qm.F32, y)
+    assert qm.device_status() == qm.OK
+    pick = [0, 1, 524287, 524288, n - 17, n - 1]
+    wv = ref.w4_values(q[pick].cpu().numpy(), f64(s[pick]), z[pick].cpu().numpy(), S)
+    want, err = ref.w4_product(f64(x), wv, S)
+    check(f64(y[:, pick]), want, ref.rounded(want, err, "f32"), "sampled rows")
+
+
+def test_stack_beyond_2_31_bytes(qm):
+    """The last group of a stack whose codes pass 2^31 bytes."""
+    import torch
+    e, n, k, S = 130, 4096, 8192, 128
+    q = torch.randint(0, 256, (e, n, k // 2), dtype=torch.uint8, device="cuda")
+    s = torch.rand(e, n, k // S, device="cuda").to(torch.bfloat16)
+    x = (0.01 * torch.randn(3, k, device="cuda")).to(torch.float16)
+    off = torch.tensor([0] * (e - 1) + [1, 3], dtype=torch.int32, device="cuda")
+    y = torch.zeros(3, n, device="cuda")
+    assert q.numel() > 2 ** 31
+    qm.w4_mm_grouped(q, qm.BF16, s, None, S, e, n, k, qm.F16, x, 3, off, qm.F32, y)
+    assert qm.device_status() == qm.OK
+    for i, r in ((e - 2, slice(0, 1)), (e - 1, slice(1, 3))):
+        pick = [0, 100, n - 1]
+        wv = ref.w4_values(q[i][pick].cpu().numpy(), f64(s[i][pick]), None, S)
+        want, err = ref.w4_product(f64(x[r]), wv, S)
+        check(f64(y[r][:, pick]), want, ref.rounded(want, err, "f32"), f"group {i}")
+
+
+@pytest.mark.parametrize("t", [1, 30])
+def test_layer_of_4_bit_experts(qm, t):
+    """Routes, sort, 4-bit gate, up and down products and the weighted sum in a run,
+    f32 activations throughout: each step within its own bound, together below
+    2^-14 of the outputs' size (five steps of at most 2^-17 for these lengths)."""
+    import torch
+    g = np.random.default_rng(t)
+    e, k, h, f, S = 16, 4, 256, 128, 64
+    x = torch.randn(t, h, device="cuda")
+    logits = torch.randn(t, e, device="cuda")
+    stacks = [weights(qm, g, e, n, c, S, "f16", True) for n, c in ((f, h), (f, h), (h, f))]
+    P = t * k
+    idx = torch.empty(t, k, dtype=torch.int32, device="cuda")
+    pos, w = torch.empty_like(idx), torch.empty(t, k, device="cuda")
+    rows, y, out = (torch.empty(n, h, device="cuda") for n in (P, P, t))
+    a = [torch.empty(P, f, device="cuda") for _ in range(2)]
+    off = torch.empty(e + 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(qm.moe_permute_workspace_size(t, e, k), dtype=torch.uint8, device="cuda")
+    qm.moe_route(qm.F32, logits, t, e, k, idx, w)
+    qm.moe_permute(qm.F32, x, t, h, idx, e, k, rows, off, pos, ws)
+    for i in range(2):
+        q, s, z, _ = stacks[i]
+        qm.w4_mm_grouped(q, qm.F16, s, z, S, e, f, h, qm.F32, rows, P, off, qm.F32, a[i])
+    q, s, z, _ = stacks[2]
+    act = torch.relu(a[0]) * a[1]
+    qm.w4_mm_grouped(q, qm.F16, s, z, S, e, h, f, qm.F32, act, P, off, qm.F32, y)
+    qm.moe_combine(qm.F32, y, P, h, pos, w, t, k, qm.F32, x, out)
+    assert qm.device_status() == qm.OK
+    i, wt, _ = ref.route(f64(logits), k, True)
+    xv, want, size = f64(x), f64(x), 0.0
+    for tok in range(t):
+        for slot in range(k):
+            gate, up, down = (st[3][i[tok, slot]] for st in stacks)
+            term = wt[tok, slot] * (down @ (np.maximum(gate @ xv[tok], 0) * (up @ xv[tok])))
+            want[tok] += term
+    off_by = np.linalg.norm(f64(out) - want) / np.linalg.norm(want)
+    assert off_by <= 2.0 ** -14, off_by
