@@ -153,8 +153,9 @@ __device__ __forceinline__ float cluster_sum(const float* src, int ranks) {
 // decrease or leave [0, M] the total is 0 and the call computes nothing: clamped
 // groups may overlap, so two would write the same rows, and their tiles may be
 // more than an int counts.  A thread per group; the time is one load latency and
-// one scan.
-__device__ __forceinline__ void build_tables(const Params& p, int nt, int nb, int* t_lo,
+// one scan.  P: any parameters with offsets, M, E and err.
+template <class P>
+__device__ __forceinline__ void build_tables(const P& p, int nt, int nb, int* t_lo,
                                              int* t_hi, int* t_pre) {
     __shared__ int wsum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

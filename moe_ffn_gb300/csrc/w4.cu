@@ -1,9 +1,12 @@
 // w4.cu — entry points of the products with 4-bit weights: argument validation and
 // launches of the kernels of w4.cuh.  See include/qmoe.h for the contract of every
 // function.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "../../include/qmoe.h"
 #include "host.cuh"
@@ -16,6 +19,82 @@ constexpr int64_t W4_MAX_ROWS = 0x7fffff00;
 constexpr int W4_MAX_GROUPS = 1024;
 
 static int w4_size(int t) { return t == QMOE_F32 ? 4 : t == QMOE_BF16 || t == QMOE_F16 ? 2 : 0; }
+
+// The kernel for few rows: tiles of 16 weight rows and as many tokens as NB MMA column
+// blocks of eight hold.
+template <class X, int S, int NB>
+static cudaError_t launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
+    constexpr int parts = std::is_same<X, float>::value ? 3 : 1;
+    p.nt = 8 * NB / parts;
+    p.cols = std::min(p.nt, p.M) * parts;
+    const int units = (p.K + w4::UNIT - 1) / w4::UNIT;
+    const int unit_bytes = p.cols * w4::UNIT * 2;
+    const int room = d.smem_pair - 512;
+    // K over the CTAs of a cluster: until x fits, and further while the tiles leave SMs
+    // idle; a CTA's part over its warps, a block of four units each
+    int ranks = 1, smem = 0;
+    for (int r = 1; r <= w4::MAX_RANKS && r <= units; r *= 2) {
+        w4::Params q = p;
+        q.rank_units = (units + r - 1) / r;
+        const int blocks = (q.rank_units + w4::BLOCK - 1) / w4::BLOCK;
+        q.wk = 1;
+        // (no more parts than a round's x leaves room for)
+        while (q.wk < w4::WARPS && q.wk < blocks && 2 * q.wk * w4::BLOCK * unit_bytes <= room / 5 * 3)
+            q.wk *= 2;
+        const int rows = 16 * w4::WARPS / q.wk;
+        q.nb = (q.N + rows - 1) / rows;
+        q.slot = r > 1 ? rows * q.nt : 0;
+        const int fixed = w4::few_fixed(q.E, NB, q.slot * r);
+        const int round_bytes = q.wk * w4::BLOCK * unit_bytes;
+        const int rounds = (blocks + q.wk - 1) / q.wk;
+        if (fixed + round_bytes > room) break;
+        q.pass_rounds = std::min(rounds, (room - fixed) / round_bytes);
+        p = q;
+        ranks = r;
+        smem = fixed + q.pass_rounds * round_bytes;
+        const bool full = gmm::max_tiles(q.M, q.E, q.nt, q.nb) * 2 * r > 2 * d.sms;
+        if (q.pass_rounds == rounds && (full || blocks <= w4::WARPS)) break;
+    }
+    const int64_t tiles = gmm::max_tiles(p.M, p.E, p.nt, p.nb);
+    auto kern = w4::few_kernel<X, S, NB>;
+    static std::atomic<bool> configured[64];
+    if (!configured[d.dev].load()) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
+        if (e != cudaSuccess) return e;
+        configured[d.dev].store(true);
+    }
+    const int clusters = static_cast<int>(std::min<int64_t>(tiles, 2 * d.sms / ranks));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
+    cfg.blockDim = dim3(w4::THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <class X, int S>
+static cudaError_t launch_rows(const w4::Params& p, const DevInfo& d, cudaStream_t st) {
+    constexpr int one = std::is_same<X, float>::value ? 2 : 8;  // tokens of one column block
+    const int64_t groups = std::min(p.M, p.E);
+    return p.M <= one * groups ? launch_few<X, S, 1>(p, d, st) : launch_few<X, S, 2>(p, d, st);
+}
+
+template <class X>
+static cudaError_t launch_scales(const w4::Params& p, const DevInfo& d, cudaStream_t st) {
+    return p.S == 32   ? launch_rows<X, 32>(p, d, st)
+           : p.S == 64 ? launch_rows<X, 64>(p, d, st)
+                       : launch_rows<X, 128>(p, d, st);
+}
 
 static qmoe_status w4_run(const char* fn, const void* W, int stype, const void* scale,
                           const uint8_t* zero, int32_t scale_cols, int32_t num_groups,
@@ -63,13 +142,16 @@ static qmoe_status w4_run(const char* fn, const void* W, int stype, const void* 
     p.E = num_groups;
     p.S = scale_cols;
     p.stype = stype;
-    p.xtype = xtype;
     p.ytype = ytype;
+    p.vec_x = aligned(x, 16) && (ldx * w4_size(xtype)) % 16 == 0;
     p.err = d->err;
-    const int64_t items = (n_rows * rows + w4::THREADS / 32 - 1) / (w4::THREADS / 32);
-    const cudaError_t e = launch_pdl(
-        w4::mm_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, d->sms * 8))),
-        dim3(w4::THREADS), 0, static_cast<cudaStream_t>(stream), p);
+    if (gmm::max_tiles(p.M, p.E, 5, (p.N + 15) / 16) > 0x7fffffff)
+        return fail(QMOE_ERR_UNSUPPORTED, "%s: rows=%lld times n=%lld is too large", fn,
+                    (long long)rows, (long long)n_rows);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = xtype == QMOE_F32    ? launch_scales<float>(p, *d, st)
+                          : xtype == QMOE_BF16 ? launch_scales<__nv_bfloat16>(p, *d, st)
+                                               : launch_scales<__half>(p, *d, st);
     if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
     return QMOE_OK;
 }

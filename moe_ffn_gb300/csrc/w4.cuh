@@ -1,8 +1,19 @@
 // w4.cuh — products with 4-bit weights: y[r][n] = sum_j W_g[n][j] x[r][j] for the rows
 // r of group g, W[n][j] = scale[n][j / S] (code[n][j] - zero[n][j / S]), S = 32, 64 or
 // 128 columns to a scale.
+//
+// The codes minus their zero point are integers of -15..15, exact in 16 bits, so the
+// tensor core multiplies them by x exactly; the sum over the columns of one scale comes
+// from it in f32, and is multiplied by the scale and added up in f32.  An f32 x is cut
+// into three bf16 values that add up to it (8 significant bits each), which take three
+// columns of the product and are added at the end.
+//
+// Orientation: weight rows are the product's M side, token rows its N side.
 #pragma once
-#include "gmm_tiles.cuh"
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gmm.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
 
@@ -18,71 +29,389 @@ struct Params {
     const int32_t* offsets; // [E + 1], or null: one group of all rows
     int64_t ldx, ldy;
     int M, N, K, E, S;
-    int stype, xtype, ytype;
+    int stype, ytype;
+    int vec_x;              // rows of x are whole aligned 16-byte units
+    int nb;                 // tiles of W
+    int nt;                 // tokens of a tile
+    int cols;               // columns that the tokens of a tile take in shared memory
+    int wk;                 // parts of K among a CTA's warps
+    int rank_units;         // 128-column units of K of a CTA of a cluster
+    int pass_rounds;        // rounds of its blocks whose x is in shared memory at a time
+    int slot;               // outputs of a tile, or 0 without a cluster
     DevCtl* err;
 };
 
-constexpr int THREADS = 256;
-
-__device__ __forceinline__ float load_typed(const void* p, int64_t i, int type) {
-    if (type == QMOE_F32) return __ldcg(static_cast<const float*>(p) + i);
-    if (type == QMOE_BF16) return to_f32(ldcg_value(static_cast<const __nv_bfloat16*>(p) + i));
-    return to_f32(ldcg_value(static_cast<const __half*>(p) + i));
+__device__ __forceinline__ float typed(uint32_t raw, int type) {
+    return type == QMOE_F32    ? __uint_as_float(raw)
+           : type == QMOE_BF16 ? __uint_as_float(raw << 16)
+                               : __half2float(__ushort_as_half(static_cast<unsigned short>(raw)));
+}
+__device__ __forceinline__ uint32_t load_raw(const void* p, int64_t i, int type) {
+    return type == QMOE_F32 ? __ldcg(static_cast<const unsigned*>(p) + i)
+                            : __ldcg(static_cast<const unsigned short*>(p) + i);
 }
 
-// A warp per output.
-__global__ void __launch_bounds__(THREADS) mm_kernel(const Params p) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void store_y(const Params& p, int64_t r, int n, float v) {
+    const int64_t at = r * p.ldy + n;
+    if (p.ytype == QMOE_F32) static_cast<float*>(p.y)[at] = v;
+    else if (p.ytype == QMOE_BF16)
+        static_cast<__nv_bfloat16*>(p.y)[at] = from_f32<__nv_bfloat16>(v);
+    else static_cast<__half*>(p.y)[at] = from_f32<__half>(v);
+}
+
+template <class X>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<X, __half>::value)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <class X>
+__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<X, __half>::value)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Codes to 16-bit values: a code in the low bits of 128.0 (bf16) or 1024.0 (f16) is
+// that plus the code, and the same with the zero point is taken from it, exactly.
+template <class X>
+struct Magic {
+    static constexpr bool F16 = std::is_same<X, __half>::value;
+    static constexpr uint32_t ONE = F16 ? 0x64006400u : 0x43004300u;
+    // both halves ONE plus byte j of z
+    static __device__ __forceinline__ uint32_t bias(uint32_t z, int j) {
+        return __byte_perm(z, ONE, 0x5050 + 0x0101 * j);
+    }
+};
+template <class X>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    if constexpr (Magic<X>::F16) {
+        const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                         *reinterpret_cast<__nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+}
+// Codes i and i + 4 of a word of eight.
+template <class X>
+__device__ __forceinline__ uint32_t codes(uint32_t w, int i, uint32_t bias) {
+    return sub2<X>(((w >> (4 * i)) & 0x000F000Fu) | Magic<X>::ONE, bias);
+}
+
+// ------------------------------------------------------- few rows per group
+// The eight warps of a CTA are WK parts of its K range times 8 / WK tiles of 16 weight
+// rows, by 8 NB columns of x.  A warp takes K in blocks of four units of 128 columns,
+// the next block's 16-byte loads in flight while this one's codes are multiplied; the
+// parts are added through shared memory in warp order, those of a cluster's CTAs, which
+// share K where there are few tiles, in rank order.
+// A lane loads the 32 codes that it multiplies from one row straight to registers, and
+// which columns the MMA's k positions stand for is chosen to fit: x lies in shared
+// memory in that order.  The columns of one scale have to be one MMA's k range: for S =
+// 128 the four lanes of a row hold 32 columns each; for 64 and 32 they first exchange
+// words.
+constexpr int WARPS = 8;
+constexpr int THREADS = 32 * WARPS;
+constexpr int UNIT = 128;
+constexpr int BLOCK = 4;      // units of a block
+constexpr int MAX_RANKS = 8;
+constexpr int RED_LD = 20;    // 16 rows of a column, padded: conflict-free
+
+// The unit's place of its o-th group of eight columns: step j, lane t of the quad.
+template <int S>
+__device__ __forceinline__ void place(int o, int* j, int* t) {
+    if (S == 128) { *t = o >> 2; *j = o & 3; }
+    else if (S == 64) { *j = ((o >> 3) << 1) | (o & 1); *t = ((o >> 2) & 1) | (o & 2); }
+    else { *j = o >> 2; *t = o & 3; }
+}
+
+// Words (one per step j) of a row after the quad's exchange.
+template <int S>
+__device__ __forceinline__ void exchange(uint4& v, int t) {
+    if constexpr (S < 128) {  // lanes t and t ^ 2
+        const bool hi = t & 2;
+        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, hi ? v.x : v.z, 2);
+        const uint32_t r1 = __shfl_xor_sync(0xffffffffu, hi ? v.y : v.w, 2);
+        if (hi) { v.x = r0; v.y = r1; } else { v.z = r0; v.w = r1; }
+    }
+    if constexpr (S == 32) {  // lanes t and t ^ 1
+        const bool odd = t & 1;
+        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1);
+        const uint32_t r1 = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 1);
+        if (odd) { v.x = r0; v.z = r1; } else { v.y = r0; v.w = r1; }
+    }
+}
+
+// Bytes of shared memory before x: the tiles' table, the warps' parts, and those of
+// the ranks (`slots` values in all).
+__host__ __device__ constexpr int few_fixed(int E, int nb_cols, int slots) {
+    return ((3 * E + 1) * 4 + 15) / 16 * 16 + 2 * WARPS * 8 * nb_cols * RED_LD * 4 +
+           slots * 2 * 4;
+}
+
+template <class X, int S, int NB>
+__global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
+    constexpr bool F32X = std::is_same<X, float>::value;
+    constexpr int PARTS = F32X ? 3 : 1;
+    constexpr int NS = UNIT / S;  // scales of a unit
+    using H = typename std::conditional<std::is_same<X, __half>::value, __half,
+                                        __nv_bfloat16>::type;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+    const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
+    const int kw = warp & (p.wk - 1), rt = warp / p.wk, rts = WARPS / p.wk;
+    int* t_lo = reinterpret_cast<int*>(smem);
+    int* t_hi = t_lo + p.E;
+    int* t_pre = t_hi + p.E;
+    float* red = reinterpret_cast<float*>(smem + ((3 * p.E + 1) * 4 + 15) / 16 * 16);
+    float* far = red + 2 * WARPS * 8 * NB * RED_LD;
+    uint4* xs = reinterpret_cast<uint4*>(smem + few_fixed(p.E, NB, p.slot * ranks));
     pdl_wait();
     pdl_trigger();
-    int bad = 0;
-    if (p.offsets)
-        for (int e = threadIdx.x; e < p.E; e += THREADS) {
-            int lo, hi;
-            if (!gmm::group_rows(__ldcg(p.offsets + e), __ldcg(p.offsets + e + 1), p.M, &lo, &hi))
-                bad = 1;
+    gmm::build_tables(p, p.nt, p.nb, t_lo, t_hi, t_pre);
+    const int tiles = t_pre[p.E];
+    if (cluster >= tiles) return;
+
+    const int units = (p.K + UNIT - 1) / UNIT;
+    const int ub = min(rank * p.rank_units, units), ue = min(ub + p.rank_units, units);
+    const int SG = p.K / S;  // scales of a row
+    // rounds: a block to each of the wk parts
+    const int rounds = max(1, (ue - ub + p.wk * BLOCK - 1) / (p.wk * BLOCK));
+
+    // what is loaded: the tile `next`, from round 0 of which on the loads follow
+    uint4 w[BLOCK][2];          // rows g and g + 8
+    uint32_t s_raw[2][NS], z_raw[2][NS];   // of the block's unit t
+    float sc[2][NS];            // of the block in hand, unit t
+    uint32_t zp[2];             // zero points, a byte each
+    gmm::Tile next;
+    const uint8_t* l_w[2];
+    int64_t l_s[2];
+    auto look_up = [&](int tile) {
+        next = gmm::tile_at_warp(tile, p.nt, 1, t_lo, t_hi, t_pre, p.E);
+        const int64_t base = static_cast<int64_t>(next.e) * p.N;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r = base + min((next.nbi * rts + rt) * 16 + g + 8 * h, p.N - 1);
+            l_w[h] = p.W + r * (p.K / 2) + t * 16;
+            l_s[h] = r * SG;
         }
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) record_error(p.err, DEV_GMM_OFFSETS);
-        return;
-    }
-    const int64_t items = static_cast<int64_t>(p.M) * p.N;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
-         it < items; it += step) {
-        const int r = static_cast<int>(it / p.N), n = static_cast<int>(it - int64_t{r} * p.N);
-        int g = 0;
-        if (p.offsets) {
-            if (r < __ldcg(p.offsets) || r >= __ldcg(p.offsets + p.E)) continue;
-            int hi = p.E;  // the last group that starts at or before r
-            while (hi - g > 1) {
-                const int mid = (g + hi) / 2;
-                if (__ldcg(p.offsets + mid) <= r) g = mid;
-                else hi = mid;
+    };
+    auto load_unit = [&](int round, int i) {
+        const int u = ub + (round * p.wk + kw) * BLOCK + i;
+        const bool in = u < ue && u * UNIT + t * 32 < p.K;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            w[i][h] = in ? __ldcg(reinterpret_cast<const uint4*>(l_w[h] + u * (UNIT / 2)))
+                         : make_uint4(0, 0, 0, 0);
+    };
+    auto load_scales = [&](int round) {
+        const int u = ub + (round * p.wk + kw) * BLOCK + t;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                const int gi = u * NS + j;
+                const bool in = u < ue && gi < SG;
+                s_raw[h][j] = in ? load_raw(p.scale, l_s[h] + gi, p.stype) : 0u;
+                z_raw[h][j] = in && p.zero ? __ldcg(p.zero + l_s[h] + gi) : 8u;
+            }
+    };
+
+    float acc[NB][4];
+    int at_col[NB];  // this lane's columns of x (one that exists where its own does not)
+    auto product = [&](int i, int unit) {  // unit: of those in shared memory
+        const uint4* xu = xs + static_cast<int64_t>(unit) * 16 * p.cols;
+        uint4 v[2] = {w[i][0], w[i][1]};
+        exchange<S>(v[0], t);
+        exchange<S>(v[1], t);
+        const int src = (lane & ~3) | i;
+        uint32_t z[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) z[h] = __shfl_sync(0xffffffffu, zp[h], src);
+        constexpr int PER = S / 32;  // steps of a scale
+        float d[NB][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t c = j == 0 ? v[h].x : j == 1 ? v[h].y : j == 2 ? v[h].z : v[h].w;
+                const uint32_t bias = Magic<H>::bias(z[h], j / PER);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) a[h][q] = codes<H>(c, q, bias);
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const uint4 b = xu[j * p.cols * 4 + at_col[n]];
+                if (j % PER == 0) mma16_first<H>(d[n], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                else mma16<H>(d[n], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                mma16<H>(d[n], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+            }
+            if (j % PER == PER - 1) {
+                const float s0 = __shfl_sync(0xffffffffu, sc[0][j / PER], src);
+                const float s8 = __shfl_sync(0xffffffffu, sc[1][j / PER], src);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    acc[n][0] = fmaf(s0, d[n][0], acc[n][0]);
+                    acc[n][1] = fmaf(s0, d[n][1], acc[n][1]);
+                    acc[n][2] = fmaf(s8, d[n][2], acc[n][2]);
+                    acc[n][3] = fmaf(s8, d[n][3], acc[n][3]);
+                }
             }
         }
-        const int64_t row = static_cast<int64_t>(g) * p.N + n;
-        const uint8_t* w = p.W + row * (p.K / 2);
-        const int64_t s0 = row * (p.K / p.S), x0 = static_cast<int64_t>(r) * p.ldx;
-        float sum = 0.f;
-        for (int j = lane * 2; j < p.K; j += 64) {
-            const int b = __ldcg(w + j / 2);
-            const int64_t s = s0 + j / p.S;
-            const int z = p.zero ? __ldcg(p.zero + s) & 15 : 8;
-            const float a = static_cast<float>((b & 15) - z) * load_typed(p.x, x0 + j, p.xtype);
-            const float c = fmaf(static_cast<float>((b >> 4) - z),
-                                 load_typed(p.x, x0 + j + 1, p.xtype), a);
-            sum = fmaf(load_typed(p.scale, s, p.stype), c, sum);
-        }
+    };
+    // x of some rounds, in the order in which the products take it: for unit, step j,
+    // column and lane t, the eight values of its place as pairs (0,4) (1,5) (2,6) (3,7)
+    auto stage_x = [&](int row0, int nv, int round) {
+        const int u0 = ub + round * p.wk * BLOCK;
+        const int n8 = min(p.pass_rounds * p.wk * BLOCK, ue - u0) * 16;  // eights of columns
+        for (int i = tid; i < n8 * nv; i += THREADS) {
+            const int tok = i / n8, o = i - tok * n8;
+            const int c = u0 * UNIT + o * 8;
+            const X* src = static_cast<const X*>(p.x) + (row0 + tok) * p.ldx + c;
+            Raw8<X> v;
+            if (c >= p.K) v.zero();
+            else if (p.vec_x) v.load(src);
+            else
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) {
-            const int64_t at = static_cast<int64_t>(r) * p.ldy + n;
-            if (p.ytype == QMOE_F32) static_cast<float*>(p.y)[at] = sum;
-            else if (p.ytype == QMOE_BF16)
-                static_cast<__nv_bfloat16*>(p.y)[at] = from_f32<__nv_bfloat16>(sum);
-            else static_cast<__half*>(p.y)[at] = from_f32<__half>(sum);
+                for (int e = 0; e < 8; ++e) {
+                    const X one = ldcg_value(src + e);
+                    if constexpr (F32X) v.w[e] = __float_as_uint(one);
+                    else reinterpret_cast<X*>(v.w)[e] = one;
+                }
+            int j, tt;
+            place<S>(o & 15, &j, &tt);
+            uint4* dst = xs + (static_cast<int64_t>(o >> 4) * 4 + j) * 4 * p.cols +
+                         tok * PARTS * 4 + tt;
+            if constexpr (F32X) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = v.get(e);
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+                    uint32_t h[8];  // the leading 8 bits, cut off; what is left is exact
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        h[e] = __float_as_uint(f[e]) >> 16;
+                        // (infinities and NaN have no rest: they stay whole in part 0)
+                        const bool fin = (h[e] & 0x7F80u) != 0x7F80u;
+                        if (!fin && (__float_as_uint(f[e]) & 0x7FFFFFu)) h[e] |= 0x40u;
+                        f[e] = fin ? f[e] - __uint_as_float(h[e] << 16) : 0.f;
+                    }
+                    dst[part * 4] = make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16,
+                                               h[2] | h[6] << 16, h[3] | h[7] << 16);
+                }
+            } else {
+                *dst = make_uint4(__byte_perm(v.w[0], v.w[2], 0x5410),
+                                  __byte_perm(v.w[0], v.w[2], 0x7632),
+                                  __byte_perm(v.w[1], v.w[3], 0x5410),
+                                  __byte_perm(v.w[1], v.w[3], 0x7632));
+            }
         }
+    };
+
+    look_up(cluster);
+    load_scales(0);
+#pragma unroll
+    for (int i = 0; i < BLOCK; ++i) load_unit(0, i);
+    int staged = -1, buf = 0;
+    for (int tile = cluster; tile < tiles; tile += clusters) {
+        const gmm::Tile c = next;
+        const bool more = tile + clusters < tiles;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            at_col[n] = min(n * 8 + g, c.nv * PARTS - 1) * 4 + t;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+        }
+        for (int round = 0; round < rounds; ++round) {
+            const int in_pass = round % p.pass_rounds;
+            if (in_pass == 0 && (p.pass_rounds < rounds || staged != c.row0)) {
+                if (round > 0) __syncthreads();  // (a tile ends with a barrier)
+                stage_x(c.row0, c.nv, round);
+                staged = c.row0;
+                __syncthreads();
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                zp[h] = 0;
+#pragma unroll
+                for (int j = 0; j < NS; ++j) {
+                    sc[h][j] = typed(s_raw[h][j], p.stype);
+                    zp[h] |= (z_raw[h][j] & 15u) << (8 * j);
+                }
+            }
+            const bool last = round + 1 == rounds;
+            if (last && more) look_up(tile + clusters);
+            const bool load = !last || more;
+            const int ahead = last ? 0 : round + 1;
+            if (load) load_scales(ahead);
+            const int unit = (in_pass * p.wk + kw) * BLOCK;
+            const int left = ue - ub - (round * p.wk + kw) * BLOCK;  // units of this block on
+#pragma unroll
+            for (int i = 0; i < BLOCK; ++i) {
+                if (i < left) product(i, unit + i);
+                if (load) load_unit(ahead, i);
+            }
+        }
+        // the warps' parts, in order (two buffers: one barrier a tile)
+        float* mine = red + (buf * WARPS + warp) * 8 * NB * RED_LD;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            float* at = mine + (n * 8 + 2 * t) * RED_LD + g;
+            at[0] = acc[n][0];
+            at[RED_LD] = acc[n][1];
+            at[8] = acc[n][2];
+            at[RED_LD + 8] = acc[n][3];
+        }
+        __syncthreads();
+        const int rows16 = rts * 16;
+        for (int i = tid; i < rows16 * c.nv; i += THREADS) {
+            const int row = i & (rows16 - 1), tok = i / rows16;
+            const float* at = red + ((buf * WARPS + (row >> 4) * p.wk) * 8 * NB + tok * PARTS) * RED_LD +
+                              (row & 15);
+            float v = 0.f;
+#pragma unroll
+            for (int part = PARTS - 1; part >= 0; --part)
+                for (int k = 0; k < p.wk; ++k) v += at[(k * 8 * NB + part) * RED_LD];
+            const int n = c.nbi * rows16 + row;
+            if (ranks > 1) cluster_st_f32(far + (buf * ranks + rank) * p.slot + i, 0u, v);
+            else if (n < p.N) store_y(p, c.row0 + tok, n, v);
+        }
+        if (ranks > 1) {
+            cluster_sync();
+            if (rank == 0)
+                for (int i = tid; i < rows16 * c.nv; i += THREADS) {
+                    const int n = c.nbi * rows16 + (i & (rows16 - 1));
+                    float v = 0.f;
+                    for (int k = 0; k < ranks; ++k) v += far[(buf * ranks + k) * p.slot + i];
+                    if (n < p.N) store_y(p, c.row0 + i / rows16, n, v);
+                }
+        }
+        buf ^= 1;
     }
 }
 
