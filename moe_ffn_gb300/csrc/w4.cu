@@ -56,6 +56,8 @@ static cudaError_t launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
         if (q.pass_rounds == rounds && (full || blocks <= w4::WARPS)) break;
     }
     const int64_t tiles = gmm::max_tiles(p.M, p.E, p.nt, p.nb);
+    p.tiles = static_cast<int>(tiles);
+    for (p.rts_log = 0; (p.wk << p.rts_log) < w4::WARPS;) ++p.rts_log;
     auto kern = w4::few_kernel<X, S, NB>;
     static std::atomic<bool> configured[64];
     if (!configured[d.dev].load()) {

@@ -32,9 +32,10 @@ struct Params {
     int stype, ytype;
     int vec_x;              // rows of x are whole aligned 16-byte units
     int nb;                 // tiles of W
+    int tiles;              // of the call, without offsets
     int nt;                 // tokens of a tile
     int cols;               // columns that the tokens of a tile take in shared memory
-    int wk;                 // parts of K among a CTA's warps
+    int wk, rts_log;        // parts of K among a CTA's warps; 2^rts_log = 8 / wk row tiles
     int rank_units;         // 128-column units of K of a CTA of a cluster
     int pass_rounds;        // rounds of its blocks whose x is in shared memory at a time
     int slot;               // outputs of a tile, or 0 without a cluster
@@ -63,14 +64,12 @@ template <class X>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
     if constexpr (std::is_same<X, __half>::value)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -80,45 +79,52 @@ template <class X>
 __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1) {
     if constexpr (std::is_same<X, __half>::value)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%10,%10,%10,%10};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
     else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%10,%10,%10,%10};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Codes to 16-bit values: a code in the low bits of 128.0 (bf16) or 1024.0 (f16) is
-// that plus the code, and the same with the zero point is taken from it, exactly.
+// Codes to 16-bit values, exactly.  The bits of a code at the low end of a 16-bit float
+// are a subnormal: code 2^-24 (f16) or code 2^-133 (bf16; the encoding stays linear over
+// the first eight bits).  One fused multiplication by a power of two brings it into the
+// normal range and takes the zero point from it: (code - zero) / UP, so that a word of
+// eight codes costs one shift, four ANDs and four of these.  UP comes back in the end.
 template <class X>
 struct Magic {
     static constexpr bool F16 = std::is_same<X, __half>::value;
-    static constexpr uint32_t ONE = F16 ? 0x64006400u : 0x43004300u;
-    // both halves ONE plus byte j of z
-    static __device__ __forceinline__ uint32_t bias(uint32_t z, int j) {
-        return __byte_perm(z, ONE, 0x5050 + 0x0101 * j);
+    static constexpr float UP = F16 ? 512.f : 64.f;
+    // multipliers of codes in bits 0..3 and 4..7 of a half: 2^15, 2^11 or 2^127, 2^123
+    static constexpr uint32_t LOW = F16 ? 0x78007800u : 0x7F007F00u;
+    static constexpr uint32_t HIGH = F16 ? 0x68006800u : 0x7D007D00u;
+    // -zero / UP, twice
+    static __device__ __forceinline__ uint32_t bias(uint32_t zero) {
+        const float v = static_cast<float>(zero & 15u) * (-1.f / UP);
+        return F16 ? pack_f16(v, v) : pack_bf16(v, v);
     }
 };
 template <class X>
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-    if constexpr (Magic<X>::F16) {
-        const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    } else {
-        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
-                                         *reinterpret_cast<__nv_bfloat162*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    if constexpr (Magic<X>::F16)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
 }
-// Codes i and i + 4 of a word of eight.
+// A word of eight codes: a[i] holds codes i and i + 4.
 template <class X>
-__device__ __forceinline__ uint32_t codes(uint32_t w, int i, uint32_t bias) {
-    return sub2<X>(((w >> (4 * i)) & 0x000F000Fu) | Magic<X>::ONE, bias);
+__device__ __forceinline__ void codes(uint32_t w, uint32_t bias, uint32_t (&a)[4]) {
+    const uint32_t v = w >> 8;
+    a[0] = fma2<X>(w & 0x000F000Fu, Magic<X>::LOW, bias);
+    a[1] = fma2<X>(w & 0x00F000F0u, Magic<X>::HIGH, bias);
+    a[2] = fma2<X>(v & 0x000F000Fu, Magic<X>::LOW, bias);
+    a[3] = fma2<X>(v & 0x00F000F0u, Magic<X>::HIGH, bias);
 }
 
 // ------------------------------------------------------- few rows per group
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
     const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
-    const int kw = warp & (p.wk - 1), rt = warp / p.wk, rts = WARPS / p.wk;
+    const int kw = warp >> p.rts_log, rts = 1 << p.rts_log, rt = warp & (rts - 1);
     int* t_lo = reinterpret_cast<int*>(smem);
     int* t_hi = t_lo + p.E;
     int* t_pre = t_hi + p.E;
@@ -191,9 +197,12 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     uint4* xs = reinterpret_cast<uint4*>(smem + few_fixed(p.E, NB, p.slot * ranks));
     pdl_wait();
     pdl_trigger();
-    gmm::build_tables(p, p.nt, p.nb, t_lo, t_hi, t_pre);
-    const int tiles = t_pre[p.E];
-    if (cluster >= tiles) return;
+    int tiles = p.tiles;
+    if (p.offsets) {
+        gmm::build_tables(p, p.nt, p.nb, t_lo, t_hi, t_pre);
+        tiles = t_pre[p.E];
+        if (cluster >= tiles) return;
+    }
 
     const int units = (p.K + UNIT - 1) / UNIT;
     const int ub = min(rank * p.rank_units, units), ue = min(ub + p.rank_units, units);
@@ -201,71 +210,84 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     // rounds: a block to each of the wk parts
     const int rounds = max(1, (ue - ub + p.wk * BLOCK - 1) / (p.wk * BLOCK));
 
-    // what is loaded: the tile `next`, from round 0 of which on the loads follow
-    uint4 w[BLOCK][2];          // rows g and g + 8
+    // what is loaded: rounds of the tile `next`
+    uint4 w[BLOCK][2];                     // rows g and g + 8
     uint32_t s_raw[2][NS], z_raw[2][NS];   // of the block's unit t
-    float sc[2][NS];            // of the block in hand, unit t
-    uint32_t zp[2];             // zero points, a byte each
     gmm::Tile next;
     const uint8_t* l_w[2];
     int64_t l_s[2];
     auto look_up = [&](int tile) {
-        next = gmm::tile_at_warp(tile, p.nt, 1, t_lo, t_hi, t_pre, p.E);
+        if (p.offsets) {
+            next = gmm::tile_at_warp(tile, p.nt, 1, t_lo, t_hi, t_pre, p.E);
+        } else {
+            const int lo = 0, hi = p.M;
+            next = gmm::tile_in(0, tile, p.nt, 1, &lo, &hi, &lo);
+        }
         const int64_t base = static_cast<int64_t>(next.e) * p.N;
+        const int n = (next.nbi * rts + rt) * 16 + g;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t r = base + min((next.nbi * rts + rt) * 16 + g + 8 * h, p.N - 1);
+            const int64_t r = base + min(n + 8 * h, p.N - 1);
             l_w[h] = p.W + r * (p.K / 2) + t * 16;
             l_s[h] = r * SG;
         }
     };
-    auto load_unit = [&](int round, int i) {
-        const int u = ub + (round * p.wk + kw) * BLOCK + i;
-        const bool in = u < ue && u * UNIT + t * 32 < p.K;
+    // the first unit of this warp's block of a round, and whether the block is whole
+    auto block_at = [&](int round) { return ub + (round * p.wk + kw) * BLOCK; };
+    auto whole = [&](int u) { return u + BLOCK <= ue && (u + BLOCK) * UNIT <= p.K; };
+    auto load_unit = [&](int u, bool all, int i) {
+        if (all) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            w[i][h] = in ? __ldcg(reinterpret_cast<const uint4*>(l_w[h] + u * (UNIT / 2)))
-                         : make_uint4(0, 0, 0, 0);
+            for (int h = 0; h < 2; ++h)
+                w[i][h] = __ldcg(reinterpret_cast<const uint4*>(l_w[h] + u * (UNIT / 2)) +
+                                 i * (UNIT / 32));
+        } else {
+            const bool in = u + i < ue && (u + i) * UNIT + t * 32 < p.K;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[i][h] = in ? __ldcg(reinterpret_cast<const uint4*>(l_w[h] + (u + i) * (UNIT / 2)))
+                             : make_uint4(0, 0, 0, 0);
+        }
     };
-    auto load_scales = [&](int round) {
-        const int u = ub + (round * p.wk + kw) * BLOCK + t;
+    auto load_scales = [&](int u, bool all) {
+        const int gi = (u + t) * NS;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-                const int gi = u * NS + j;
-                const bool in = u < ue && gi < SG;
-                s_raw[h][j] = in ? load_raw(p.scale, l_s[h] + gi, p.stype) : 0u;
-                z_raw[h][j] = in && p.zero ? __ldcg(p.zero + l_s[h] + gi) : 8u;
+                const bool in = all || (u + t < ue && gi + j < SG);
+                s_raw[h][j] = 0u;
+                z_raw[h][j] = 8u;
+                if (in) s_raw[h][j] = load_raw(p.scale, l_s[h] + gi + j, p.stype);
+                if (in && p.zero) z_raw[h][j] = __ldcg(p.zero + l_s[h] + gi + j);
             }
     };
 
+    float sc[2][NS];      // of the block in hand, unit t
+    uint32_t zb[2][NS];
     float acc[NB][4];
-    int at_col[NB];  // this lane's columns of x (one that exists where its own does not)
-    auto product = [&](int i, int unit) {  // unit: of those in shared memory
-        const uint4* xu = xs + static_cast<int64_t>(unit) * 16 * p.cols;
+    int at_col[NB];       // this lane's columns of x (one that exists where its own does not)
+    const int js = p.cols * 4;
+    auto product = [&](int i, const uint4* xu) {
         uint4 v[2] = {w[i][0], w[i][1]};
         exchange<S>(v[0], t);
         exchange<S>(v[1], t);
         const int src = (lane & ~3) | i;
-        uint32_t z[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) z[h] = __shfl_sync(0xffffffffu, zp[h], src);
         constexpr int PER = S / 32;  // steps of a scale
         float d[NB][4];
+        uint32_t bias[2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t a[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t c = j == 0 ? v[h].x : j == 1 ? v[h].y : j == 2 ? v[h].z : v[h].w;
-                const uint32_t bias = Magic<H>::bias(z[h], j / PER);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) a[h][q] = codes<H>(c, q, bias);
+                if (j % PER == 0) bias[h] = __shfl_sync(0xffffffffu, zb[h][j / PER], src);
+                codes<H>(c, bias[h], a[h]);
             }
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const uint4 b = xu[j * p.cols * 4 + at_col[n]];
+                const uint4 b = xu[j * js + at_col[n]];
                 if (j % PER == 0) mma16_first<H>(d[n], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
                 else mma16<H>(d[n], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
                 mma16<H>(d[n], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
@@ -334,9 +356,13 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     };
 
     look_up(cluster);
-    load_scales(0);
+    {
+        const int u = block_at(0);
+        const bool all = whole(u);
+        load_scales(u, all);
 #pragma unroll
-    for (int i = 0; i < BLOCK; ++i) load_unit(0, i);
+        for (int i = 0; i < BLOCK; ++i) load_unit(u, all, i);
+    }
     int staged = -1, buf = 0;
     for (int tile = cluster; tile < tiles; tile += clusters) {
         const gmm::Tile c = next;
@@ -347,8 +373,8 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
         }
+        int in_pass = 0;
         for (int round = 0; round < rounds; ++round) {
-            const int in_pass = round % p.pass_rounds;
             if (in_pass == 0 && (p.pass_rounds < rounds || staged != c.row0)) {
                 if (round > 0) __syncthreads();  // (a tile ends with a barrier)
                 stage_x(c.row0, c.nv, round);
@@ -356,47 +382,46 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
                 __syncthreads();
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                zp[h] = 0;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < NS; ++j) {
                     sc[h][j] = typed(s_raw[h][j], p.stype);
-                    zp[h] |= (z_raw[h][j] & 15u) << (8 * j);
+                    zb[h][j] = Magic<H>::bias(z_raw[h][j]);
                 }
-            }
             const bool last = round + 1 == rounds;
             if (last && more) look_up(tile + clusters);
             const bool load = !last || more;
-            const int ahead = last ? 0 : round + 1;
-            if (load) load_scales(ahead);
-            const int unit = (in_pass * p.wk + kw) * BLOCK;
-            const int left = ue - ub - (round * p.wk + kw) * BLOCK;  // units of this block on
+            const int u = block_at(last ? 0 : round + 1);
+            const bool all = whole(u);
+            if (load) load_scales(u, all);
+            const int left = ue - block_at(round);  // units of this block and after it
+            const uint4* xu = xs + static_cast<int64_t>((in_pass * p.wk + kw) * BLOCK) * 4 * js;
 #pragma unroll
             for (int i = 0; i < BLOCK; ++i) {
-                if (i < left) product(i, unit + i);
-                if (load) load_unit(ahead, i);
+                if (i < left) product(i, xu + i * 4 * js);
+                if (load) load_unit(u, all, i);
             }
+            if (++in_pass == p.pass_rounds) in_pass = 0;
         }
         // the warps' parts, in order (two buffers: one barrier a tile)
         float* mine = red + (buf * WARPS + warp) * 8 * NB * RED_LD;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             float* at = mine + (n * 8 + 2 * t) * RED_LD + g;
-            at[0] = acc[n][0];
-            at[RED_LD] = acc[n][1];
-            at[8] = acc[n][2];
-            at[RED_LD + 8] = acc[n][3];
+            at[0] = acc[n][0] * Magic<H>::UP;
+            at[RED_LD] = acc[n][1] * Magic<H>::UP;
+            at[8] = acc[n][2] * Magic<H>::UP;
+            at[RED_LD + 8] = acc[n][3] * Magic<H>::UP;
         }
         __syncthreads();
-        const int rows16 = rts * 16;
+        const int shift = 4 + p.rts_log, rows16 = 16 << p.rts_log;
         for (int i = tid; i < rows16 * c.nv; i += THREADS) {
-            const int row = i & (rows16 - 1), tok = i / rows16;
-            const float* at = red + ((buf * WARPS + (row >> 4) * p.wk) * 8 * NB + tok * PARTS) * RED_LD +
-                              (row & 15);
+            const int row = i & (rows16 - 1), tok = i >> shift;
+            const float* at = red + ((buf * WARPS + (row >> 4)) * 8 * NB + tok * PARTS) * RED_LD + (row & 15);
             float v = 0.f;
 #pragma unroll
             for (int part = PARTS - 1; part >= 0; --part)
-                for (int k = 0; k < p.wk; ++k) v += at[(k * 8 * NB + part) * RED_LD];
+                for (int k = 0; k < p.wk; ++k) v += at[((k << p.rts_log) * 8 * NB + part) * RED_LD];
             const int n = c.nbi * rows16 + row;
             if (ranks > 1) cluster_st_f32(far + (buf * ranks + rank) * p.slot + i, 0u, v);
             else if (n < p.N) store_y(p, c.row0 + tok, n, v);
@@ -408,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
                     const int n = c.nbi * rows16 + (i & (rows16 - 1));
                     float v = 0.f;
                     for (int k = 0; k < ranks; ++k) v += far[(buf * ranks + k) * p.slot + i];
-                    if (n < p.N) store_y(p, c.row0 + i / rows16, n, v);
+                    if (n < p.N) store_y(p, c.row0 + (i >> shift), n, v);
                 }
         }
         buf ^= 1;
