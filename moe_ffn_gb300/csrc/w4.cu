@@ -11,12 +11,14 @@
 #include "../../include/qmoe.h"
 #include "host.cuh"
 #include "w4.cuh"
+#include "w4_many.cuh"
 
 namespace qmoe {
 
 constexpr int64_t W4_MAX_COLS = 1 << 20;
 constexpr int64_t W4_MAX_ROWS = 0x7fffff00;
 constexpr int W4_MAX_GROUPS = 1024;
+constexpr int W4_FEW = 8;  // rows per group up to which the kernel for few rows is taken
 
 static int w4_size(int t) { return t == QMOE_F32 ? 4 : t == QMOE_BF16 || t == QMOE_F16 ? 2 : 0; }
 
@@ -84,15 +86,78 @@ static cudaError_t launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// The codes as [E][N][K / 2] bytes, boxes of 256 rows by 64 bytes.
+static qmoe_status codes_map(CUtensorMap* m, const w4::Params& p) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return fail(QMOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t row = static_cast<cuuint64_t>(p.K / 2);
+    const cuuint64_t dims[3] = {row, static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.E)};
+    const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(p.N)};
+    const cuuint32_t box[3] = {64, w4::MANY_ROWS, 1};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.W), dims,
+                          strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(QMOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return QMOE_OK;
+}
+
+// The kernel for many rows: a CTA per SM, or clusters that share K while the tiles are
+// fewer.
 template <class X, int S>
-static cudaError_t launch_rows(const w4::Params& p, const DevInfo& d, cudaStream_t st) {
+static qmoe_status launch_many(w4::Params p, const DevInfo& d, cudaStream_t st) {
+    using C = w4::Many<X, S>;
+    static_assert(C::smem(W4_MAX_GROUPS) + 256 <= 232448, "shared memory, static arrays included");
+    auto kern = w4::many_kernel<C, X>;
+    static std::atomic<bool> configured[64];
+    if (!configured[d.dev].load()) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(W4_MAX_GROUPS));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(4-bit product)");
+        configured[d.dev].store(true);
+    }
+    CUtensorMap tw;
+    if (qmoe_status s = codes_map(&tw, p)) return s;
+    p.nb = (p.N + w4::MANY_ROWS - 1) / w4::MANY_ROWS;
+    const int64_t tiles = gmm::max_tiles(p.M, p.E, w4::MANY_NT, p.nb);
+    const int kb = (p.K + 127) / 128;
+    int ranks = 1;
+    while (ranks < gmm::MAX_RANKS && 2 * ranks * tiles <= d.sms && 2 * ranks <= kb) ranks *= 2;
+    const int clusters = static_cast<int>(std::min<int64_t>(tiles, ranks > 1 ? tiles : d.sms));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
+    cfg.blockDim = dim3(w4::MANY_THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.E));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, tw);
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
+    return QMOE_OK;
+}
+
+template <class X, int S>
+static qmoe_status launch_rows(const w4::Params& p, const DevInfo& d, cudaStream_t st) {
     constexpr int one = std::is_same<X, float>::value ? 2 : 8;  // tokens of one column block
     const int64_t groups = std::min(p.M, p.E);
-    return p.M <= one * groups ? launch_few<X, S, 1>(p, d, st) : launch_few<X, S, 2>(p, d, st);
+    if (p.M > W4_FEW * groups) return launch_many<X, S>(p, d, st);
+    const cudaError_t e =
+        p.M <= one * groups ? launch_few<X, S, 1>(p, d, st) : launch_few<X, S, 2>(p, d, st);
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
+    return QMOE_OK;
 }
 
 template <class X>
-static cudaError_t launch_scales(const w4::Params& p, const DevInfo& d, cudaStream_t st) {
+static qmoe_status launch_scales(const w4::Params& p, const DevInfo& d, cudaStream_t st) {
     return p.S == 32   ? launch_rows<X, 32>(p, d, st)
            : p.S == 64 ? launch_rows<X, 64>(p, d, st)
                        : launch_rows<X, 128>(p, d, st);
@@ -151,11 +216,9 @@ static qmoe_status w4_run(const char* fn, const void* W, int stype, const void* 
         return fail(QMOE_ERR_UNSUPPORTED, "%s: rows=%lld times n=%lld is too large", fn,
                     (long long)rows, (long long)n_rows);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = xtype == QMOE_F32    ? launch_scales<float>(p, *d, st)
-                          : xtype == QMOE_BF16 ? launch_scales<__nv_bfloat16>(p, *d, st)
-                                               : launch_scales<__half>(p, *d, st);
-    if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
-    return QMOE_OK;
+    return xtype == QMOE_F32    ? launch_scales<float>(p, *d, st)
+           : xtype == QMOE_BF16 ? launch_scales<__nv_bfloat16>(p, *d, st)
+                                : launch_scales<__half>(p, *d, st);
 }
 
 }  // namespace qmoe

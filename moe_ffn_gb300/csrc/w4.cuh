@@ -127,6 +127,35 @@ __device__ __forceinline__ void codes(uint32_t w, uint32_t bias, uint32_t (&a)[4
     a[3] = fma2<X>(v & 0x00F000F0u, Magic<X>::HIGH, bias);
 }
 
+// Eight values of x as the products take them, pairs (0,4) (1,5) (2,6) (3,7); an f32 x in
+// three parts of eight leading bits each, cut off one after another, which leaves exact
+// rests.  (Infinities and NaN have no rest: they stay whole in part 0.)
+template <class X>
+__device__ __forceinline__ void pack_x(const Raw8<X>& v,
+                                       uint4 (&out)[std::is_same<X, float>::value ? 3 : 1]) {
+    if constexpr (std::is_same<X, float>::value) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = v.get(e);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[e] = __float_as_uint(f[e]) >> 16;
+                const bool finite = (h[e] & 0x7F80u) != 0x7F80u;
+                if (!finite && (__float_as_uint(f[e]) & 0x7FFFFFu)) h[e] |= 0x40u;
+                f[e] = finite ? f[e] - __uint_as_float(h[e] << 16) : 0.f;
+            }
+            out[q] = make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16,
+                                h[3] | h[7] << 16);
+        }
+    } else {
+        out[0] = make_uint4(__byte_perm(v.w[0], v.w[2], 0x5410), __byte_perm(v.w[0], v.w[2], 0x7632),
+                            __byte_perm(v.w[1], v.w[3], 0x5410), __byte_perm(v.w[1], v.w[3], 0x7632));
+    }
+}
+
 // ------------------------------------------------------- few rows per group
 // The eight warps of a CTA are WK parts of its K range times 8 / WK tiles of 16 weight
 // rows, by 8 NB columns of x.  A warp takes K in blocks of four units of 128 columns,
@@ -328,30 +357,10 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
             place<S>(o & 15, &j, &tt);
             uint4* dst = xs + (static_cast<int64_t>(o >> 4) * 4 + j) * 4 * p.cols +
                          tok * PARTS * 4 + tt;
-            if constexpr (F32X) {
-                float f[8];
+            uint4 out[PARTS];
+            pack_x<X>(v, out);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = v.get(e);
-#pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    uint32_t h[8];  // the leading 8 bits, cut off; what is left is exact
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        h[e] = __float_as_uint(f[e]) >> 16;
-                        // (infinities and NaN have no rest: they stay whole in part 0)
-                        const bool fin = (h[e] & 0x7F80u) != 0x7F80u;
-                        if (!fin && (__float_as_uint(f[e]) & 0x7FFFFFu)) h[e] |= 0x40u;
-                        f[e] = fin ? f[e] - __uint_as_float(h[e] << 16) : 0.f;
-                    }
-                    dst[part * 4] = make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16,
-                                               h[2] | h[6] << 16, h[3] | h[7] << 16);
-                }
-            } else {
-                *dst = make_uint4(__byte_perm(v.w[0], v.w[2], 0x5410),
-                                  __byte_perm(v.w[0], v.w[2], 0x7632),
-                                  __byte_perm(v.w[1], v.w[3], 0x5410),
-                                  __byte_perm(v.w[1], v.w[3], 0x7632));
-            }
+            for (int q = 0; q < PARTS; ++q) dst[q * 4] = out[q];
         }
     };
 
