@@ -86,61 +86,87 @@ static cudaError_t launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// The codes as [E][N][K / 2] bytes, boxes of 256 rows by 64 bytes.
-static qmoe_status codes_map(CUtensorMap* m, const w4::Params& p) {
+static qmoe_status tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
+                              const cuuint64_t* dims, const cuuint64_t* strides,
+                              const cuuint32_t* box) {
     const EncodeTiledFn fn = encode_tiled();
     if (!fn) return fail(QMOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint64_t row = static_cast<cuuint64_t>(p.K / 2);
-    const cuuint64_t dims[3] = {row, static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.E)};
-    const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(p.N)};
-    const cuuint32_t box[3] = {64, w4::MANY_ROWS, 1};
     const cuuint32_t estride[3] = {1, 1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.W), dims,
-                          strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = fn(m, type, rank, const_cast<void*>(base), dims, strides, box, estride,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(QMOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
     return QMOE_OK;
 }
+// The codes as [E][N][K / 2] bytes, boxes of 256 rows by 128 bytes.
+static qmoe_status codes_map(CUtensorMap* m, const w4::Params& p) {
+    const cuuint64_t row = static_cast<cuuint64_t>(p.K / 2);
+    const cuuint64_t dims[3] = {row, static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.E)};
+    const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(p.N)};
+    const cuuint32_t box[3] = {128, w4::MANY_ROWS, 1};
+    return tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.W, dims, strides, box);
+}
+// 16-bit token rows, boxes of 64 rows by 64 columns.
+static qmoe_status rows_map(CUtensorMap* m, const w4::Params& p, bool bf16) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.ldx) * 2};
+    const cuuint32_t box[2] = {64, w4::MANY_NT};
+    return tensor_map(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      2, p.x, dims, strides, box);
+}
 
 // The kernel for many rows: a CTA per SM, or clusters that share K while the tiles are
 // fewer.
-template <class X, int S>
+template <class C>
 static qmoe_status launch_many(w4::Params p, const DevInfo& d, cudaStream_t st) {
-    using C = w4::Many<X, S>;
     static_assert(C::smem(W4_MAX_GROUPS) + 256 <= 232448, "shared memory, static arrays included");
-    auto kern = w4::many_kernel<C, X>;
+    auto kern = w4::many_kernel<C>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.E));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    // clusters of two, four and eight that the GPU holds at once
+    static std::atomic<int> fit[64][3];
     static std::atomic<bool> configured[64];
     if (!configured[d.dev].load()) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(W4_MAX_GROUPS));
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(4-bit product)");
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::smem(W4_MAX_GROUPS));
+        cfg.numAttrs = 1;
+        for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+            int n = 0;
+            attr[0].val.clusterDim.x = 2u << i;
+            cfg.gridDim = dim3(2u << i);
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            fit[d.dev][i].store(n);
+        }
+        if (e != cudaSuccess) return cuda_fail(e, "setting up the 4-bit product");
         configured[d.dev].store(true);
     }
-    CUtensorMap tw;
+    CUtensorMap tw, tx;
     if (qmoe_status s = codes_map(&tw, p)) return s;
+    tx = tw;
+    if constexpr (C::TMA_X)
+        if (qmoe_status s = rows_map(&tx, p, std::is_same<typename C::X, __nv_bfloat16>::value))
+            return s;
     p.nb = (p.N + w4::MANY_ROWS - 1) / w4::MANY_ROWS;
     const int64_t tiles = gmm::max_tiles(p.M, p.E, w4::MANY_NT, p.nb);
     const int kb = (p.K + 127) / 128;
     int ranks = 1;
-    while (ranks < gmm::MAX_RANKS && 2 * ranks * tiles <= d.sms && 2 * ranks <= kb) ranks *= 2;
-    const int clusters = static_cast<int>(std::min<int64_t>(tiles, ranks > 1 ? tiles : d.sms));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
-    cfg.blockDim = dim3(w4::MANY_THREADS);
-    cfg.dynamicSmemBytes = static_cast<size_t>(C::smem(p.E));
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
+    for (int i = 0; i < 3 && tiles <= fit[d.dev][i].load() && (2 << i) <= kb; ++i) ranks = 2 << i;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, tw);
+    cfg.gridDim = dim3(static_cast<unsigned>(
+        ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, d.sms)));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, tw, tx);
     if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
     return QMOE_OK;
 }
@@ -149,7 +175,11 @@ template <class X, int S>
 static qmoe_status launch_rows(const w4::Params& p, const DevInfo& d, cudaStream_t st) {
     constexpr int one = std::is_same<X, float>::value ? 2 : 8;  // tokens of one column block
     const int64_t groups = std::min(p.M, p.E);
-    if (p.M > W4_FEW * groups) return launch_many<X, S>(p, d, st);
+    if (p.M > W4_FEW * groups) {
+        if constexpr (!std::is_same<X, float>::value)
+            if (p.vec_x) return launch_many<w4::Many<X, S, true>>(p, d, st);
+        return launch_many<w4::Many<X, S, false>>(p, d, st);
+    }
     const cudaError_t e =
         p.M <= one * groups ? launch_few<X, S, 1>(p, d, st) : launch_few<X, S, 2>(p, d, st);
     if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");

@@ -60,6 +60,29 @@ __device__ __forceinline__ void store_y(const Params& p, int64_t r, int n, float
     else static_cast<__half*>(p.y)[at] = from_f32<__half>(v);
 }
 
+// Weight row n of a tile's tokens.
+template <int NT>
+__device__ __forceinline__ void store_column(const Params& p, const gmm::Tile& c, int n,
+                                             const float (&v)[NT], float up) {
+    const int64_t at = static_cast<int64_t>(c.row0) * p.ldy + n;
+    if (p.ytype == QMOE_F32) {
+        float* y = static_cast<float*>(p.y) + at;
+#pragma unroll
+        for (int i = 0; i < NT; ++i, y += p.ldy)
+            if (i < c.nv) *y = v[i] * up;
+    } else if (p.ytype == QMOE_BF16) {
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
+#pragma unroll
+        for (int i = 0; i < NT; ++i, y += p.ldy)
+            if (i < c.nv) *y = from_f32<__nv_bfloat16>(v[i] * up);
+    } else {
+        __half* y = static_cast<__half*>(p.y) + at;
+#pragma unroll
+        for (int i = 0; i < NT; ++i, y += p.ldy)
+            if (i < c.nv) *y = from_f32<__half>(v[i] * up);
+    }
+}
+
 template <class X>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -127,29 +150,34 @@ __device__ __forceinline__ void codes(uint32_t w, uint32_t bias, uint32_t (&a)[4
     a[3] = fma2<X>(v & 0x00F000F0u, Magic<X>::HIGH, bias);
 }
 
-// Eight values of x as the products take them, pairs (0,4) (1,5) (2,6) (3,7); an f32 x in
-// three parts of eight leading bits each, cut off one after another, which leaves exact
-// rests.  (Infinities and NaN have no rest: they stay whole in part 0.)
+// Eight f32 values in three bf16 parts each (their bits), of eight leading bits, cut off one
+// after another, which leaves exact rests.  (Infinities and NaN have no rest: they stay
+// whole in part 0.)
+__device__ __forceinline__ void split3(const Raw8<float>& v, uint32_t (&h)[3][8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float f = v.get(e);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            h[q][e] = __float_as_uint(f) >> 16;
+            const bool finite = (h[q][e] & 0x7F80u) != 0x7F80u;
+            if (!finite && (__float_as_uint(f) & 0x7FFFFFu)) h[q][e] |= 0x40u;
+            f = finite ? f - __uint_as_float(h[q][e] << 16) : 0.f;
+        }
+    }
+}
+// Eight values of x as pairs (0,4) (1,5) (2,6) (3,7), the order in which codes() leaves a
+// word; an f32 x in three parts.
 template <class X>
 __device__ __forceinline__ void pack_x(const Raw8<X>& v,
                                        uint4 (&out)[std::is_same<X, float>::value ? 3 : 1]) {
     if constexpr (std::is_same<X, float>::value) {
-        float f[8];
+        uint32_t h[3][8];
+        split3(v, h);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v.get(e);
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                h[e] = __float_as_uint(f[e]) >> 16;
-                const bool finite = (h[e] & 0x7F80u) != 0x7F80u;
-                if (!finite && (__float_as_uint(f[e]) & 0x7FFFFFu)) h[e] |= 0x40u;
-                f[e] = finite ? f[e] - __uint_as_float(h[e] << 16) : 0.f;
-            }
-            out[q] = make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16,
-                                h[3] | h[7] << 16);
-        }
+        for (int q = 0; q < 3; ++q)
+            out[q] = make_uint4(h[q][0] | h[q][4] << 16, h[q][1] | h[q][5] << 16,
+                                h[q][2] | h[q][6] << 16, h[q][3] | h[q][7] << 16);
     } else {
         out[0] = make_uint4(__byte_perm(v.w[0], v.w[2], 0x5410), __byte_perm(v.w[0], v.w[2], 0x7632),
                             __byte_perm(v.w[1], v.w[3], 0x5410), __byte_perm(v.w[1], v.w[3], 0x7632));
