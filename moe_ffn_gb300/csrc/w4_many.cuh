@@ -38,17 +38,17 @@ struct Many {
     static constexpr int W_BYTES = MANY_ROWS * 128;
     static constexpr int X_TILE = MANY_NT * 128;   // 64 columns of a part
     static constexpr int X_BYTES = PARTS * 2 * X_TILE;
-    // warps: 0 MMA, 1 TMA, 2-3 scales; then [4 token rows], 16 codes, 8 sums
-    static constexpr int FIRST = TMA_X ? 4 : 8;
+    // warps: 0-1 MMA, one to a half, 2 TMA, 3 scales if 4-7 load token rows, else 4-7
+    // scales, 16 codes, 8 sums
+    static constexpr int FIRST = 8;
     static constexpr int THREADS = (FIRST + 24) * 32;
-    // registers per thread after the split; with the launch's, they add up to no more
-    // than the launch was given (72 or 64 for all)
-    static constexpr int REGS_LAUNCH = TMA_X ? 72 : 64;
-    static constexpr int REGS_AUX = TMA_X ? 56 : 40, REGS_X = 56, REGS_CODES = TMA_X ? 56 : 48,
-                         REGS_SUMS = 112;
-    static_assert(REGS_AUX + (TMA_X ? 0 : REGS_X) + 4 * REGS_CODES + 2 * REGS_SUMS <=
-                      REGS_LAUNCH * (FIRST + 24) / 4, "register split");
-    static constexpr int BATCH = F32X ? 2 : 4;     // eights of columns in flight per thread
+    // registers per thread after the split: no more in all than the launch was given,
+    // 64 for each
+    static constexpr int REGS_AUX = 40, REGS_CODES = 56, REGS_SUMS = 104;
+    static_assert(2 * REGS_AUX + 4 * REGS_CODES + 2 * REGS_SUMS <= 64 * (FIRST + 24) / 4,
+                  "register split");
+    static constexpr int S_WARPS = TMA_X ? 4 : 1;  // for scales
+    static constexpr int BATCH = F32X ? 1 : 2;     // eights of columns in flight per thread
     static constexpr int TM_A = DB * 2 * MANY_NT, TM_COLS = 512;
     static_assert(TM_A + AB * 2 * 64 <= TM_COLS, "tensor memory");
     static constexpr int O_W = XS * X_BYTES;
@@ -129,9 +129,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int i = 0; i < C::WS; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_empty[i], 16); }
         for (int i = 0; i < C::XS; ++i) {
             mbar_init(&x_full[i], C::TMA_X ? 1 : 4);
-            mbar_init(&x_empty[i], 1);
+            mbar_init(&x_empty[i], 2);
         }
-        for (int i = 0; i < C::SR; ++i) { mbar_init(&s_full[i], 2); mbar_init(&s_empty[i], 24); }
+        for (int i = 0; i < C::SR; ++i) { mbar_init(&s_full[i], C::S_WARPS); mbar_init(&s_empty[i], 24); }
         for (int i = 0; i < 2 * C::AB; ++i) { mbar_init(&a_full[i], 4); mbar_init(&a_empty[i], 1); }
         for (int i = 0; i < 2 * C::DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 4); }
         fence_barrier_init();
@@ -166,77 +166,161 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     auto wait = [&](uint64_t* b, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait_spin(b, parity, p.err, DEV_GMM_TIMEOUT)) != 0;
     };
+    // scales: chunks of four per row, for `n` threads
+    auto scales = [&](int th, int n) {
+        const int SG = p.K / C::S;
+        const int ss = p.stype == QMOE_F32 ? 4 : 2;
+        const bool vec = SG % 4 == 0 && (kbeg * C::GPB) % 4 == 0 &&
+                         reinterpret_cast<uintptr_t>(p.scale) % (4 * ss) == 0 &&
+                         reinterpret_cast<uintptr_t>(p.zero) % 4 == 0;
+        uint32_t ch = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
+            const gmm::Tile c = tile_of(t);
+            for (int k = 0; k < nkb && ok; k += C::CB, ++ch) {
+                const int g0 = (kbeg + k) * C::GPB;
+                const uint32_t s = ch % C::SR;
+                const bool whole = vec && g0 + 4 <= SG;
+                for (int r0 = th; r0 < MANY_ROWS; r0 += 2 * n) {
+                    uint4 raw[2];  // as they lie: four of 32 bits, or .x and .y two of 16 each
+                    uint32_t zero[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = min(c.nbi * MANY_ROWS + r0 + j * n, p.N - 1);
+                        const int64_t at = (static_cast<int64_t>(c.e) * p.N + r) * SG + g0;
+                        zero[j] = 0x08080808u;
+                        if (whole) {
+                            if (ss == 4) {
+                                raw[j] = __ldcg(reinterpret_cast<const uint4*>(
+                                    static_cast<const float*>(p.scale) + at));
+                            } else {
+                                const uint2 q = __ldcg(reinterpret_cast<const uint2*>(
+                                    static_cast<const uint16_t*>(p.scale) + at));
+                                raw[j].x = q.x;
+                                raw[j].y = q.y;
+                            }
+                            if (p.zero)
+                                zero[j] = __ldcg(reinterpret_cast<const uint32_t*>(p.zero + at));
+                        } else {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const bool in = g0 + g < SG;
+                                v[g] = in ? load_raw(p.scale, at + g, p.stype) : 0u;
+                                if (p.zero && in)
+                                    zero[j] = (zero[j] & ~(0xFFu << (8 * g))) |
+                                              (static_cast<uint32_t>(__ldcg(p.zero + at + g))
+                                               << (8 * g));
+                            }
+                            raw[j] = ss == 4 ? make_uint4(v[0], v[1], v[2], v[3])
+                                             : make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, 0, 0);
+                        }
+                    }
+                    if (r0 == th) ok = wait(&s_empty[s], ((ch / C::SR) & 1) ^ 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t v[4] = {ss == 4 ? raw[j].x : raw[j].x & 0xFFFFu,
+                                               ss == 4 ? raw[j].y : raw[j].x >> 16,
+                                               ss == 4 ? raw[j].z : raw[j].y & 0xFFFFu,
+                                               ss == 4 ? raw[j].w : raw[j].y >> 16};
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int at = (s * 4 + g) * MANY_ROWS + r0 + j * n;
+                            sc_s[at] = typed(v[g], p.stype);
+                            sc_z[at] = static_cast<uint16_t>(Magic<H>::bias(zero[j] >> (8 * g)));
+                        }
+                    }
+                }
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(&s_full[s]);
+            }
+        }
+    };
 
     if (warp < 4) {
         regs_dec<C::REGS_AUX>();
-        if (warp == 0) {
+        if (warp < 2) {
             // -------------------------------------------------------- MMA
+            const int h = warp;
             const uint64_t d0 = umma::desc_sw128(smem_u32(base));
             const uint32_t b_hi = static_cast<uint32_t>(d0 >> 32), b_lo = static_cast<uint32_t>(d0);
             const uint32_t fmt = std::is_same<X, __half>::value ? 0u : 1u;
-            uint32_t it = 0, gi = 0, na[2] = {0, 0};  // na: uses of the A buffers
+            uint32_t xs = 0, xph = 0, db = 0, dph = 1, na0 = 0, na1 = 0, nx = 0;
             bool ok = true;
             for (int t = first; t < tiles && ok; t += step) {
                 const gmm::Tile c = tile_of(t);
+                const bool mine = live(c, h);
                 const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) |
                                        (static_cast<uint32_t>(c.np >> 3) << 17) |
                                        ((128u >> 4) << 24);
-                for (int k = 0; k < nkb && ok; ++k, ++it) {
-                    const uint32_t xs = it % C::XS, ab = k & 1;
-                    const uint32_t aph = (ab ? na[1] : na[0]) & 1;
-                    ok = wait(&x_full[xs], (it / C::XS) & 1);
+#pragma unroll 1
+                for (int k = 0; k < nkb; ++k) {
+                    const uint32_t ab = k & 1, aph = (ab ? na1 : na0) & 1;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && wait(&a_full[ab * 2 + h], aph);
-#pragma unroll
-                        for (int g = 0; g < C::GPB; ++g) {
-                            const uint32_t db = (gi + g) % C::DB;
-                            // (before any use of a buffer the wait passes at once)
-                            ok = ok && wait(&d_empty[db * 2 + h], (((gi + g) / C::DB) & 1) ^ 1);
-                            if (!ok) break;
-                            umma::fence_after_sync();
-                            if (elect_one()) {
-                                const uint32_t d = tmem + (db * 2 + h) * MANY_NT;
-                                const uint32_t a = tmem + C::TM_A + (ab * 2 + h) * 64;
-                                const uint32_t b = b_lo + ((xs * C::X_BYTES) >> 4);
-                                constexpr int KS = C::S / 16;
-                                if (live(c, h))
-#pragma unroll
-                                    for (int q = C::PARTS - 1; q >= 0; --q)
-#pragma unroll
-                                        for (int s = g * KS; s < (g + 1) * KS; ++s)
-                                            umma::mma_f16_ta(
-                                                d, a + s * 8,
-                                                b + (((2 * q + (s >> 2)) * C::X_TILE) >> 4) +
-                                                    2 * (s & 3),
-                                                b_hi, idesc,
-                                                (q < C::PARTS - 1 || s > g * KS) ? 1u : 0u);
-                                umma::commit(&d_full[db * 2 + h]);
-                                if (g == C::GPB - 1) {
-                                    umma::commit(&a_empty[ab * 2 + h]);
-                                    if (h == 1) umma::commit(&x_empty[xs]);
-                                }
+                    for (int g = 0; g < C::GPB; ++g) {
+                        // all waits tried before any is acted on (before any use of a
+                        // buffer the wait for it passes at once)
+                        bool r0 = true, r1 = true, r2 = mbar_try_wait(&d_empty[db * 2 + h], dph);
+                        if (g == 0) {
+                            r0 = mbar_try_wait(&x_full[xs], xph);
+                            r1 = mbar_try_wait(&a_full[ab * 2 + h], aph);
+                        }
+                        if (!__all_sync(0xffffffffu, r0 && r1 && r2)) {
+                            if (g == 0) {
+                                ok = wait(&x_full[xs], xph);
+                                ok = ok && wait(&a_full[ab * 2 + h], aph);
                             }
-                            __syncwarp();
+                            ok = ok && wait(&d_empty[db * 2 + h], dph);
+                            if (!ok) break;
+                        }
+                        umma::fence_after_sync();
+                        if (elect_one()) {
+                            const uint32_t d = tmem + (db * 2 + h) * MANY_NT;
+                            const uint32_t a = tmem + C::TM_A + (ab * 2 + h) * 64;
+                            const uint32_t b = b_lo + ((xs * C::X_BYTES) >> 4);
+                            constexpr int KS = C::S / 16;
+                            if (mine)
+#pragma unroll
+                                for (int q = C::PARTS - 1; q >= 0; --q)
+#pragma unroll
+                                    for (int s = g * KS; s < (g + 1) * KS; ++s)
+                                        umma::mma_f16_ta(
+                                            d, a + s * 8,
+                                            b + (((2 * q + (s >> 2)) * C::X_TILE) >> 4) +
+                                                2 * (s & 3),
+                                            b_hi, idesc,
+                                            (q < C::PARTS - 1 || s > g * KS) ? 1u : 0u);
+                            umma::commit(&d_full[db * 2 + h]);
+                            if (g == C::GPB - 1) {
+                                umma::commit(&a_empty[ab * 2 + h]);
+                                umma::commit(&x_empty[xs]);
+                            }
+                        }
+                        __syncwarp();
+                        if (++db == C::DB) {
+                            db = 0;
+                            dph ^= 1;
                         }
                     }
-                    gi += C::GPB;
-                    if (ab) ++na[1]; else ++na[0];
+                    if (!ok) break;
+                    ++nx;
+                    if (++xs == C::XS) {
+                        xs = 0;
+                        xph ^= 1;
+                    }
+                    if (ab) ++na1; else ++na0;
                 }
             }
             // Every arrival that the tensor core owes lands before the CTA ends (the
             // accumulators' are waited for by the warps that read them).
             if (ok) {
-                for (uint32_t i = it > C::XS ? it - C::XS : 0; i < it; ++i)
+                for (uint32_t i = nx > C::XS ? nx - C::XS : 0; i < nx; ++i)
                     wait(&x_empty[i % C::XS], (i / C::XS) & 1);
-#pragma unroll
-                for (int ab = 0; ab < 2; ++ab)
-                    if (na[ab] > 0) {
-                        wait(&a_empty[ab * 2], (na[ab] - 1) & 1);
-                        wait(&a_empty[ab * 2 + 1], (na[ab] - 1) & 1);
-                    }
+                if (na0 > 0) wait(&a_empty[h], (na0 - 1) & 1);
+                if (na1 > 0) wait(&a_empty[2 + h], (na1 - 1) & 1);
             }
-        } else if (warp == 1) {
+        } else if (warp == 2) {
             // -------------------------------------------------------- TMA
             uint32_t it = 0, wi = 0;
             bool ok = !skip;
@@ -279,81 +363,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 wait(&w_full[i % C::WS], (i / C::WS) & 1);
             for (uint32_t i = it > C::XS ? it - C::XS : 0; i < it; ++i)
                 wait(&x_full[i % C::XS], (i / C::XS) & 1);
-        } else {
-            // ----------------------------------------------------- scales
-            // chunks of four per row, four rows to a thread
-            const int th = tid - 64;
-            const int SG = p.K / C::S;
-            const int ss = p.stype == QMOE_F32 ? 4 : 2;
-            const bool vec = SG % 4 == 0 && (kbeg * C::GPB) % 4 == 0 &&
-                             reinterpret_cast<uintptr_t>(p.scale) % (4 * ss) == 0 &&
-                             reinterpret_cast<uintptr_t>(p.zero) % 4 == 0;
-            uint32_t ch = 0;
-            bool ok = true;
-            for (int t = first; t < tiles && ok; t += step) {
-                const gmm::Tile c = tile_of(t);
-                for (int k = 0; k < nkb && ok; k += C::CB, ++ch) {
-                    const int g0 = (kbeg + k) * C::GPB;
-                    uint4 raw[4];   // as they lie: four of 32 bits, or .x and .y two of 16 each
-                    uint32_t zero[4];
-                    const bool whole = vec && g0 + 4 <= SG;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int n = min(c.nbi * MANY_ROWS + 64 * j + th, p.N - 1);
-                        const int64_t at = (static_cast<int64_t>(c.e) * p.N + n) * SG + g0;
-                        zero[j] = 0x08080808u;
-                        if (whole) {
-                            if (ss == 4) {
-                                raw[j] = __ldcg(reinterpret_cast<const uint4*>(
-                                    static_cast<const float*>(p.scale) + at));
-                            } else {
-                                const uint2 q = __ldcg(reinterpret_cast<const uint2*>(
-                                    static_cast<const uint16_t*>(p.scale) + at));
-                                raw[j].x = q.x;
-                                raw[j].y = q.y;
-                            }
-                            if (p.zero)
-                                zero[j] = __ldcg(reinterpret_cast<const uint32_t*>(p.zero + at));
-                        } else {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const bool in = g0 + g < SG;
-                                v[g] = in ? load_raw(p.scale, at + g, p.stype) : 0u;
-                                if (p.zero && in)
-                                    zero[j] = (zero[j] & ~(0xFFu << (8 * g))) |
-                                              (static_cast<uint32_t>(__ldcg(p.zero + at + g))
-                                               << (8 * g));
-                            }
-                            raw[j] = ss == 4 ? make_uint4(v[0], v[1], v[2], v[3])
-                                             : make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, 0, 0);
-                        }
-                    }
-                    const uint32_t s = ch % C::SR;
-                    ok = wait(&s_empty[s], ((ch / C::SR) & 1) ^ 1);
-                    if (!ok) break;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t v[4] = {ss == 4 ? raw[j].x : raw[j].x & 0xFFFFu,
-                                               ss == 4 ? raw[j].y : raw[j].x >> 16,
-                                               ss == 4 ? raw[j].z : raw[j].y & 0xFFFFu,
-                                               ss == 4 ? raw[j].w : raw[j].y >> 16};
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int at = (s * 4 + g) * MANY_ROWS + 64 * j + th;
-                            sc_s[at] = typed(v[g], p.stype);
-                            sc_z[at] =
-                                static_cast<uint16_t>(Magic<H>::bias(zero[j] >> (8 * g)));
-                        }
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_full[s]);
-                }
-            }
+        } else if constexpr (!C::TMA_X) {
+            scales(lane, 32);
         }
+    } else if (C::TMA_X && warp < 8) {
+        regs_dec<C::REGS_AUX>();
+        scales(tid - 128, 128);
     } else if (!C::TMA_X && warp < 8) {
         // ----------------------------------------------------- token rows
-        regs_dec<C::REGS_X>();
+        regs_dec<C::REGS_AUX>();
         const int th = tid - 128;
         uint32_t it = 0;
         bool ok = true;
