@@ -20,6 +20,7 @@ namespace w4 {
 
 constexpr int MANY_ROWS = 256;
 constexpr int MANY_NT = 64;
+constexpr unsigned NAP_NS = 200;
 
 // TMA_X: token rows by TMA.
 template <class X_, int S_, bool TMA_X_>
@@ -102,6 +103,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     using X = typename C::X;
     using H = typename C::H;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_naps;  // of a wait that runs out
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* sc_s = reinterpret_cast<float*>(base + C::O_S);
@@ -134,6 +136,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int i = 0; i < C::SR; ++i) { mbar_init(&s_full[i], C::S_WARPS); mbar_init(&s_empty[i], 24); }
         for (int i = 0; i < 2 * C::AB; ++i) { mbar_init(&a_full[i], 4); mbar_init(&a_empty[i], 1); }
         for (int i = 0; i < 2 * C::DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 4); }
+        const unsigned long long naps = wait_limit(p.err) / NAP_NS + 1;
+        s_naps = naps < 0xFFFFFFFFu ? static_cast<uint32_t>(naps) : 0xFFFFFFFFu;
         fence_barrier_init();
         prefetch_tensormap(&tm_w);
         if constexpr (C::TMA_X) prefetch_tensormap(&tm_x);
@@ -162,9 +166,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // whether a tile's half has weight rows (one without goes through the same steps,
     // its MMAs and sums left out)
     auto live = [&](const gmm::Tile& c, int h) { return c.nbi * MANY_ROWS + 128 * h < p.N; };
-    // (a wait that runs out does so for the whole warp: what follows is warp-wide)
+    // Waits.  A try itself suspends the warp for a while, so a second one is rare; what
+    // follows the first is kept short, for there are many of these and the roles' loops
+    // share the instruction caches (with the pipelines' usual longer form 43 us for 64
+    // groups of 64 rows, 1024 x 2048, with this one 39).  The limit is counted in naps.  A
+    // wait that runs out does so for the whole warp: what follows is warp-wide.
     auto wait = [&](uint64_t* b, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_spin(b, parity, p.err, DEV_GMM_TIMEOUT)) != 0;
+        bool ok = mbar_try_wait(b, parity);
+        if (__all_sync(0xffffffffu, ok)) return true;
+#pragma unroll 1
+        for (uint32_t i = s_naps; i > 0 && !ok; --i) {
+            __nanosleep(NAP_NS);
+            ok = mbar_try_wait(b, parity);
+        }
+        if (!ok) record_error(p.err, DEV_GMM_TIMEOUT);
+        return __all_sync(0xffffffffu, ok) != 0;
     };
     // scales: chunks of four per row, for `n` threads
     auto scales = [&](int th, int n) {
@@ -441,12 +457,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if ((k & 1) == set) {
                     ok = wait(&w_full[ws], (wi / C::WS) & 1);
                     if (!ok) break;
-                    uint4 w[4];
                     const uint8_t* wr = base + C::O_W + ws * C::W_BYTES + row * 128;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        w[q] = *reinterpret_cast<const uint4*>(
-                            wr + (((set * 4 + q) ^ (row & 7)) << 4));
                     uint32_t bias[C::GPB];
 #pragma unroll
                     for (int g = 0; g < C::GPB; ++g)
@@ -456,14 +467,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (!ok) break;
                     umma::fence_after_sync();
                     if (mine)
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < 4; ++q) {
                             uint32_t r[16];
-                            const uint32_t b = bias[q * 32 / C::S];
-                            codes_in_order<H>(w[q].x, b, r);
-                            codes_in_order<H>(w[q].y, b, r + 4);
-                            codes_in_order<H>(w[q].z, b, r + 8);
-                            codes_in_order<H>(w[q].w, b, r + 12);
+                            uint32_t b = bias[0];
+#pragma unroll
+                            for (int g = 1; g < C::GPB; ++g)
+                                if (q * 32 / C::S == g) b = bias[g];
+                            const uint4 v = *reinterpret_cast<const uint4*>(
+                                wr + (((set * 4 + q) ^ (row & 7)) << 4));
+                            codes_in_order<H>(v.x, b, r);
+                            codes_in_order<H>(v.y, b, r + 4);
+                            codes_in_order<H>(v.z, b, r + 8);
+                            codes_in_order<H>(v.w, b, r + 12);
                             umma::st_32x32b_x16(a + 16 * q, r);
                         }
                     umma::wait_st();
@@ -563,9 +579,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (warp >= C::FIRST + 16 && first < tiles) {
             const gmm::Tile c = tile_of(first);
             const int row = tid - (C::FIRST + 16) * 32, n = c.nbi * MANY_ROWS + row;
-            for (int j = rank; j < c.nv; j += ranks) {
-                const float v = gmm::cluster_sum(part + j * MANY_ROWS + row, ranks);
-                if (n < p.N) store_y(p, c.row0 + j, n, v);
+            // (four columns at a time: the remote loads take longer than all else)
+            for (int j = rank; j < c.nv; j += 4 * ranks) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = gmm::cluster_sum(part + min(j + i * ranks, c.nv - 1) * MANY_ROWS + row,
+                                            ranks);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j + i * ranks < c.nv && n < p.N)
+                        store_y(p, c.row0 + j + i * ranks, n, v[i]);
             }
         }
         __syncwarp();

@@ -185,10 +185,126 @@ def test_w4_mm_grouped_bad_offsets_are_reported(qm, off):
     assert qm.device_status() == qm.OK and (y != 55.0).all()
 
 
+MANY = [  # tokens, rows, cols, scale_cols: sizes that the kernel for many rows takes
+    (40, 4096, 4096, 128), (64, 14336, 1024, 64), (65, 14000, 992, 32), (130, 5000, 1120, 32),
+    (200, 3000, 2240, 64), (333, 4097, 2176, 128), (600, 16385, 128, 128), (700, 8300, 96, 32),
+    (1500, 1030, 1024, 64), (5000, 300, 640, 128), (20000, 40, 1152, 128),
+]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("m,n,k,S", MANY)
+def test_w4_mm_many_rows(qm, kind, m, n, k, S):
+    """Full and ragged tiles of tokens and of weight rows, halves of a tile without rows,
+    K that ends inside a block, clusters that share K, scales in whole chunks and not."""
+    import torch
+    g = np.random.default_rng(m + n + k)
+    zeros = k % 64 != 0
+    q, s, z, wv = weights(qm, g, 1, n, k, S, "f16", zeros)
+    code, dt = kinds(qm)[kind]
+    x = torch.from_numpy(0.01 * g.standard_normal((m, k)).astype(np.float32)).to(dt).cuda()
+    y = torch.full((m, n), 55.0, device="cuda")
+    qm.w4_mm(q, qm.F16, s, z, S, n, k, code, x, m, qm.F32, y)
+    assert qm.device_status() == qm.OK
+    # (in 64 bits on the GPU: the products of the larger cases take a CPU minutes)
+    xd, wd = x.double(), torch.from_numpy(wv[0]).cuda()
+    want = xd @ wd.T
+    terms = 1.01 * 2 * (16 + S / 16) + k / S + 1 + 32
+    tol = terms * ref.U * (xd.abs() @ wd.abs().T) + ref.U * want.abs()
+    off = (y.double() - want).abs() - tol
+    assert float(off.max()) <= 0, f"{int((off > 0).sum())} of {off.numel()} outside"
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("ldx,ldy,offset", [(1032, 1300, 0), (1025, 1281, 1), (1024, 1280, 4),
+                                            (1040, 1290, 8)])
+def test_w4_mm_many_rows_strides(qm, kind, ldx, ldy, offset):
+    run_mm(qm, 500, 1280, 1024, 64, kind, okind="bf16", ldx=ldx, ldy=ldy, offset=offset)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("name,n,k,S", [("uneven", 520, 1024, 128), ("uneven", 768, 672, 32),
+                                        ("many groups", 256, 512, 64)])
+def test_w4_mm_grouped_many_rows(qm, kind, name, n, k, S):
+    """Uneven groups with rows before the first and behind the last, which are left as
+    they were, by the kernel for many rows."""
+    import torch
+    g = np.random.default_rng(n + k)
+    if name == "uneven":
+        sizes = [0, 150, 1, 64, 0, 65, 129, 7, 0, 300, 63, 2, 200, 0]
+    else:
+        sizes = list(g.integers(0, 70, 300))
+    e, head, tail = len(sizes), 3, 5
+    q, s, z, wv = weights(qm, g, e, n, k, S, "bf16", True)
+    off = np.cumsum([head] + sizes).astype(np.int32)
+    m = int(off[-1]) + tail
+    code, dt = kinds(qm)[kind]
+    x = torch.from_numpy(0.01 * g.standard_normal((m, k)).astype(np.float32)).to(dt).cuda()
+    y = torch.full((m, n), 55.0, dtype=dt, device="cuda")
+    qm.w4_mm_grouped(q, qm.BF16, s, z, S, e, n, k, code, x, m, dev(off), code, y)
+    assert qm.device_status() == qm.OK
+    assert (y[:head] == 55.0).all() and (y[int(off[-1]):] == 55.0).all()
+    xv, got = f64(x), f64(y)
+    for i in range(e):
+        r = slice(off[i], off[i + 1])
+        want, err = ref.w4_product(xv[r], wv[i], S)
+        check(got[r], want, ref.rounded(want, err, kind), f"group {i}")
+
+
+def test_many_rows_keep_nan_and_infinities_to_themselves(qm):
+    import torch
+    n, k, S, m = 2048, 1024, 128, 500
+    g = np.random.default_rng(8)
+    for kind in TYPES:
+        q, s, z, wv = weights(qm, g, 1, n, k, S, "f32", True)
+        s[0, 1000, 3] = float("nan")
+        x = torch.randn(m, k, device="cuda") * 0.01
+        x[77, 3], x[499, 100] = float("inf"), float("nan")
+        x = x.to(kinds(qm)[kind][1])
+        y = torch.zeros(m, n, device="cuda")
+        qm.w4_mm(q, qm.F32, s, z, S, n, k, kinds(qm)[kind][0], x, m, qm.F32, y)
+        assert qm.device_status() == qm.OK
+        got = y.cpu().numpy()
+        assert np.isnan(got[:, 1000]).all() and np.isnan(got[499]).all()
+        rest = np.delete(np.delete(got, [77, 499], 0), 1000, 1)
+        assert np.isfinite(rest).all()
+        w3, other = wv[0][:, 3], np.arange(n) != 1000
+        assert np.array_equal(np.isnan(got[77, other]), w3[other] == 0)
+        live = other & (w3 != 0)
+        assert np.array_equal(got[77, live], np.sign(w3[live]) * np.inf)
+
+
+@pytest.mark.parametrize("cta", [0, 3])
+@pytest.mark.parametrize("m,n,k", [(64, 4096, 4096), (600, 8000, 1024)], ids=["shared_k", "tiles"])
+def test_wait_that_runs_out_is_reported(qm, m, n, k, cta):
+    """One CTA of the kernel for many rows loads nothing and every device wait gives up
+    after 5 ms: the call returns, the status says so, and the next call is right."""
+    import torch
+    g = np.random.default_rng(71)
+    q, s, z, wv = weights(qm, g, 1, n, k, 128, "f16", True)
+    x = (0.01 * torch.randn(m, k, device="cuda")).to(torch.bfloat16)
+    y = torch.zeros(m, n, device="cuda")
+    args = (q, qm.F16, s, z, 128, n, k, qm.BF16, x, m, qm.F32)
+    torch.cuda.synchronize()
+    qm.set_fault_injection(5_000_000, cta)
+    try:
+        qm.w4_mm(*args, y)
+        assert qm.device_status() == qm.ERR_TIMEOUT
+        assert "wait" in qm.last_error()
+    finally:
+        qm.set_fault_injection(0, -1)
+    qm.w4_mm(*args, y)
+    assert qm.device_status() == qm.OK
+    pick = np.arange(0, n, 37)
+    want, err = ref.w4_product(f64(x), wv[0][pick], 128)
+    check(f64(y)[:, pick], want, ref.rounded(want, err, "f32"), "after the timeout")
+
+
 def test_same_inputs_same_bits(qm):
     import torch
     g = np.random.default_rng(1)
-    for m, n, k in ((1, 4096, 4096), (5, 1000, 2048), (200, 300, 512)):
+    for m, n, k in ((1, 4096, 4096), (5, 1000, 2048), (200, 300, 512), (64, 4096, 4096),
+                    (300, 9000, 1024)):
         q, s, z, _ = weights(qm, g, 1, n, k, 128, "f16", True)
         x = torch.randn(m, k, device="cuda").to(torch.bfloat16)
         ys = [torch.empty(m, n, device="cuda") for _ in range(4)]
