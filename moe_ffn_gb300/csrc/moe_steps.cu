@@ -108,7 +108,7 @@ static size_t permute_ws(int64_t n_tokens, int32_t num_experts, int32_t top_k) {
     if (n_tokens * top_k <= steps::P_ALONE) return 256;
     int run, runs;
     permute_runs(n_tokens, top_k, &run, &runs);
-    return (static_cast<size_t>(runs) * num_experts * 2 + 255) / 256 * 256;
+    return (static_cast<size_t>(runs) * ((num_experts + 7) / 8 * 8) * 2 + 255) / 256 * 256;
 }
 
 template <int VB>
@@ -297,12 +297,13 @@ qmoe_status moe_permute(int xtype, const void* x, int64_t n_tokens, int64_t cols
     p.pos = pos;
     p.P = static_cast<int>(n_tokens * top_k);
     p.E = num_experts;
+    p.Ep = (num_experts + 7) / 8 * 8;
     p.k = top_k;
     if (p.P > steps::P_ALONE) {
         permute_runs(n_tokens, top_k, &p.run, &p.runs);
         p.counts = static_cast<uint16_t*>(ws);
         const cudaError_t e = launch_pdl(steps::count_kernel, dim3(p.runs), dim3(steps::P_THREADS),
-                                         static_cast<size_t>(p.E) * 4, st, p);
+                                         static_cast<size_t>(p.Ep) * 4, st, p);
         if (e != cudaSuccess) return cuda_fail(e, "count launch");
     } else {
         p.run = static_cast<int>(std::max<int64_t>(1, (n_tokens + 2 * d->sms - 1) / (2 * d->sms)));
@@ -318,7 +319,7 @@ qmoe_status moe_permute(int xtype, const void* x, int64_t n_tokens, int64_t cols
     const int share = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(d->sms / p.runs, (segs + steps::P_WARPS - 1) / steps::P_WARPS)));
     const dim3 grid(p.runs, share);
-    const size_t smem = static_cast<size_t>(steps::P_WARPS + 2) * p.E * 4;
+    const size_t smem = static_cast<size_t>(steps::P_WARPS + 2) * p.Ep * 4;
     const cudaError_t e = units(16)  ? launch_permute<16>(p, row_bytes, grid, smem, st)
                           : units(4) ? launch_permute<4>(p, row_bytes, grid, smem, st)
                                      : launch_permute<2>(p, row_bytes, grid, smem, st);

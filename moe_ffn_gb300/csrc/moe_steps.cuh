@@ -17,9 +17,13 @@ constexpr int MAX_EXPERTS = 1024;
 constexpr int MAX_TOPK = 16;  // a token's slots lie in the lanes of one warp
 
 // ------------------------------------------------------------------ routing
-// A warp per token; lane i holds the logits i V .. i V + V - 1 as ranking keys
-// (route.cuh), so the lowest lane with the largest key also has the lowest index
-// among equals.  Each of the k rounds takes the largest key left.
+// A warp per token; lane i holds the logits i V .. i V + V - 1.  Each lane sorts its own
+// once, best first, and each of the k rounds takes the best of the lanes' heads, so that a
+// round costs one warp maximum and a shift of one lane's list.  16-bit logits rank by one
+// 32-bit word, the ranking key of route.cuh's rule above the inverted index, whose
+// maximum is the winner, index and all; f32 logits need the key's 32 bits for themselves,
+// and the lowest lane with the largest key then has the lowest index among equals.
+// Bound by instruction issue: MEASURED_ROUTE.
 constexpr int R_WARPS = 4;
 
 struct RouteParams {
@@ -76,16 +80,116 @@ __device__ __forceinline__ void load_run(const T* row, int c, int E, bool vec, f
     for (int i = 0; i < V; ++i) v[i] = c + i < E ? to_f32(ldcg_value(row + c + i)) : fill;
 }
 
-// The softmax's largest logit and the sum of exponentials around it, over a warp.
-template <int V>
-__device__ __forceinline__ float warp_expsum(const float (&v)[V], int c, int E, float top) {
-    float z = 0.f;
+// A sorting network (odd-even merge) over V items held in registers, larger first.
+template <int V, class Swap>
+__device__ __forceinline__ void sort_network(Swap swap) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (c + i < E) z += expf(v[i] - top);
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p))
+                        swap(i + j, i + j + k);
+}
+
+// Ranking key of a 16-bit logit's bits by route.cuh's rule, as 16 bits, and the value of
+// a key.
+template <class T>
+__device__ __forceinline__ uint32_t key16(uint32_t b) {
+    constexpr uint32_t inf = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    if ((b & 0x7FFFu) > inf) return 0xFFFFu;   // NaN
+    if ((b & 0x7FFFu) == 0u) b = 0u;           // -0 ranks as +0
+    return (b & 0x8000u) ? ~b & 0xFFFFu : b | 0x8000u;
+}
+template <class T>
+__device__ __forceinline__ float key16_value(uint32_t k) {
+    const unsigned short b =
+        static_cast<unsigned short>((k & 0x8000u) ? k & 0x7FFFu : ~k & 0xFFFFu);
+    return to_f32(*reinterpret_cast<const T*>(&b));
+}
+
+__device__ __forceinline__ float warp_sum(float z) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     return z;
+}
+
+// The k best of a warp's logits: lane s gets the s-th's index and value; all lanes the
+// best value.
+template <class T, int V>
+__device__ __forceinline__ float take_best(const float (&v)[V], int c, int E, int k, int lane,
+                                           int* idx, float* value) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t w[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const T raw = from_f32<T>(v[i]);  // (exact: it came from there)
+            const uint32_t b = *reinterpret_cast<const unsigned short*>(&raw);
+            w[i] = c + i < E ? key16<T>(b) << 16 | (0xFFFFu - (c + i)) : 0u;
+        }
+        sort_network<V>([&](int i, int j) {
+            const uint32_t hi = max(w[i], w[j]), lo = min(w[i], w[j]);
+            w[i] = hi;
+            w[j] = lo;
+        });
+        uint32_t mine = 0, top = 0;
+        for (int s = 0; s < k; ++s) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, w[0]);
+            if (s == 0) top = m;
+            if (lane == s) mine = m;
+            const bool won = w[0] == m;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t next = i + 1 < V ? w[i + 1] : 0u;
+                w[i] = won ? next : w[i];
+            }
+        }
+        *idx = static_cast<int>(0xFFFFu - (mine & 0xFFFFu));
+        *value = key16_value<T>(mine >> 16);
+        return key16_value<T>(top >> 16);
+    } else {
+        uint32_t key[V];  // 0: none left (no key is 0)
+        int at[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            key[i] = c + i < E ? route_key(v[i]) : 0u;
+            at[i] = c + i;
+        }
+        sort_network<V>([&](int i, int j) {
+            const bool ok = key[i] > key[j] || (key[i] == key[j] && at[i] < at[j]);
+            const uint32_t hi = ok ? key[i] : key[j], lo = ok ? key[j] : key[i];
+            const int first = ok ? at[i] : at[j], second = ok ? at[j] : at[i];
+            key[i] = hi;
+            key[j] = lo;
+            at[i] = first;
+            at[j] = second;
+        });
+        uint32_t mine = 0, top = 0;
+        int index = 0;
+        for (int s = 0; s < k; ++s) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, key[0]);
+            const int who = __ffs(__ballot_sync(0xffffffffu, key[0] == m)) - 1;
+            const int e = __shfl_sync(0xffffffffu, at[0], who);
+            if (s == 0) top = m;
+            if (lane == s) {
+                mine = m;
+                index = e;
+            }
+            const bool won = lane == who;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t next = i + 1 < V ? key[i + 1] : 0u;
+                key[i] = won ? next : key[i];
+                if (i + 1 < V) at[i] = won ? at[i + 1] : at[i];
+            }
+        }
+        *idx = index;
+        *value = route_key_value(mine);
+        return route_key_value(top);
+    }
 }
 
 template <class T, int V>
@@ -98,51 +202,26 @@ __global__ void __launch_bounds__(R_WARPS * 32) route_kernel(const RouteParams p
     const int c = lane * V;
     float v[V];
     load_run<T, V>(static_cast<const T*>(p.logits) + t * p.ldl, c, p.E, p.vec, 0.f, v);
-    uint32_t key[V];
-    uint32_t best = 0;  // 0: none left (no key is 0)
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        key[i] = c + i < p.E ? route_key(v[i]) : 0u;
-        if (key[i] > best) { best = key[i]; at = i; }
-    }
-    uint32_t my_key = 0;
-    int my_idx = 0;
-    uint32_t top_key = 0;
-    for (int s = 0; s < p.k; ++s) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-        const int who = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
-        const int e = __shfl_sync(0xffffffffu, c + at, who);
-        if (s == 0) top_key = m;
-        if (lane == s) { my_key = m; my_idx = e; }
-        if (lane == who) {
-            best = 0;
-            const int gone = at;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (i == gone) key[i] = 0u;
-                if (key[i] > best) { best = key[i]; at = i; }
-            }
-        }
-    }
-    const float top = route_key_value(top_key);
+    int idx;
+    float value;
+    const float top = take_best<T, V>(v, c, p.E, p.k, lane, &idx, &value);
     float w;
     if (route_degenerate(top)) {
-        my_idx = lane;
+        idx = lane;
         w = __int_as_float(0x7FC00000);
     } else {
-        const float x = lane < p.k ? expf(route_key_value(my_key) - top) : 0.f;
+        const float x = lane < p.k ? expf(value - top) : 0.f;
         float z = x;
-        if (p.renorm) {
+        if (!p.renorm) {
+            z = 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        } else {
-            z = warp_expsum<V>(v, c, p.E, top);
+            for (int i = 0; i < V; ++i)
+                if (c + i < p.E) z += expf(v[i] - top);
         }
-        w = x / z;
+        w = x / warp_sum(z);
     }
     if (lane < p.k) {
-        p.idx[t * p.k + lane] = my_idx;
+        p.idx[t * p.k + lane] = idx;
         p.w[t * p.k + lane] = w;
     }
 }
@@ -152,48 +231,61 @@ __global__ void __launch_bounds__(R_WARPS * 32) route_kernel(const RouteParams p
 //   renormalised      dl_e = sum over slots s of e: w_s (dw_s - c)
 //   not renormalised  dl_e = p_e ((sum over slots s of e: dw_s) - c), p the softmax
 //                     over all experts, formed again from the logits
+// The slots' terms are scattered through shared memory; where two slots of a token name
+// one expert, which moe_route never does, they are added in slot order.
 template <class T, int V>
 __global__ void __launch_bounds__(R_WARPS * 32) route_backward_kernel(const RouteParams p) {
+    __shared__ float s_row[R_WARPS][32 * V];
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * R_WARPS + (threadIdx.x >> 5);
     pdl_wait();
     pdl_trigger();
     if (t >= p.n_tokens) return;
     const int c = lane * V;
+    float* row = s_row[threadIdx.x >> 5];
     int idx = lane < p.k ? __ldcg(p.idx + t * p.k + lane) : -1;
     const bool live = idx >= 0 && idx < p.E;
-    if (!live) idx = -1;
+    if (!live) idx = -1 - lane;  // (distinct)
     const float w = live ? __ldcg(p.w + t * p.k + lane) : 0.f;
     const float d = live ? __ldcg(p.grad_w + t * p.k + lane) : 0.f;
     float v[V], g[V];
     if (!p.renorm)
         load_run<T, V>(static_cast<const T*>(p.logits) + t * p.ldl, c, p.E, p.vec,
                        -__int_as_float(0x7F800000), v);
-    float dot = w * d;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    for (int i = 0; i < V; ++i) row[c + i] = 0.f;
+    const float dot = warp_sum(w * d);
     const float mine = p.renorm ? w * (d - dot) : d;
-#pragma unroll
-    for (int i = 0; i < V; ++i) g[i] = 0.f;
-    for (int s = 0; s < p.k; ++s) {
-        const int e = __shfl_sync(0xffffffffu, idx, s);
-        const float m = __shfl_sync(0xffffffffu, mine, s);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e == c + i) g[i] += m;
+    const unsigned same = __match_any_sync(0xffffffffu, idx);
+    __syncwarp();
+    if (!__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {
+        if (live) row[idx] = mine;
+    } else {
+        for (int s = 0; s < p.k; ++s) {
+            if (lane == s && live) row[idx] += mine;
+            __syncwarp();
+        }
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = row[c + i];
     if (!p.renorm) {
         uint32_t best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) best = max(best, c + i < p.E ? route_key(v[i]) : 0u);
         const float top = route_key_value(__reduce_max_sync(0xffffffffu, best));
-        const float inv = 1.f / warp_expsum<V>(v, c, p.E, top);
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[i] = c + i < p.E ? expf(v[i] - top) : 0.f;
+            z += v[i];
+        }
+        const float inv = 1.f / warp_sum(z);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            g[i] = route_degenerate(top) ? __int_as_float(0x7FC00000)
-                                         : expf(v[i] - top) * inv * (g[i] - dot);
+            g[i] = route_degenerate(top) ? __int_as_float(0x7FC00000) : v[i] * inv * (g[i] - dot);
     }
-    T* row = static_cast<T*>(p.grad) + t * p.ldg + c;
+    T* out = static_cast<T*>(p.grad) + t * p.ldg + c;
     constexpr int BYTES = V * static_cast<int>(sizeof(T));
     if constexpr (BYTES >= 4) {
         if (p.vec_g) {
@@ -207,19 +299,19 @@ __global__ void __launch_bounds__(R_WARPS * 32) route_backward_kernel(const Rout
             if constexpr (BYTES >= 16) {
 #pragma unroll
                 for (int i = 0; i < BYTES / 16; ++i)
-                    reinterpret_cast<uint4*>(row)[i] =
+                    reinterpret_cast<uint4*>(out)[i] =
                         make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
             } else if constexpr (BYTES == 8) {
-                *reinterpret_cast<uint2*>(row) = make_uint2(q[0], q[1]);
+                *reinterpret_cast<uint2*>(out) = make_uint2(q[0], q[1]);
             } else {
-                *reinterpret_cast<uint32_t*>(row) = q[0];
+                *reinterpret_cast<uint32_t*>(out) = q[0];
             }
             return;
         }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        if (c + i < p.E) row[i] = from_f32<T>(g[i]);
+        if (c + i < p.E) out[i] = from_f32<T>(g[i]);
 }
 
 // ------------------------------------------------------------------ permute
@@ -230,11 +322,16 @@ __global__ void __launch_bounds__(R_WARPS * 32) route_backward_kernel(const Rout
 // experts, plus the pairs of its expert in earlier runs, plus those before it in
 // its own run.  The first two come from all the indices, counted by every CTA
 // for itself, while they are few (up to P_ALONE pairs: one launch), else from a
-// table of counts [runs][E] that count_kernel makes.
+// table of counts [runs][Ep] that count_kernel makes, eight experts to a load.
+// The rows to copy do not depend on any of it: they are on their way to registers
+// (four segments of a row per warp) while their places are found.
+// Bound by writing the rows: MEASURED_PERMUTE.
 constexpr int P_THREADS = 256;
 constexpr int P_WARPS = P_THREADS / 32;
 constexpr int P_ALONE = 8192;
 constexpr int P_POS = 1024;   // positions of a run kept in shared memory
+constexpr int P_AHEAD = 4;    // units of a lane in a segment of a row
+constexpr int P_EARLY = 4;    // segments loaded before their places are known
 
 struct PermuteParams {
     const uint8_t* x;
@@ -246,9 +343,10 @@ struct PermuteParams {
     int32_t* offsets;
     int32_t* pos;
     int P, E, k;
+    int Ep;                 // experts, rounded up to eight
     int run;                // tokens of a run
     int runs;
-    uint16_t* counts;       // [runs][E], or null
+    uint16_t* counts;       // [runs][Ep], or null
 };
 
 // The expert of pair i, or -1.
@@ -260,7 +358,7 @@ __device__ __forceinline__ int expert_of(const int32_t* idx, int i, int E) {
 __global__ void __launch_bounds__(P_THREADS) count_kernel(const PermuteParams p) {
     extern __shared__ int hist[];
     const int tid = threadIdx.x;
-    for (int e = tid; e < p.E; e += P_THREADS) hist[e] = 0;
+    for (int e = tid; e < p.Ep; e += P_THREADS) hist[e] = 0;
     pdl_wait();
     pdl_trigger();
     __syncthreads();
@@ -270,8 +368,8 @@ __global__ void __launch_bounds__(P_THREADS) count_kernel(const PermuteParams p)
         if (e >= 0) atomicAdd(&hist[e], 1);
     }
     __syncthreads();
-    uint16_t* out = p.counts + static_cast<int64_t>(blockIdx.x) * p.E;
-    for (int e = tid; e < p.E; e += P_THREADS) out[e] = static_cast<uint16_t>(hist[e]);
+    uint16_t* out = p.counts + static_cast<int64_t>(blockIdx.x) * p.Ep;
+    for (int e = tid; e < p.Ep; e += P_THREADS) out[e] = static_cast<uint16_t>(hist[e]);
 }
 
 template <int VB>
@@ -286,40 +384,87 @@ __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams 
     extern __shared__ int sm[];
     __shared__ int s_pos[P_POS];
     __shared__ int s_wsum[P_WARPS];
-    int* whist = sm;                    // [P_WARPS][E] this run's counts, then next rows
-    int* total = sm + P_WARPS * p.E;    // [E]
-    int* before = total + p.E;          // [E]
+    int* whist = sm;                    // [P_WARPS][Ep] this run's counts, then next rows
+    int* total = sm + P_WARPS * p.Ep;   // [Ep]
+    int* before = total + p.Ep;         // [Ep]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = blockIdx.x;
-    for (int i = tid; i < (P_WARPS + 2) * p.E; i += P_THREADS) sm[i] = 0;
+    for (int i = tid; i < (P_WARPS + 2) * p.Ep; i += P_THREADS) sm[i] = 0;
     pdl_wait();
     pdl_trigger();
-    __syncthreads();
     const int beg = r * p.run * p.k, end = min(beg + p.run * p.k, p.P);
+    // (token, segment) items, spread over the warps of all CTAs of this run
+    const int ntok = (end - beg) / p.k;
+    const int nseg = (p.nvec + 32 * P_AHEAD - 1) / (32 * P_AHEAD);
+    const int64_t items = static_cast<int64_t>(ntok) * nseg;
+    const int64_t it0 = blockIdx.y * P_WARPS + warp, it_step = gridDim.y * P_WARPS;
+    auto load = [&](int64_t it, U (&u)[P_AHEAD]) {
+        if (it >= items) return;
+        const int tok = static_cast<int>(it / nseg);
+        const int v0 = static_cast<int>(it - static_cast<int64_t>(tok) * nseg) * 32 * P_AHEAD + lane;
+        const U* src = reinterpret_cast<const U*>(p.x + (static_cast<int64_t>(r) * p.run + tok) *
+                                                            p.ldx);
+#pragma unroll
+        for (int a = 0; a < P_AHEAD; ++a)
+            if (v0 + 32 * a < p.nvec) u[a] = __ldcg(src + v0 + 32 * a);
+    };
+    auto store = [&](int64_t it, const U (&u)[P_AHEAD]) {
+        if (it >= items) return;
+        const int tok = static_cast<int>(it / nseg);
+        const int v0 = static_cast<int>(it - static_cast<int64_t>(tok) * nseg) * 32 * P_AHEAD + lane;
+        for (int s = 0; s < p.k; ++s) {
+            const int i = tok * p.k + s;
+            const int row = i < P_POS ? s_pos[i] : __ldcg(p.pos + beg + i);
+            if (row < 0) continue;
+            U* dst = reinterpret_cast<U*>(p.rows + static_cast<int64_t>(row) * p.ldr);
+#pragma unroll
+            for (int a = 0; a < P_AHEAD; ++a)
+                if (v0 + 32 * a < p.nvec) dst[v0 + 32 * a] = u[a];
+        }
+    };
+    U early[P_EARLY][P_AHEAD];
+#pragma unroll
+    for (int i = 0; i < P_EARLY; ++i) load(it0 + i * it_step, early[i]);
+    __syncthreads();
     if (p.counts) {
-        for (int e = tid; e < p.E; e += P_THREADS) {
-            int all = 0, ahead = 0;
-            for (int j = 0; j < p.runs; ++j) {
-                const int c = __ldcg(p.counts + static_cast<int64_t>(j) * p.E + e);
-                all += c;
-                if (j < r) ahead += c;
+        // eight experts to a thread, the runs spread over the groups of threads that
+        // cover them all
+        const int per = p.Ep / 8, groups = P_THREADS / per;
+        const int group = tid / per, e0 = (tid - group * per) * 8;
+        if (group < groups) {
+            int all[8], ahead[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) all[i] = ahead[i] = 0;
+#pragma unroll 8
+            for (int j = group; j < p.runs; j += groups) {
+                const uint4 q = __ldcg(reinterpret_cast<const uint4*>(
+                    p.counts + static_cast<int64_t>(j) * p.Ep + e0));
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int n = static_cast<int>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+                    all[i] += n;
+                    ahead[i] += j < r ? n : 0;
+                }
             }
-            total[e] = all;
-            before[e] = ahead;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (all[i]) atomicAdd(&total[e0 + i], all[i]);
+                if (ahead[i]) atomicAdd(&before[e0 + i], ahead[i]);
+            }
         }
     } else {
+        // (both counts in one word: there are at most 8192 pairs)
+#pragma unroll 8
         for (int i = tid; i < p.P; i += P_THREADS) {
             const int e = expert_of(p.idx, i, p.E);
-            if (e >= 0) {
-                atomicAdd(&total[e], 1);
-                if (i < beg) atomicAdd(&before[e], 1);
-            }
+            if (e >= 0) atomicAdd(&total[e], i < beg ? 0x10001 : 0x10000);
         }
     }
     // this run's pairs, a part to each warp
     const int part = ((end - beg + P_WARPS - 1) / P_WARPS + 31) & ~31;
     const int wbeg = min(beg + warp * part, end), wend = min(wbeg + part, end);
-    int* h = whist + warp * p.E;
+    int* h = whist + warp * p.Ep;
     for (int i = wbeg; i < wend; i += 32) {
         const int e = i + lane < wend ? expert_of(p.idx, i + lane, p.E) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, e);
@@ -330,8 +475,9 @@ __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams 
     // exclusive sum over the experts, a run of experts to each thread
     const int per = (p.E + P_THREADS - 1) / P_THREADS;
     const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
+    auto total_of = [&](int e) { return p.counts ? total[e] : total[e] >> 16; };
     int mine = 0;
-    for (int e = e0; e < e1; ++e) mine += total[e];
+    for (int e = e0; e < e1; ++e) mine += total_of(e);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -345,12 +491,13 @@ __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams 
     const bool tell = r == 0 && blockIdx.y == 0;
     for (int e = e0; e < e1; ++e) {
         if (tell) p.offsets[e] = first;
-        int at = first + before[e];
-        first += total[e];
+        int at = first + (p.counts ? before[e] : total[e] & 0xFFFF);
+        first += total_of(e);
+#pragma unroll
         for (int w = 0; w < P_WARPS; ++w) {
-            const int c = whist[w * p.E + e];
-            whist[w * p.E + e] = at;
-            at += c;
+            const int n = whist[w * p.Ep + e];
+            whist[w * p.Ep + e] = at;
+            at += n;
         }
         if (tell && e == p.E - 1) p.offsets[p.E] = first;
     }
@@ -369,28 +516,12 @@ __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams 
         }
     }
     __syncthreads();
-    constexpr int AHEAD = 4;
-    const int ntok = (end - beg) / p.k;
-    const int nseg = (p.nvec + 32 * AHEAD - 1) / (32 * AHEAD);
-    const int64_t items = static_cast<int64_t>(ntok) * nseg;
-    for (int64_t it = blockIdx.y * P_WARPS + warp; it < items; it += gridDim.y * P_WARPS) {
-        const int tok = static_cast<int>(it / nseg);
-        const int v0 = static_cast<int>(it - static_cast<int64_t>(tok) * nseg) * 32 * AHEAD + lane;
-        const int64_t t = static_cast<int64_t>(r) * p.run + tok;
-        const U* src = reinterpret_cast<const U*>(p.x + t * p.ldx);
-        U u[AHEAD];
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a)
-            if (v0 + 32 * a < p.nvec) u[a] = __ldcg(src + v0 + 32 * a);
-        for (int s = 0; s < p.k; ++s) {
-            const int i = tok * p.k + s;
-            const int row = i < P_POS ? s_pos[i] : __ldcg(p.pos + beg + i);
-            if (row < 0) continue;
-            U* dst = reinterpret_cast<U*>(p.rows + static_cast<int64_t>(row) * p.ldr);
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a)
-                if (v0 + 32 * a < p.nvec) dst[v0 + 32 * a] = u[a];
-        }
+    for (int i = 0; i < P_EARLY; ++i) store(it0 + i * it_step, early[i]);
+    for (int64_t it = it0 + P_EARLY * it_step; it < items; it += it_step) {
+        U u[P_AHEAD];
+        load(it, u);
+        store(it, u);
     }
 }
 
