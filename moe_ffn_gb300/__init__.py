@@ -11,8 +11,10 @@ Function names follow the C ABI declared in ``include/qmoe.h``.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import subprocess
+import sysconfig
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
 LIB_PATH = os.path.join(_HERE, "libqmoe.so")
 HEADER = os.path.join(_ROOT, "include", "qmoe.h")
+CALLS_PATH = os.path.join(_HERE, "_calls.so")  # csrc/calls.c, the short way into the library
 
 # qmoe_qtype
 F32, Q8_0, Q4_0, Q4_K, Q5_K, Q6_K = 0, 1, 2, 3, 4, 5
@@ -48,14 +51,14 @@ class QmoeError(RuntimeError):
 
 def _sources():
     return sorted(os.path.join(_CSRC, f) for f in os.listdir(_CSRC)
-                  if f.endswith((".cu", ".cuh")))
+                  if f.endswith((".cu", ".cuh", ".c")))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile libqmoe.so in-tree for sm_103a with nvcc."""
     srcs = _sources() + [HEADER]
-    if (not force and os.path.exists(LIB_PATH)
-            and os.path.getmtime(LIB_PATH) >= max(os.path.getmtime(s) for s in srcs)):
+    built = min((os.path.getmtime(f) if os.path.exists(f) else 0) for f in (LIB_PATH, CALLS_PATH))
+    if not force and built >= max(os.path.getmtime(s) for s in srcs):
         return LIB_PATH
     nvcc = os.environ.get("NVCC", "nvcc")
     if not os.path.exists(nvcc) and os.path.exists("/usr/local/cuda/bin/nvcc"):
@@ -68,8 +71,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd))
         procs.append(subprocess.Popen(cmd))
+    calls = CALLS_PATH + tag
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC",
+           "-I" + sysconfig.get_paths()["include"], "-o", calls, os.path.join(_CSRC, "calls.c")]
+    if verbose:
+        print(" ".join(cmd))
+    procs.append(subprocess.Popen(cmd))
     codes = [p.wait() for p in procs]
     try:
+        if codes[-1]:
+            raise subprocess.CalledProcessError(codes[-1], "calls.c")
+        os.replace(calls, CALLS_PATH)
         for u, c in zip(UNITS, codes):
             if c:
                 raise subprocess.CalledProcessError(c, f"nvcc {u}")
@@ -429,10 +441,47 @@ def moe_experts_f8(gate_stack, gate_scale, up_stack, up_scale, down_stack, down_
 
 
 # ------------------- steps around the experts' products (include/qmoe.h)
+# These calls first go the short way of csrc/calls.c, which answers None for whatever it
+# leaves to the checks below.
+_calls = None
+
+
+def _bind_calls():
+    """The module of csrc/calls.c, bound to the library; raises if it has not been built."""
+    global _calls
+    import torch
+    h = lib()
+    with _lock:
+        if _calls is None:
+            if not os.path.exists(CALLS_PATH):
+                raise QmoeError(ERR_CUDA, f"{CALLS_PATH} is missing: run moe_ffn_gb300.build()")
+            spec = importlib.util.spec_from_file_location("moe_ffn_gb300._calls", CALLS_PATH)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.bind(tuple(ctypes.cast(getattr(h, f), _P).value for f in (
+                "moe_route", "moe_route_backward", "moe_permute", "moe_combine",
+                "moe_combine_backward", "w4_mm", "w4_mm_grouped")),
+                (torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.uint8),
+                torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+            _calls = m
+    return _calls
+
+
+def _answered(status) -> bool:
+    """Whether the short way took the call; raises for a status other than OK."""
+    if status:
+        raise QmoeError(status, last_error())
+    return status is not None
+
+
 def moe_route(ltype: int, logits, n_tokens: int, num_experts: int, top_k: int, topk_idx, topk_w,
               renormalize: bool = True, ldl=None, stream=None) -> None:
     """topk_idx, topk_w = the top-k experts of each token's logits and their softmax
     weights (see include/qmoe.h)."""
+    if ldl is None and _answered((_calls or _bind_calls()).route(
+            ltype, logits, n_tokens, num_experts, top_k, topk_idx, topk_w,
+            0 if renormalize else ROUTE_NO_RENORM, stream)):
+        return
     fn, ldl = "moe_route", num_experts if ldl is None else ldl
     dev, st = _context(stream)
     P = n_tokens * top_k
@@ -446,6 +495,10 @@ def moe_route_backward(ltype: int, logits, n_tokens: int, num_experts: int, top_
                        topk_w, grad_w, grad_logits, renormalize: bool = True, ldl=None, ldg=None,
                        stream=None) -> None:
     """grad_logits from the gradient of moe_route's weights (see include/qmoe.h)."""
+    if ldl is None and ldg is None and _answered((_calls or _bind_calls()).route_backward(
+            ltype, logits, n_tokens, num_experts, top_k, topk_idx, topk_w, grad_w, grad_logits,
+            0 if renormalize else ROUTE_NO_RENORM, stream)):
+        return
     fn = "moe_route_backward"
     ldl, ldg = num_experts if ldl is None else ldl, num_experts if ldg is None else ldg
     dev, st = _context(stream)
@@ -469,6 +522,9 @@ def moe_permute_workspace_size(n_tokens: int, num_experts: int, top_k: int) -> i
 def moe_permute(xtype: int, x, n_tokens: int, cols: int, topk_idx, num_experts: int, top_k: int,
                 rows, offsets, pos, ws, ldx=None, ldr=None, ws_bytes=None, stream=None) -> None:
     """rows[pos[t][s]] = x[t], the rows sorted by expert (see include/qmoe.h)."""
+    if ldx is None and ldr is None and ws_bytes is None and _answered((_calls or _bind_calls()).permute(
+            xtype, x, n_tokens, cols, topk_idx, num_experts, top_k, rows, offsets, pos, ws, stream)):
+        return
     fn = "moe_permute"
     ldx, ldr = cols if ldx is None else ldx, cols if ldr is None else ldr
     ws_need = 0
@@ -489,6 +545,9 @@ def moe_permute(xtype: int, x, n_tokens: int, cols: int, topk_idx, num_experts: 
 def moe_combine(ytype: int, y, n_rows: int, cols: int, pos, topk_w, n_tokens: int, top_k: int,
                 otype: int, residual, out, ldy=None, ldo=None, stream=None) -> None:
     """out[t] = residual[t] + sum_s topk_w[t][s] y[pos[t][s]] (see include/qmoe.h)."""
+    if ldy is None and ldo is None and _answered((_calls or _bind_calls()).combine(
+            ytype, y, n_rows, cols, pos, topk_w, n_tokens, top_k, otype, residual, out, stream)):
+        return
     fn = "moe_combine"
     ldy, ldo = cols if ldy is None else ldy, cols if ldo is None else ldo
     dev, st = _context(stream)
@@ -504,6 +563,10 @@ def moe_combine_backward(ytype: int, y, n_rows: int, cols: int, pos, topk_w, n_t
                          top_k: int, otype: int, grad_out, grad_y, grad_w, ldy=None, ldo=None,
                          ldg=None, stream=None) -> None:
     """grad_y and grad_w (either may be None) of moe_combine (see include/qmoe.h)."""
+    if ldy is None and ldo is None and ldg is None and _answered((_calls or _bind_calls()).combine_backward(
+            ytype, y, n_rows, cols, pos, topk_w, n_tokens, top_k, otype, grad_out, grad_y, grad_w,
+            stream)):
+        return
     fn = "moe_combine_backward"
     ldy, ldo = cols if ldy is None else ldy, cols if ldo is None else ldo
     ldg = cols if ldg is None else ldg
@@ -523,6 +586,10 @@ def w4_mm(W, stype: int, scale, zero, scale_cols: int, rows: int, cols: int, xty
           n_tokens: int, ytype: int, y, ldx=None, ldy=None, stream=None) -> None:
     """y = x W^T with 4-bit weights, a scale and zero point per scale_cols columns (see
     include/qmoe.h)."""
+    if ldx is None and ldy is None and _answered((_calls or _bind_calls()).w4(
+            W, stype, scale, zero, scale_cols, -1, rows, cols, xtype, x, n_tokens, None, ytype, y,
+            stream)):
+        return
     fn = "w4_mm"
     ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
     dev, st = _context(stream)
@@ -540,6 +607,10 @@ def w4_mm_grouped(W, stype: int, scale, zero, scale_cols: int, num_groups: int, 
                   ldy=None, stream=None) -> None:
     """y[r] = W_g x[r] for the rows of every group, with 4-bit weights (see
     include/qmoe.h)."""
+    if ldx is None and ldy is None and _answered((_calls or _bind_calls()).w4(
+            W, stype, scale, zero, scale_cols, num_groups, rows, cols, xtype, x, n_rows, offsets,
+            ytype, y, stream)):
+        return
     fn = "w4_mm_grouped"
     ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
     dev, st = _context(stream)

@@ -363,12 +363,12 @@ qmoe_status moe_combine_backward(int ytype, const void* y, int64_t n_rows, int64
                                  void* stream) {
     clear_error();
     const char* fn = "moe_combine_backward";
+    if (!grad_y && !grad_w)
+        return fail(QMOE_ERR_INVALID_ARGUMENT, "%s: grad_y and grad_w are both null", fn);
     // (without grad_w the rows are not read and y may be null)
     if (qmoe_status s = combine_check(fn, ytype, grad_w ? y : grad_y, n_rows, cols, ldy, pos,
                                       topk_w, n_tokens, top_k, otype, ldo))
         return s;
-    if (!grad_y && !grad_w)
-        return fail(QMOE_ERR_INVALID_ARGUMENT, "%s: grad_y and grad_w are both null", fn);
     if (grad_y && ldg < cols)
         return fail(QMOE_ERR_INVALID_ARGUMENT, "%s: ldg=%lld must be >= cols=%lld", fn,
                     (long long)ldg, (long long)cols);
