@@ -251,13 +251,6 @@ __device__ __forceinline__ int cluster_ld_s32(const int* p, uint32_t rank) {
     return v;
 }
 
-// A store to the address that `p` has in CTA `rank`'s shared memory.
-__device__ __forceinline__ void cluster_st_f32(float* p, uint32_t rank, float v) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
-}
-
 // The address in shared::cluster space that `p` has in CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     uint32_t a;

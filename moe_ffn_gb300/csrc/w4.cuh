@@ -42,6 +42,11 @@ struct Params {
     DevCtl* err;
 };
 
+// A store to the address that `p` has in CTA `rank`'s shared memory.
+__device__ __forceinline__ void cluster_st_f32(float* p, uint32_t rank, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ float typed(uint32_t raw, int type) {
     return type == QMOE_F32    ? __uint_as_float(raw)
            : type == QMOE_BF16 ? __uint_as_float(raw << 16)
