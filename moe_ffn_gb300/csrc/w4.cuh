@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
-    const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
+    const int lg = 31 - __clz(ranks);
+    const int cluster = blockIdx.x >> lg, clusters = gridDim.x >> lg;
     const int kw = warp >> p.rts_log, rts = 1 << p.rts_log, rt = warp & (rts - 1);
     int* t_lo = reinterpret_cast<int*>(smem);
     int* t_hi = t_lo + p.E;
@@ -257,20 +258,14 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     float* red = reinterpret_cast<float*>(smem + ((3 * p.E + 1) * 4 + 15) / 16 * 16);
     float* far = red + 2 * WARPS * 8 * NB * RED_LD;
     uint4* xs = reinterpret_cast<uint4*>(smem + few_fixed(p.E, NB, p.slot * ranks));
-    pdl_wait();
-    pdl_trigger();
     int tiles = p.tiles;
-    if (p.offsets) {
-        gmm::build_tables(p, p.nt, p.nb, t_lo, t_hi, t_pre);
-        tiles = t_pre[p.E];
-        if (cluster >= tiles) return;
-    }
-
     const int units = (p.K + UNIT - 1) / UNIT;
     const int ub = min(rank * p.rank_units, units), ue = min(ub + p.rank_units, units);
     const int SG = p.K / S;  // scales of a row
     // rounds: a block to each of the wk parts
-    const int rounds = max(1, (ue - ub + p.wk * BLOCK - 1) / (p.wk * BLOCK));
+    const int kw_shift = 5 - p.rts_log;  // log2 of the units of a round, 4 wk
+    static_assert(WARPS * BLOCK == 32, "kw_shift");
+    const int rounds = max(1, (ue - ub + (1 << kw_shift) - 1) >> kw_shift);
 
     // what is loaded: rounds of the tile `next`
     uint4 w[BLOCK][2];                     // rows g and g + 8
@@ -294,8 +289,17 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
             l_s[h] = r * SG;
         }
     };
+    // (what does not depend on earlier launches comes before the wait for them)
+    if (!p.offsets) look_up(cluster);
+    pdl_wait();
+    pdl_trigger();
+    if (p.offsets) {
+        gmm::build_tables(p, p.nt, p.nb, t_lo, t_hi, t_pre);
+        tiles = t_pre[p.E];
+        if (cluster >= tiles) return;
+    }
     // the first unit of this warp's block of a round, and whether the block is whole
-    auto block_at = [&](int round) { return ub + (round * p.wk + kw) * BLOCK; };
+    auto block_at = [&](int round) { return ub + (round << kw_shift) + kw * BLOCK; };
     auto whole = [&](int u) { return u + BLOCK <= ue && (u + BLOCK) * UNIT <= p.K; };
     auto load_unit = [&](int u, bool all, int i) {
         if (all) {
@@ -369,43 +373,69 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     };
     // x of some rounds, in the order in which the products take it: for unit, step j,
     // column and lane t, the eight values of its place as pairs (0,4) (1,5) (2,6) (3,7)
-    auto stage_x = [&](int row0, int nv, int round) {
-        const int u0 = ub + round * p.wk * BLOCK;
-        const int n8 = min(p.pass_rounds * p.wk * BLOCK, ue - u0) * 16;  // eights of columns
-        for (int i = tid; i < n8 * nv; i += THREADS) {
-            const int tok = i / n8, o = i - tok * n8;
-            const int c = u0 * UNIT + o * 8;
-            const X* src = static_cast<const X*>(p.x) + (row0 + tok) * p.ldx + c;
-            Raw8<X> v;
-            if (c >= p.K) v.zero();
-            else if (p.vec_x) v.load(src);
-            else
+    // `then` runs once, behind the first loads.
+    auto stage_x = [&](int row0, int nv, int round, auto then) {
+        const int u0 = ub + (round << kw_shift);
+        const int n8 = min(p.pass_rounds << kw_shift, ue - u0) * 16;  // eights of columns
+        constexpr int AHEAD = F32X ? 2 : 4;  // loads in flight per thread
+        int tok = 0, o = tid;
+        auto settle = [&]() {
+            while (o >= n8 && tok < nv) {
+                o -= n8;
+                ++tok;
+            }
+        };
+        settle();
+        bool first = true;
+        do {
+            Raw8<X> v[AHEAD];
+            int at[AHEAD];  // token and eight of columns
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const X one = ldcg_value(src + e);
-                    if constexpr (F32X) v.w[e] = __float_as_uint(one);
-                    else reinterpret_cast<X*>(v.w)[e] = one;
-                }
-            int j, tt;
-            place<S>(o & 15, &j, &tt);
-            uint4* dst = xs + (static_cast<int64_t>(o >> 4) * 4 + j) * 4 * p.cols +
-                         tok * PARTS * 4 + tt;
-            uint4 out[PARTS];
-            pack_x<X>(v, out);
+            for (int b = 0; b < AHEAD; ++b) {
+                at[b] = -1;
+                if (tok >= nv) continue;
+                at[b] = tok << 24 | o;
+                const int c = u0 * UNIT + o * 8;
+                const X* src = static_cast<const X*>(p.x) + (row0 + tok) * p.ldx + c;
+                if (c >= p.K) v[b].zero();
+                else if (p.vec_x) v[b].load(src);
+                else
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) dst[q * 4] = out[q];
-        }
+                    for (int e = 0; e < 8; ++e) {
+                        const X one = ldcg_value(src + e);
+                        if constexpr (F32X) v[b].w[e] = __float_as_uint(one);
+                        else reinterpret_cast<X*>(v[b].w)[e] = one;
+                    }
+                o += THREADS;
+                settle();
+            }
+            if (first) then();
+            first = false;
+#pragma unroll
+            for (int b = 0; b < AHEAD; ++b) {
+                if (at[b] < 0) continue;
+                const int ob = at[b] & 0xFFFFFF;
+                int j, tt;
+                place<S>(ob & 15, &j, &tt);
+                uint4* dst = xs + static_cast<int64_t>((ob >> 4) * 4 + j) * js +
+                             (at[b] >> 24) * PARTS * 4 + tt;
+                uint4 out[PARTS];
+                pack_x<X>(v[b], out);
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) dst[q * 4] = out[q];
+            }
+        } while (tok < nv);
     };
 
-    look_up(cluster);
-    {
+    if (p.offsets) look_up(cluster);
+    auto load_first = [&]() {
         const int u = block_at(0);
         const bool all = whole(u);
         load_scales(u, all);
 #pragma unroll
         for (int i = 0; i < BLOCK; ++i) load_unit(u, all, i);
-    }
-    int staged = -1, buf = 0;
+    };
+    int staged = -1, buf = 0;  // -1: nothing is loaded yet
     for (int tile = cluster; tile < tiles; tile += clusters) {
         const gmm::Tile c = next;
         const bool more = tile + clusters < tiles;
@@ -419,7 +449,11 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
         for (int round = 0; round < rounds; ++round) {
             if (in_pass == 0 && (p.pass_rounds < rounds || staged != c.row0)) {
                 if (round > 0) __syncthreads();  // (a tile ends with a barrier)
-                stage_x(c.row0, c.nv, round);
+                // (the first tile's x, which comes from L2, and its codes, from further
+                // away, are asked for at once)
+                stage_x(c.row0, c.nv, round, [&]() {
+                    if (staged < 0) load_first();
+                });
                 staged = c.row0;
                 __syncthreads();
             }
@@ -437,7 +471,7 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
             const bool all = whole(u);
             if (load) load_scales(u, all);
             const int left = ue - block_at(round);  // units of this block and after it
-            const uint4* xu = xs + static_cast<int64_t>((in_pass * p.wk + kw) * BLOCK) * 4 * js;
+            const uint4* xu = xs + ((in_pass << kw_shift) + kw * BLOCK) * 4 * js;
 #pragma unroll
             for (int i = 0; i < BLOCK; ++i) {
                 if (i < left) product(i, xu + i * 4 * js);
@@ -462,8 +496,14 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
             const float* at = red + ((buf * WARPS + (row >> 4)) * 8 * NB + tok * PARTS) * RED_LD + (row & 15);
             float v = 0.f;
 #pragma unroll
-            for (int part = PARTS - 1; part >= 0; --part)
-                for (int k = 0; k < p.wk; ++k) v += at[((k << p.rts_log) * 8 * NB + part) * RED_LD];
+            for (int part = PARTS - 1; part >= 0; --part) {
+                float q[WARPS];
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k)
+                    q[k] = k < p.wk ? at[((k << p.rts_log) * 8 * NB + part) * RED_LD] : 0.f;
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k) v += q[k];
+            }
             const int n = c.nbi * rows16 + row;
             if (ranks > 1) cluster_st_f32(far + (buf * ranks + rank) * p.slot + i, 0u, v);
             else if (n < p.N) store_y(p, c.row0 + tok, n, v);
