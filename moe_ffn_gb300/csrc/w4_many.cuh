@@ -45,7 +45,7 @@ struct Many {
     static constexpr int THREADS = (FIRST + 24) * 32;
     // registers per thread after the split: no more in all than the launch was given,
     // 64 for each
-    static constexpr int REGS_AUX = 40, REGS_CODES = 56, REGS_SUMS = 104;
+    static constexpr int REGS_AUX = 40, REGS_CODES = 48, REGS_SUMS = 120;
     static_assert(2 * REGS_AUX + 4 * REGS_CODES + 2 * REGS_SUMS <= 64 * (FIRST + 24) / 4,
                   "register split");
     static constexpr int S_WARPS = TMA_X ? 4 : 1;  // for scales
@@ -452,11 +452,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int k = 0; k < nkb; ++k) {
                 const int kk = k % C::CB;
                 const uint32_t sr = ch % C::SR, ws = wi % C::WS;
+                // (every stage is waited for in turn, by a set that has nothing in it too:
+                // a wait must not be two phases ahead of its barrier)
                 if (kk == 0) ok = wait(&s_full[sr], (ch / C::SR) & 1);
+                if ((k & 1) == 0) ok = ok && wait(&w_full[ws], (wi / C::WS) & 1);
                 if (!ok) break;
                 if ((k & 1) == set) {
-                    ok = wait(&w_full[ws], (wi / C::WS) & 1);
-                    if (!ok) break;
                     const uint8_t* wr = base + C::O_W + ws * C::W_BYTES + row * 128;
                     uint32_t bias[C::GPB];
 #pragma unroll
