@@ -111,11 +111,11 @@ static size_t permute_ws(int64_t n_tokens, int32_t num_experts, int32_t top_k) {
     return (static_cast<size_t>(runs) * ((num_experts + 7) / 8 * 8) * 2 + 255) / 256 * 256;
 }
 
-template <int VB>
+template <int VB, bool STREAM>
 static cudaError_t launch_permute(steps::PermuteParams p, int64_t row_bytes, dim3 grid, size_t smem,
                                   cudaStream_t st) {
     p.nvec = static_cast<int>(row_bytes / VB);
-    return launch_pdl(steps::permute_kernel<VB>, grid, dim3(steps::P_THREADS), smem, st, p);
+    return launch_pdl(steps::permute_kernel<VB, STREAM>, grid, dim3(steps::P_THREADS), smem, st, p);
 }
 
 // ------------------------------------------------------------------- combine
@@ -158,10 +158,10 @@ static cudaError_t launch_combine(const steps::CombineParams& p, int64_t n_token
     if (p.grad_out)
         return launch_pdl(steps::combine_backward_kernel<Y, O, N>,
                           dim3(static_cast<unsigned>(n_tokens)), dim3(steps::C_THREADS), 0, st, p);
-    const int per = steps::C_THREADS * N;
+    const int per = steps::SUM_THREADS<N> * N;
     return launch_pdl(steps::combine_kernel<Y, O, N>,
                       dim3(static_cast<unsigned>(n_tokens), (p.cols + per - 1) / per),
-                      dim3(steps::C_THREADS), 0, st, p);
+                      dim3(steps::SUM_THREADS<N>), 0, st, p);
 }
 
 static qmoe_status run_combine(const steps::CombineParams& p, int ytype, int otype,
@@ -314,15 +314,21 @@ qmoe_status moe_permute(int xtype, const void* x, int64_t n_tokens, int64_t cols
         return aligned(x, b) && aligned(rows, b) && row_bytes % b == 0 && p.ldx % b == 0 &&
                p.ldr % b == 0;
     };
+    // Rows of more than half of L2 are written as a stream, evicted first: 4096 x 2048 top-8
+    // (134 MB) 29.8 -> 27.3 us, 16384 x 1024 (268 MB) 57.7 -> 53.0; fewer take as long either
+    // way and may still be there for the product that reads them.
+    const bool past_l2 = static_cast<int64_t>(p.P) * row_bytes > (int64_t{64} << 20);
     // few runs: several CTAs share a run's columns (and each finds its rows)
     const int64_t segs = (row_bytes / 16 + 127) / 128 * p.run;
     const int share = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(d->sms / p.runs, (segs + steps::P_WARPS - 1) / steps::P_WARPS)));
     const dim3 grid(p.runs, share);
     const size_t smem = static_cast<size_t>(steps::P_WARPS + 2) * p.Ep * 4;
-    const cudaError_t e = units(16)  ? launch_permute<16>(p, row_bytes, grid, smem, st)
-                          : units(4) ? launch_permute<4>(p, row_bytes, grid, smem, st)
-                                     : launch_permute<2>(p, row_bytes, grid, smem, st);
+    const cudaError_t e =
+        units(16) ? (past_l2 ? launch_permute<16, true>(p, row_bytes, grid, smem, st)
+                            : launch_permute<16, false>(p, row_bytes, grid, smem, st))
+        : units(4) ? launch_permute<4, false>(p, row_bytes, grid, smem, st)
+                   : launch_permute<2, false>(p, row_bytes, grid, smem, st);
     if (e != cudaSuccess) return cuda_fail(e, "permute launch");
     return QMOE_OK;
 }

@@ -378,7 +378,8 @@ template <> struct Unit<16> { using type = uint4; };
 template <> struct Unit<4> { using type = uint32_t; };
 template <> struct Unit<2> { using type = uint16_t; };
 
-template <int VB>
+// STREAM: rows that L2 does not hold, written evict-first.
+template <int VB, bool STREAM>
 __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams p) {
     using U = typename Unit<VB>::type;
     extern __shared__ int sm[];
@@ -419,9 +420,16 @@ __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams 
             U* dst = reinterpret_cast<U*>(p.rows + static_cast<int64_t>(row) * p.ldr);
 #pragma unroll
             for (int a = 0; a < P_AHEAD; ++a)
-                if (v0 + 32 * a < p.nvec) dst[v0 + 32 * a] = u[a];
+                if (v0 + 32 * a < p.nvec) {
+                    if constexpr (STREAM) __stcs(dst + v0 + 32 * a, u[a]);
+                    else dst[v0 + 32 * a] = u[a];
+                }
         }
     };
+    // this run's pairs, a part to each warp, the first 32 of it in registers
+    const int part = ((end - beg + P_WARPS - 1) / P_WARPS + 31) & ~31;
+    const int wbeg = min(beg + warp * part, end), wend = min(wbeg + part, end);
+    const int head_idx = wbeg + lane < wend ? __ldcg(p.idx + wbeg + lane) : -1;
     U early[P_EARLY][P_AHEAD];
 #pragma unroll
     for (int i = 0; i < P_EARLY; ++i) load(it0 + i * it_step, early[i]);
@@ -461,12 +469,10 @@ __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams 
             if (e >= 0) atomicAdd(&total[e], i < beg ? 0x10001 : 0x10000);
         }
     }
-    // this run's pairs, a part to each warp
-    const int part = ((end - beg + P_WARPS - 1) / P_WARPS + 31) & ~31;
-    const int wbeg = min(beg + warp * part, end), wend = min(wbeg + part, end);
+    const int head = head_idx >= 0 && head_idx < p.E ? head_idx : -1;
     int* h = whist + warp * p.Ep;
     for (int i = wbeg; i < wend; i += 32) {
-        const int e = i + lane < wend ? expert_of(p.idx, i + lane, p.E) : -1;
+        const int e = i == wbeg ? head : i + lane < wend ? expert_of(p.idx, i + lane, p.E) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, e);
         if (e >= 0 && lane == __ffs(same) - 1) h[e] += __popc(same);
         __syncwarp();
@@ -503,7 +509,7 @@ __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams 
     }
     __syncthreads();
     for (int i = wbeg; i < wend; i += 32) {
-        const int e = i + lane < wend ? expert_of(p.idx, i + lane, p.E) : -1;
+        const int e = i == wbeg ? head : i + lane < wend ? expert_of(p.idx, i + lane, p.E) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, e);
         int row = -1;
         if (e >= 0) row = h[e] + __popc(same & ((1u << lane) - 1u));
@@ -531,6 +537,10 @@ __global__ void __launch_bounds__(P_THREADS) permute_kernel(const PermuteParams 
 // whole aligned 16-byte units, else 1), eight slots at a step.
 constexpr int C_THREADS = 128;
 constexpr int C_AHEAD = 8;
+// Threads of the sum's CTAs: 64 take 512 columns of whole units (4096 x 2048 top-8: 28.3 us, 128
+// threads 29.3, 256 30.1), 128 single columns (1000 x 1111: 10.5 us, 64 threads 19.0).
+template <int N>
+constexpr int SUM_THREADS = N == 8 ? 64 : 128;
 
 struct CombineParams {
     const void* y;
@@ -549,6 +559,17 @@ struct CombineParams {
     float* grad_w;          // null: not wanted
 };
 
+// Eight values that are not read again by this call: evicted first from L2, where other
+// operands may still be wanted.
+template <class T>
+__device__ __forceinline__ void load_once(Raw8<T>& v, const T* p, uint64_t policy) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+        asm volatile(
+            "ld.relaxed.gpu.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+            : "=r"(v.w[4 * i]), "=r"(v.w[4 * i + 1]), "=r"(v.w[4 * i + 2]), "=r"(v.w[4 * i + 3])
+            : "l"(reinterpret_cast<const uint4*>(p) + i), "l"(policy));
+}
 // One value, with the interface of Raw8.
 template <class T>
 struct Raw1 {
@@ -577,13 +598,14 @@ __device__ __forceinline__ void load_slots(const CombineParams& p, int64_t t, in
 }
 
 template <class Y, class O, int N>
-__global__ void __launch_bounds__(C_THREADS) combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(SUM_THREADS<N>) combine_kernel(const CombineParams p) {
     const int64_t t = blockIdx.x;
-    const int c = (blockIdx.y * C_THREADS + threadIdx.x) * N;
+    const int c = (blockIdx.y * SUM_THREADS<N> + threadIdx.x) * N;
     const int lane = threadIdx.x & 31;
     const bool in = c < p.cols;
     pdl_wait();
     pdl_trigger();
+    const uint64_t once = policy_evict_first();
     int slot_row;
     float slot_w;
     load_slots(p, t, lane, &slot_row, &slot_w);
@@ -602,8 +624,11 @@ __global__ void __launch_bounds__(C_THREADS) combine_kernel(const CombineParams 
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s) {
             v[s].zero();
-            if (in && r[s] >= 0)
-                v[s].load(static_cast<const Y*>(p.y) + static_cast<int64_t>(r[s]) * p.ldy + c);
+            if (in && r[s] >= 0) {
+                const Y* at = static_cast<const Y*>(p.y) + static_cast<int64_t>(r[s]) * p.ldy + c;
+                if constexpr (N == 8) load_once(v[s], at, once);
+                else v[s].load(at);
+            }
         }
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s)
