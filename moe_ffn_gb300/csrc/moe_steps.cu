@@ -158,7 +158,7 @@ static cudaError_t launch_combine(const steps::CombineParams& p, int64_t n_token
     if (p.grad_out)
         return launch_pdl(steps::combine_backward_kernel<Y, O, N>,
                           dim3(static_cast<unsigned>(n_tokens)), dim3(steps::C_THREADS), 0, st, p);
-    const int per = steps::SUM_THREADS<N> * N;
+    const int per = steps::SUM_GROUPS<N> * steps::SUM_THREADS<N> * N;
     return launch_pdl(steps::combine_kernel<Y, O, N>,
                       dim3(static_cast<unsigned>(n_tokens), (p.cols + per - 1) / per),
                       dim3(steps::SUM_THREADS<N>), 0, st, p);

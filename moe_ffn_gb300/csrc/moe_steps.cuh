@@ -541,6 +541,9 @@ constexpr int C_AHEAD = 8;
 // threads 29.3, 256 30.1), 128 single columns (1000 x 1111: 10.5 us, 64 threads 19.0).
 template <int N>
 constexpr int SUM_THREADS = N == 8 ? 64 : 128;
+// Groups of N columns a thread takes, a CTA's width apart.
+template <int N>
+constexpr int SUM_GROUPS = N == 8 ? 1 : 4;
 
 struct CombineParams {
     const void* y;
@@ -599,21 +602,23 @@ __device__ __forceinline__ void load_slots(const CombineParams& p, int64_t t, in
 
 template <class Y, class O, int N>
 __global__ void __launch_bounds__(SUM_THREADS<N>) combine_kernel(const CombineParams p) {
+    constexpr int G = SUM_GROUPS<N>, STEP = SUM_THREADS<N> * N;
     const int64_t t = blockIdx.x;
-    const int c = (blockIdx.y * SUM_THREADS<N> + threadIdx.x) * N;
+    const int c0 = blockIdx.y * G * STEP + threadIdx.x * N;
     const int lane = threadIdx.x & 31;
-    const bool in = c < p.cols;
     pdl_wait();
     pdl_trigger();
     const uint64_t once = policy_evict_first();
     int slot_row;
     float slot_w;
     load_slots(p, t, lane, &slot_row, &slot_w);
-    float a[N];
+    float a[G][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i] = 0.f;
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[g][i] = 0.f;
     for (int s0 = 0; s0 < p.k; s0 += C_AHEAD) {
-        Run<Y, N> v[C_AHEAD];
+        Run<Y, N> v[C_AHEAD][G];
         float w[C_AHEAD];
         int r[C_AHEAD];
 #pragma unroll
@@ -623,26 +628,34 @@ __global__ void __launch_bounds__(SUM_THREADS<N>) combine_kernel(const CombinePa
         }
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s) {
-            v[s].zero();
-            if (in && r[s] >= 0) {
-                const Y* at = static_cast<const Y*>(p.y) + static_cast<int64_t>(r[s]) * p.ldy + c;
-                if constexpr (N == 8) load_once(v[s], at, once);
-                else v[s].load(at);
+            const Y* at = static_cast<const Y*>(p.y) + static_cast<int64_t>(r[s]) * p.ldy + c0;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                v[s][g].zero();
+                if (r[s] < 0 || c0 + g * STEP >= p.cols) continue;
+                if constexpr (N == 8) load_once(v[s][g], at + g * STEP, once);
+                else v[s][g].load(at + g * STEP);
             }
         }
 #pragma unroll
         for (int s = 0; s < C_AHEAD; ++s)
 #pragma unroll
-            for (int i = 0; i < N; ++i) a[i] = fmaf(w[s], v[s].get(i), a[i]);
-    }
-    if (!in) return;
-    if (p.residual) {
-        Run<O, N> q;
-        q.load(static_cast<const O*>(p.residual) + t * p.ldo + c);
+            for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int i = 0; i < N; ++i) a[i] += q.get(i);
+                for (int i = 0; i < N; ++i) a[g][i] = fmaf(w[s], v[s][g].get(i), a[g][i]);
     }
-    store_run<O, N>(static_cast<O*>(p.out) + t * p.ldo + c, a);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int c = c0 + g * STEP;
+        if (c >= p.cols) continue;
+        if (p.residual) {
+            Run<O, N> q;
+            q.load(static_cast<const O*>(p.residual) + t * p.ldo + c);
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[g][i] += q.get(i);
+        }
+        store_run<O, N>(static_cast<O*>(p.out) + t * p.ldo + c, a[g]);
+    }
 }
 
 // Gradients: of a row, grad_y[pos[t][s]] = w[t][s] grad_out[t], rounded once; of a
