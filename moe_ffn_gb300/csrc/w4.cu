@@ -18,13 +18,19 @@ namespace qmoe {
 constexpr int64_t W4_MAX_COLS = 1 << 20;
 constexpr int64_t W4_MAX_ROWS = 0x7fffff00;
 constexpr int W4_MAX_GROUPS = 1024;
+constexpr int64_t W4_MAX_TILES = 0x7fff0000;  // an int counts them, one grid past the last
 
 static int w4_size(int t) { return t == QMOE_F32 ? 4 : t == QMOE_BF16 || t == QMOE_F16 ? 2 : 0; }
+
+static qmoe_status too_many_tiles(const w4::Params& p) {
+    return fail(QMOE_ERR_UNSUPPORTED, "4-bit product: %d rows of W times %d of x in %d groups are too "
+                "many", p.N, p.M, p.E);
+}
 
 // The kernel for few rows: tiles of 16 weight rows and as many tokens as NB MMA column
 // blocks of eight hold.
 template <class X, int S, int NB>
-static cudaError_t launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
+static qmoe_status launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
     constexpr int parts = std::is_same<X, float>::value ? 3 : 1;
     p.nt = 8 * NB / parts;
     p.cols = std::min(p.nt, p.M) * parts;
@@ -57,6 +63,7 @@ static cudaError_t launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
         if (q.pass_rounds == rounds && (full || blocks <= w4::WARPS)) break;
     }
     const int64_t tiles = gmm::max_tiles(p.M, p.E, p.nt, p.nb);
+    if (tiles > W4_MAX_TILES) return too_many_tiles(p);
     p.tiles = static_cast<int>(tiles);
     for (p.rts_log = 0; (p.wk << p.rts_log) < w4::WARPS;) ++p.rts_log;
     auto kern = w4::few_kernel<X, S, NB>;
@@ -64,7 +71,7 @@ static cudaError_t launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
     if (!configured[d.dev].load()) {
         const cudaError_t e = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(4-bit product)");
         configured[d.dev].store(true);
     }
     const int clusters = static_cast<int>(std::min<int64_t>(tiles, 2 * d.sms / ranks));
@@ -82,7 +89,9 @@ static cudaError_t launch_few(w4::Params p, const DevInfo& d, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
+    return QMOE_OK;
 }
 
 static qmoe_status tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
@@ -158,6 +167,7 @@ static qmoe_status launch_many(w4::Params p, const DevInfo& d, cudaStream_t st) 
             return s;
     p.nb = (p.N + w4::MANY_ROWS - 1) / w4::MANY_ROWS;
     const int64_t tiles = gmm::max_tiles(p.M, p.E, w4::MANY_NT, p.nb);
+    if (tiles > W4_MAX_TILES) return too_many_tiles(p);
     const int kb = (p.K + 127) / 128;
     int ranks = 1;
     for (int i = 0; i < 3 && tiles <= fit[d.dev][i].load() && (2 << i) <= kb; ++i) ranks = 2 << i;
@@ -197,10 +207,7 @@ static qmoe_status launch_rows(const w4::Params& p, const DevInfo& d, cudaStream
             if (p.vec_x) return launch_many<w4::Many<X, S, true>>(p, d, st);
         return launch_many<w4::Many<X, S, false>>(p, d, st);
     }
-    const cudaError_t e =
-        p.M <= one * groups ? launch_few<X, S, 1>(p, d, st) : launch_few<X, S, 2>(p, d, st);
-    if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
-    return QMOE_OK;
+    return p.M <= one * groups ? launch_few<X, S, 1>(p, d, st) : launch_few<X, S, 2>(p, d, st);
 }
 
 template <class X>
@@ -259,9 +266,6 @@ static qmoe_status w4_run(const char* fn, const void* W, int stype, const void* 
     p.ytype = ytype;
     p.vec_x = aligned(x, 16) && (ldx * w4_size(xtype)) % 16 == 0;
     p.err = d->err;
-    if (gmm::max_tiles(p.M, p.E, 5, (p.N + 15) / 16) > 0x7fffffff)
-        return fail(QMOE_ERR_UNSUPPORTED, "%s: rows=%lld times n=%lld is too large", fn,
-                    (long long)rows, (long long)n_rows);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return xtype == QMOE_F32    ? launch_scales<float>(p, *d, st)
            : xtype == QMOE_BF16 ? launch_scales<__nv_bfloat16>(p, *d, st)

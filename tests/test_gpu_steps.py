@@ -561,3 +561,69 @@ def test_rows_beyond_2_31_elements(qm):
         tok, slot = int(order[i]) // k, int(order[i]) % k
         want = (w[tok, slot] * x[tok].float()).to(torch.bfloat16)
         assert torch.equal(rows[i], want)
+
+
+def test_named_streams_and_addresses(qm):
+    """The checks' long way: a stream object, a stream's address, arrays by address."""
+    import torch
+    g = np.random.default_rng(6)
+    t, e, k, h = 40, 16, 4, 72
+    x, logits, _, _ = layer_inputs(g, t, h, 32, e)
+    new = {"idx": (t, k), "pos": (t, k), "off": (e + 1,)}
+    b = {n: torch.zeros(*s, dtype=torch.int32, device="cuda") for n, s in new.items()}
+    b["w"], b["out"] = torch.zeros(t, k, device="cuda"), torch.zeros(t, h, device="cuda")
+    b["rows"] = torch.zeros(t * k, h, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(qm.moe_permute_workspace_size(t, e, k), dtype=torch.uint8, device="cuda")
+
+    def run(stream, at):
+        qm.moe_route(qm.F32, at(logits), t, e, k, at(b["idx"]), at(b["w"]), stream=stream)
+        qm.moe_permute(qm.BF16, at(x), t, h, at(b["idx"]), e, k, at(b["rows"]), at(b["off"]),
+                       at(b["pos"]), at(ws), ws_bytes=ws.numel(), stream=stream)
+        qm.moe_combine(qm.BF16, at(b["rows"]), t * k, h, at(b["pos"]), at(b["w"]), t, k, qm.F32,
+                       None, at(b["out"]), stream=stream)
+    run(None, lambda a: a)
+    torch.cuda.synchronize()
+    want = {n: a.clone() for n, a in b.items()}
+    side = torch.cuda.Stream()
+    for stream, at in ((side, lambda a: a), (side.cuda_stream, lambda a: a.data_ptr())):
+        for a in b.values():
+            a.zero_()
+        torch.cuda.synchronize()
+        run(stream, at)
+        torch.cuda.synchronize()
+        assert all(torch.equal(want[n], b[n]) for n in b)
+
+
+def test_sort_beside_an_overlapping_consumer(qm):
+    """A chain in which every launch may start before its predecessor has ended, many times
+    over: each sort and sum sees the routes and rows of its own turn."""
+    import torch
+    g = np.random.default_rng(12)
+    t, e, k, h = 1300, 32, 8, 64     # (sorted by two launches)
+    x, _, _, _ = layer_inputs(g, t, h, 32, e)
+    logits = [torch.randn(t, e, device="cuda") for _ in range(6)]
+    one = [{}, {}]
+    for b in one:
+        b.update(idx=torch.zeros(t, k, dtype=torch.int32, device="cuda"),
+                 w=torch.zeros(t, k, device="cuda"),
+                 pos=torch.zeros(t, k, dtype=torch.int32, device="cuda"),
+                 off=torch.zeros(e + 1, dtype=torch.int32, device="cuda"),
+                 rows=torch.zeros(t * k, h, dtype=torch.bfloat16, device="cuda"),
+                 ws=torch.empty(qm.moe_permute_workspace_size(t, e, k), dtype=torch.uint8,
+                                device="cuda"))
+
+    def turn(b, lg, out):
+        qm.moe_route(qm.F32, lg, t, e, k, b["idx"], b["w"])
+        qm.moe_permute(qm.BF16, x, t, h, b["idx"], e, k, b["rows"], b["off"], b["pos"], b["ws"])
+        qm.moe_combine(qm.BF16, b["rows"], t * k, h, b["pos"], b["w"], t, k, qm.F32, None, out)
+        return out
+    want = []
+    for lg in logits:
+        want.append(turn(one[0], lg, torch.zeros(t, h, device="cuda")))
+        torch.cuda.synchronize()
+    outs = [torch.zeros(t, h, device="cuda") for _ in range(60)]
+    for i, out in enumerate(outs):
+        turn(one[1], logits[i % 6], out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want[i % 6]) for i, out in enumerate(outs))
+    assert qm.device_status() == qm.OK

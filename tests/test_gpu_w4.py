@@ -400,3 +400,105 @@ def test_layer_of_4_bit_experts(qm, t):
             want[tok] += term
     off_by = np.linalg.norm(f64(out) - want) / np.linalg.norm(want)
     assert off_by <= 2.0 ** -14, off_by
+
+
+# ------------------------------------------------- streams, graphs, addresses
+def test_first_calls_may_be_captured():
+    """A process whose first call of each function is inside a capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, moe_ffn_gb300 as qm
+t, e, k, h = 3, 8, 2, 128
+def new(*s, dt=torch.float32): return torch.zeros(*s, dtype=dt, device="cuda")
+x, logits = torch.randn(t, h, device="cuda"), torch.randn(t, e, device="cuda")
+idx, w, pos = new(t, k, dt=torch.int32), new(t, k), new(t, k, dt=torch.int32)
+rows, off, out = new(t * k, h), new(e + 1, dt=torch.int32), new(t, h)
+gw, gy, gl = new(t, k), new(t * k, h), new(t, e)
+ws = torch.empty(qm.moe_permute_workspace_size(t, e, k), dtype=torch.uint8, device="cuda")
+# code 9 and scale 1 everywhere: every output is the sum of its row of x
+W, s = torch.full((64, h // 2), 0x99, dtype=torch.uint8, device="cuda"), torch.ones(64, 1, device="cuda")
+big, bs = torch.full((4096, 512), 0x99, dtype=torch.uint8, device="cuda"), torch.ones(4096, 8, device="cuda")
+xb, yb = torch.ones(64, 1024, device="cuda").bfloat16(), new(64, 4096)
+y = new(t, 64)
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    qm.moe_route(qm.F32, logits, t, e, k, idx, w)
+    qm.moe_permute(qm.F32, x, t, h, idx, e, k, rows, off, pos, ws)
+    qm.moe_combine(qm.F32, rows, t * k, h, pos, w, t, k, qm.F32, None, out)
+    qm.moe_combine_backward(qm.F32, rows, t * k, h, pos, w, t, k, qm.F32, x, gy, gw)
+    qm.moe_route_backward(qm.F32, logits, t, e, k, idx, w, gw, gl)
+    qm.w4_mm(W, qm.F32, s, None, 128, 64, h, qm.F32, x, t, qm.F32, y)
+    qm.w4_mm(big, qm.F32, bs, None, 128, 4096, 1024, qm.BF16, xb, 64, qm.F32, yb)
+g.replay()
+torch.cuda.synchronize()
+assert qm.device_status() == qm.OK
+assert torch.allclose(out, x, atol=1e-5)          # (weights add up to 1)
+assert torch.allclose(y, x.sum(1, keepdim=True).expand(t, 64), atol=1e-4)
+assert (yb == 1024).all()
+assert torch.allclose(gl.sum(1), new(t), atol=1e-4)
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("m", [3, 400])
+def test_streams_graphs_and_addresses(qm, m):
+    """The same bits on another stream (current, or named), by addresses, and replayed from a
+    graph beside a plain call on a second stream."""
+    import torch
+    g = np.random.default_rng(m)
+    n, k, S = 1500, 1024, 64
+    q, s, z, _ = weights(qm, g, 1, n, k, S, "f16", True)
+    x = torch.randn(m, k, device="cuda").to(torch.bfloat16)
+
+    def call(y, stream=None, addresses=False):
+        a = [t.data_ptr() for t in (q, s, z, x, y)] if addresses else [q, s, z, x, y]
+        qm.w4_mm(a[0], qm.F16, a[1], a[2], S, n, k, qm.BF16, a[3], m, qm.F32, a[4], stream=stream)
+    want = torch.zeros(m, n, device="cuda")
+    call(want)
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    ys = [torch.zeros(m, n, device="cuda") for _ in range(5)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(one):
+        call(ys[0])
+    call(ys[1], stream=one)
+    call(ys[2], stream=two.cuda_stream, addresses=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=one):
+        call(ys[3])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(one):
+        graph.replay()
+    with torch.cuda.stream(two):
+        call(ys[4])
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, y) for y in ys)
+    assert qm.device_status() == qm.OK
+
+
+@pytest.mark.parametrize("m", [1, 300])
+def test_reads_what_the_stream_has_just_written(qm, m):
+    """Weights, scales and rows written by the launches right before the call."""
+    import torch
+    n, k, S = 2000, 2048, 128
+    g = np.random.default_rng(4)
+    q, s, z, wv = weights(qm, g, 1, n, k, S, "f32", True)
+    x = (0.01 * torch.randn(m, k, device="cuda")).to(torch.float16)
+    live = [torch.zeros_like(t) for t in (q, s, z, x)]
+    y = torch.zeros(m, n, device="cuda")
+    want, err = ref.w4_product(f64(x), wv[0], S)
+    for _ in range(20):
+        for a in live:
+            a.zero_()
+        qm.w4_mm(live[0], qm.F32, live[1], live[2], S, n, k, qm.F16, live[3], m, qm.F32, y)
+        for a, b in zip(live, (q, s, z, x)):
+            a.copy_(b)
+        qm.w4_mm(live[0], qm.F32, live[1], live[2], S, n, k, qm.F16, live[3], m, qm.F32, y)
+    check(f64(y), want, ref.rounded(want, err, "f32"), "after copies")
