@@ -155,21 +155,31 @@ __device__ __forceinline__ void codes(uint32_t w, uint32_t bias, uint32_t (&a)[4
     a[3] = fma2<X>(v & 0x00F000F0u, Magic<X>::HIGH, bias);
 }
 
-// Eight f32 values in three bf16 parts each (their bits), of eight leading bits, cut off one
-// after another, which leaves exact rests.  (Infinities and NaN have no rest: they stay
-// whole in part 0.)
+// Eight f32 values in three bf16 parts each, of eight leading bits, cut off one after
+// another, which leaves exact rests: the upper halves of h.  (Infinities and NaN have no
+// rest: they stay whole in part 0.)
 __device__ __forceinline__ void split3(const Raw8<float>& v, uint32_t (&h)[3][8]) {
+    uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        float f = v.get(e);
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {
-            h[q][e] = __float_as_uint(f) >> 16;
-            const bool finite = (h[q][e] & 0x7F80u) != 0x7F80u;
-            if (!finite && (__float_as_uint(f) & 0x7FFFFFu)) h[q][e] |= 0x40u;
-            f = finite ? f - __uint_as_float(h[q][e] << 16) : 0.f;
-        }
+        const float f1 = __uint_as_float(v.w[e]) - __uint_as_float(v.w[e] & 0xFFFF0000u);
+        const float f2 = f1 - __uint_as_float(__float_as_uint(f1) & 0xFFFF0000u);
+        h[0][e] = v.w[e];
+        h[1][e] = __float_as_uint(f1);
+        h[2][e] = __float_as_uint(f2);
+        top = max(top, v.w[e] & 0x7FFFFFFFu);
     }
+    if (top < 0x7F800000u) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if ((v.w[e] & 0x7F800000u) == 0x7F800000u) {
+            if (v.w[e] & 0x7FFFFFu) h[0][e] |= 0x00400000u;  // (a NaN by its low bits alone)
+            h[1][e] = h[2][e] = 0u;
+        }
+}
+// The bf16 in the upper halves of two words, a's first.
+__device__ __forceinline__ uint32_t upper2(uint32_t a, uint32_t b) {
+    return __byte_perm(a, b, 0x7632);
 }
 // Eight values of x as pairs (0,4) (1,5) (2,6) (3,7), the order in which codes() leaves a
 // word; an f32 x in three parts.
@@ -181,8 +191,8 @@ __device__ __forceinline__ void pack_x(const Raw8<X>& v,
         split3(v, h);
 #pragma unroll
         for (int q = 0; q < 3; ++q)
-            out[q] = make_uint4(h[q][0] | h[q][4] << 16, h[q][1] | h[q][5] << 16,
-                                h[q][2] | h[q][6] << 16, h[q][3] | h[q][7] << 16);
+            out[q] = make_uint4(upper2(h[q][0], h[q][4]), upper2(h[q][1], h[q][5]),
+                                upper2(h[q][2], h[q][6]), upper2(h[q][3], h[q][7]));
     } else {
         out[0] = make_uint4(__byte_perm(v.w[0], v.w[2], 0x5410), __byte_perm(v.w[0], v.w[2], 0x7632),
                             __byte_perm(v.w[1], v.w[3], 0x5410), __byte_perm(v.w[1], v.w[3], 0x7632));

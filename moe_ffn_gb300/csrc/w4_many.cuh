@@ -45,11 +45,12 @@ struct Many {
     static constexpr int THREADS = (FIRST + 24) * 32;
     // registers per thread after the split: no more in all than the launch was given,
     // 64 for each
-    static constexpr int REGS_AUX = 40, REGS_CODES = 48, REGS_SUMS = 120;
-    static_assert(2 * REGS_AUX + 4 * REGS_CODES + 2 * REGS_SUMS <= 64 * (FIRST + 24) / 4,
+    static constexpr int REGS_AUX = 40, REGS_X = TMA_X ? REGS_AUX : 72, REGS_CODES = 48,
+                         REGS_SUMS = TMA_X ? 120 : 104;
+    static_assert(REGS_AUX + REGS_X + 4 * REGS_CODES + 2 * REGS_SUMS <= 64 * (FIRST + 24) / 4,
                   "register split");
     static constexpr int S_WARPS = TMA_X ? 4 : 1;  // for scales
-    static constexpr int BATCH = F32X ? 1 : 2;     // eights of columns in flight per thread
+    static constexpr int BATCH = F32X ? 4 : 8;     // eights of columns in flight per thread
     static constexpr int TM_A = DB * 2 * MANY_NT, TM_COLS = 512;
     static_assert(TM_A + AB * 2 * 64 <= TM_COLS, "tensor memory");
     static constexpr int O_W = XS * X_BYTES;
@@ -89,8 +90,8 @@ __device__ __forceinline__ void in_order(const Raw8<X>& v,
         split3(v, h);
 #pragma unroll
         for (int q = 0; q < 3; ++q)
-            out[q] = make_uint4(h[q][0] | h[q][1] << 16, h[q][2] | h[q][3] << 16,
-                                h[q][4] | h[q][5] << 16, h[q][6] | h[q][7] << 16);
+            out[q] = make_uint4(upper2(h[q][0], h[q][1]), upper2(h[q][2], h[q][3]),
+                                upper2(h[q][4], h[q][5]), upper2(h[q][6], h[q][7]));
     } else {
         out[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
     }
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         scales(tid - 128, 128);
     } else if (!C::TMA_X && warp < 8) {
         // ----------------------------------------------------- token rows
-        regs_dec<C::REGS_AUX>();
+        regs_inc<C::REGS_X>();
         const int th = tid - 128;
         uint32_t it = 0;
         bool ok = true;
