@@ -228,13 +228,5 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
                    "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
-// The same for two loads.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[16], uint32_t (&q)[16]) {
-    wait_ld(r);
-    asm volatile("" : "+r"(q[0]), "+r"(q[1]), "+r"(q[2]), "+r"(q[3]), "+r"(q[4]), "+r"(q[5]),
-                 "+r"(q[6]), "+r"(q[7]), "+r"(q[8]), "+r"(q[9]), "+r"(q[10]), "+r"(q[11]),
-                 "+r"(q[12]), "+r"(q[13]), "+r"(q[14]), "+r"(q[15])::"memory");
-}
-
 }  // namespace umma
 }  // namespace qmoe
