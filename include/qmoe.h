@@ -563,9 +563,9 @@ qmoe_status qmoe_set_exec_mode(int mode);
  * and, if skip_arrive_cta >= 0, that CTA of the cooperative layer kernels
  * never arrives at their grid barriers, so the other CTAs' waits run out:
  * the kernels then record QMOE_ERR_TIMEOUT (qmoe_device_status) and return
- * without writing the layer's output.  In f8_mm, mm_grouped and
- * moe_experts_f8 that CTA loads nothing, so the waits for its operands run
- * out.  (-1, 0) restores normal operation.
+ * without writing the layer's output.  In f8_mm, mm_grouped,
+ * moe_experts_f8 and the 4-bit products' kernel for many rows that CTA loads
+ * nothing, so the waits for its operands run out.  (-1, 0) restores normal operation.
  * Synchronises the device before writing the setting.  Errors: CUDA,
  * UNSUPPORTED (not sm_103), INVALID_ARGUMENT (skip_arrive_cta < -1).  The
  * pages have no counterpart; their CudaError model ("refuse, never compute

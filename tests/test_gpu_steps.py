@@ -215,6 +215,16 @@ def test_permute(qm, kind, t, h, e, k):
     run_permute(qm, g.standard_normal((t, h)), kind, g.integers(0, e, (t, k)), e)
 
 
+@pytest.mark.parametrize("t,e", [(20000, 128), (40000, 3)])
+def test_permute_long_runs(qm, t, e):
+    """More than 1024 pairs in a CTA's run (66 and 132 tokens of 16 slots): their rows do
+    not all fit in its table and the rest are read back from pos."""
+    g = np.random.default_rng(t)
+    idx = g.integers(0, e, (t, 16))
+    idx[g.random(idx.shape) < 0.05] = -1
+    run_permute(qm, g.standard_normal((t, 4)), "bf16", idx, e)
+
+
 @pytest.mark.parametrize("t", [1, 40, 1500])
 def test_permute_padding(qm, t):
     """Slots outside [0, E), experts without rows, tokens without any, all padded, and
