@@ -42,6 +42,14 @@ struct Params {
     DevCtl* err;
 };
 
+// A barrier over the cluster's threads in two steps that orders no memory: once it is
+// passed every CTA of the cluster has started, so its shared memory may be written.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // A store to the address that `p` has in CTA `rank`'s shared memory.
 __device__ __forceinline__ void cluster_st_f32(float* p, uint32_t rank, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "f"(v) : "memory");
@@ -270,6 +278,8 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     const int lg = 31 - __clz(ranks);
     const int cluster = blockIdx.x >> lg, clusters = gridDim.x >> lg;
     const int kw = warp >> p.rts_log, rts = 1 << p.rts_log, rt = warp & (rts - 1);
+    // (waited for before the first store to another CTA, when all have long started)
+    if (ranks > 1) cluster_arrive();
     int* t_lo = reinterpret_cast<int*>(smem);
     int* t_hi = t_lo + p.E;
     int* t_pre = t_hi + p.E;
@@ -314,7 +324,10 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     if (p.offsets) {
         gmm::build_tables(p, p.nt, p.nb, t_lo, t_hi, t_pre);
         tiles = t_pre[p.E];
-        if (cluster >= tiles) return;
+        if (cluster >= tiles) {
+            if (ranks > 1) cluster_wait();
+            return;
+        }
     }
     // the first unit of this warp's block of a round, and whether the block is whole
     auto block_at = [&](int round) { return ub + (round << kw_shift) + kw * BLOCK; };
@@ -509,6 +522,7 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
         }
         __syncthreads();
         const int shift = 4 + p.rts_log, rows16 = 16 << p.rts_log;
+        if (ranks > 1 && tile == cluster) cluster_wait();
         for (int i = tid; i < rows16 * c.nv; i += THREADS) {
             const int row = i & (rows16 - 1), tok = i >> shift;
             const float* at = red + ((buf * WARPS + (row >> 4)) * 8 * NB + tok * PARTS) * RED_LD + (row & 15);
