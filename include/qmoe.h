@@ -559,7 +559,9 @@ qmoe_status qmoe_device_status(void* stream);
 qmoe_status qmoe_set_exec_mode(int mode);
 
 /* Tests of the failure path only: on the current device, every bounded
- * device wait gives up after wait_limit_ns (0 restores the default, 2 s),
+ * device wait gives up after wait_limit_ns (0 restores the default, 2 s;
+ * within a factor of two in the 4-bit products' kernel for many rows, which
+ * counts tries of a barrier instead of reading the clock),
  * and, if skip_arrive_cta >= 0, that CTA of the cooperative layer kernels
  * never arrives at their grid barriers, so the other CTAs' waits run out:
  * the kernels then record QMOE_ERR_TIMEOUT (qmoe_device_status) and return

@@ -29,6 +29,7 @@ namespace w4 {
 constexpr int MANY_ROWS = 256;
 constexpr int MANY_NT = 64;
 constexpr unsigned NAP_NS = 200;
+constexpr unsigned TRY_NS = 3760;  // a nap and a try of a barrier that does not complete
 
 // TMA_X: token rows by TMA.
 template <class X_, int S_, bool TMA_X_>
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     using X = typename C::X;
     using H = typename C::H;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t s_naps;  // of a wait that runs out
+    __shared__ uint32_t s_tries;  // of a wait that runs out
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* sc_s = reinterpret_cast<float*>(base + C::O_S);
@@ -145,8 +146,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int i = 0; i < C::SR; ++i) { mbar_init(&s_full[i], C::S_WARPS); mbar_init(&s_empty[i], 24); }
         for (int i = 0; i < 2 * C::AB; ++i) { mbar_init(&a_full[i], 4); mbar_init(&a_empty[i], 1); }
         for (int i = 0; i < 2 * C::DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 4); }
-        const unsigned long long naps = wait_limit(p.err) / NAP_NS + 1;
-        s_naps = naps < 0xFFFFFFFFu ? static_cast<uint32_t>(naps) : 0xFFFFFFFFu;
+        const unsigned long long tries = wait_limit(p.err) / TRY_NS + 1;
+        s_tries = tries < 0xFFFFFFFFu ? static_cast<uint32_t>(tries) : 0xFFFFFFFFu;
         fence_barrier_init();
         prefetch_tensormap(&tm_w);
         if constexpr (C::TMA_X) prefetch_tensormap(&tm_x);
@@ -175,16 +176,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // whether a tile's half has weight rows (one without goes through the same steps,
     // its MMAs and sums left out)
     auto live = [&](const gmm::Tile& c, int h) { return c.nbi * MANY_ROWS + 128 * h < p.N; };
-    // Waits.  A try itself suspends the warp for a while, so a second one is rare; what
-    // follows the first is kept short, for there are many of these and the roles' loops
-    // share the instruction caches (with the pipelines' usual longer form 43 us for 64
-    // groups of 64 rows, 1024 x 2048, with this one 39).  The limit is counted in naps.  A
-    // wait that runs out does so for the whole warp: what follows is warp-wide.
+    // Waits.  A try itself suspends the warp, until the phase completes or for a time that the
+    // hardware sets, so a second one is rare; what follows the first is kept short, for there
+    // are many of these and the roles' loops share the instruction caches (with the
+    // pipelines' usual longer form 43 us for 64 groups of 64 rows, 1024 x 2048, with this one
+    // 39).  So the limit is a number of tries instead of a time: TRY_NS is what one took
+    // (25,000 in 93.8 ms; a longer suspend-time hint does not change the hardware's part).
+    // Reading the clock in this loop, in seven forms, cost 3 to 5% (37.7 -> 39.0 to 39.7
+    // us).  A wait that runs out does so for the whole warp: what follows is warp-wide.
     auto wait = [&](uint64_t* b, uint32_t parity) {
         bool ok = mbar_try_wait(b, parity);
         if (__all_sync(0xffffffffu, ok)) return true;
 #pragma unroll 1
-        for (uint32_t i = s_naps; i > 0 && !ok; --i) {
+        for (uint32_t i = s_tries; i > 0 && !ok; --i) {
             __nanosleep(NAP_NS);
             ok = mbar_try_wait(b, parity);
         }
