@@ -348,6 +348,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     wait(&x_empty[i % C::XS], (i / C::XS) & 1);
                 if (na0 > 0) wait(&a_empty[h], (na0 - 1) & 1);
                 if (na1 > 0) wait(&a_empty[2 + h], (na1 - 1) & 1);
+            } else if (nx > 0 || db > 0 || dph == 0) {
+                // (after a wait that ran out the other half may never commit what these
+                // barriers count: the last group's own commit says that all MMAs are done,
+                // which takes a microsecond, the tries 3.7 ms)
+                uint64_t* last = &d_full[(db > 0 ? db - 1 : C::DB - 1) * 2 + h];
+                const uint32_t done = db > 0 ? dph ^ 1 : dph;
+#pragma unroll 1
+                for (int i = 0; i < 1000 && !mbar_try_wait(last, done); ++i) {}
             }
         } else if (warp == 2) {
             // -------------------------------------------------------- TMA
