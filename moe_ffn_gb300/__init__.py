@@ -363,6 +363,19 @@ def _span(rows: int, cols: int, ld: int) -> int:
     return (rows - 1) * ld + cols if rows > 0 else 0
 
 
+def _fit(fn: str, small, large=(), nbytes: int = 0) -> None:
+    """Refuses integers that ctypes would cut to 32 (`small`) or 64 bits (`large`), or take
+    for a huge number of bytes: the library would go by another type or size than the one
+    the arrays were checked for.  (Callers first look at the OR of all of them, which is
+    nearly always 0 to 2^31 - 1.)"""
+    for bits, values in ((32, small), (64, large)):
+        for v in values:
+            if not -1 << bits - 1 <= v < 1 << bits - 1:
+                raise QmoeError(ERR_INVALID_ARGUMENT, f"{fn}: {v} does not fit {bits} bits")
+    if not 0 <= nbytes < 1 << 63:
+        raise QmoeError(ERR_INVALID_ARGUMENT, f"{fn}: ws_bytes={nbytes} does not fit a size")
+
+
 def f8_blocks(n: int) -> int:
     """Blocks of 128 that cover n elements (scales per row, or per column)."""
     return -(-n // 128)
@@ -371,6 +384,8 @@ def f8_blocks(n: int) -> int:
 def f8_quantize(xtype: int, x, rows: int, cols: int, q, scale, ldx=None, stream=None) -> None:
     """q, scale = e4m3 rows of x with one scale per 128 columns (see include/qmoe.h)."""
     fn, ldx = "f8_quantize", cols if ldx is None else ldx
+    if (xtype | rows | cols | ldx) >> 31:
+        _fit(fn, (xtype,), (rows, cols, ldx))
     dev, st = _context(stream)
     _check((_libh or lib()).f8_quantize(
         xtype, _arg(fn, "x", x, xtype, _span(rows, cols, ldx), dev, ldx), rows, cols, ldx,
@@ -383,6 +398,8 @@ def f8_mm(W, w_scale, rows: int, cols: int, x, x_scale, n_tokens: int, ytype: in
     """y = x W^T with e4m3 operands and block scales (see include/qmoe.h)."""
     fn, kb = "f8_mm", f8_blocks(cols)
     ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
+    if (ytype | rows | cols | n_tokens | ldx | ldy) >> 31:
+        _fit(fn, (ytype,), (rows, cols, n_tokens, ldx, ldy))
     dev, st = _context(stream)
     _check((_libh or lib()).f8_mm(
         _arg(fn, "W", W, E4M3, rows * cols, dev),
@@ -397,6 +414,8 @@ def mm_grouped(wtype: int, W, w_scale, num_groups: int, rows: int, cols: int, x,
     """y[r] = W_g x[r] for the rows of every group (see include/qmoe.h)."""
     fn, kb = "mm_grouped", f8_blocks(cols)
     ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
+    if (wtype | num_groups | ytype | rows | cols | n_rows | ldx | ldy) >> 31:
+        _fit(fn, (wtype, num_groups, ytype), (rows, cols, n_rows, ldx, ldy))
     dev, st = _context(stream)
     _check((_libh or lib()).mm_grouped(
         wtype, _arg(fn, "W", W, wtype, num_groups * rows * cols, dev),
@@ -427,6 +446,8 @@ def moe_experts_f8(gate_stack, gate_scale, up_stack, up_scale, down_stack, down_
         ws_bytes = ws.numel() * ws.element_size()
     elif ws is not None and not isinstance(ws, int):
         ws_need = -(-ws_bytes // ws.element_size())
+    if (xtype | ws_bytes) >> 31:
+        _fit(fn, (xtype,), (), ws_bytes)
     dev, st = _context(stream)
     _check((_libh or lib()).moe_experts_f8(
         _arg(fn, "gate_stack", gate_stack, E4M3, EFH, dev),
@@ -483,6 +504,8 @@ def moe_route(ltype: int, logits, n_tokens: int, num_experts: int, top_k: int, t
             0 if renormalize else ROUTE_NO_RENORM, stream)):
         return
     fn, ldl = "moe_route", num_experts if ldl is None else ldl
+    if (ltype | num_experts | top_k | n_tokens | ldl) >> 31:
+        _fit(fn, (ltype, num_experts, top_k), (n_tokens, ldl))
     dev, st = _context(stream)
     P = n_tokens * top_k
     _check((_libh or lib()).moe_route(
@@ -501,6 +524,8 @@ def moe_route_backward(ltype: int, logits, n_tokens: int, num_experts: int, top_
         return
     fn = "moe_route_backward"
     ldl, ldg = num_experts if ldl is None else ldl, num_experts if ldg is None else ldg
+    if (ltype | num_experts | top_k | n_tokens | ldl | ldg) >> 31:
+        _fit(fn, (ltype, num_experts, top_k), (n_tokens, ldl, ldg))
     dev, st = _context(stream)
     P = n_tokens * top_k
     _check((_libh or lib()).moe_route_backward(
@@ -513,6 +538,7 @@ def moe_route_backward(ltype: int, logits, n_tokens: int, num_experts: int, top_
 
 
 def moe_permute_workspace_size(n_tokens: int, num_experts: int, top_k: int) -> int:
+    _fit("moe_permute_workspace_size", (num_experts, top_k), (n_tokens,))
     n = int(lib().moe_permute_workspace_size(n_tokens, num_experts, top_k))
     if n == 0:
         raise QmoeError(ERR_INVALID_ARGUMENT, last_error())
@@ -532,6 +558,8 @@ def moe_permute(xtype: int, x, n_tokens: int, cols: int, topk_idx, num_experts: 
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     elif ws is not None and not isinstance(ws, int):
         ws_need = -(-ws_bytes // ws.element_size())
+    if (xtype | num_experts | top_k | n_tokens | cols | ldx | ldr | ws_bytes) >> 31:
+        _fit(fn, (xtype, num_experts, top_k), (n_tokens, cols, ldx, ldr), ws_bytes)
     dev, st = _context(stream)
     P = n_tokens * top_k
     _check((_libh or lib()).moe_permute(
@@ -550,6 +578,8 @@ def moe_combine(ytype: int, y, n_rows: int, cols: int, pos, topk_w, n_tokens: in
         return
     fn = "moe_combine"
     ldy, ldo = cols if ldy is None else ldy, cols if ldo is None else ldo
+    if (ytype | otype | top_k | n_rows | cols | n_tokens | ldy | ldo) >> 31:
+        _fit(fn, (ytype, otype, top_k), (n_rows, cols, n_tokens, ldy, ldo))
     dev, st = _context(stream)
     P, TH = n_tokens * top_k, _span(n_tokens, cols, ldo)
     _check((_libh or lib()).moe_combine(
@@ -570,6 +600,8 @@ def moe_combine_backward(ytype: int, y, n_rows: int, cols: int, pos, topk_w, n_t
     fn = "moe_combine_backward"
     ldy, ldo = cols if ldy is None else ldy, cols if ldo is None else ldo
     ldg = cols if ldg is None else ldg
+    if (ytype | otype | top_k | n_rows | cols | n_tokens | ldy | ldo | ldg) >> 31:
+        _fit(fn, (ytype, otype, top_k), (n_rows, cols, n_tokens, ldy, ldo, ldg))
     dev, st = _context(stream)
     P = n_tokens * top_k
     _check((_libh or lib()).moe_combine_backward(
@@ -592,6 +624,8 @@ def w4_mm(W, stype: int, scale, zero, scale_cols: int, rows: int, cols: int, xty
         return
     fn = "w4_mm"
     ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
+    if (stype | scale_cols | xtype | ytype | rows | cols | n_tokens | ldx | ldy) >> 31:
+        _fit(fn, (stype, scale_cols, xtype, ytype), (rows, cols, n_tokens, ldx, ldy))
     dev, st = _context(stream)
     blocks = rows * (cols // scale_cols) if scale_cols > 0 else 0
     _check((_libh or lib()).w4_mm(
@@ -613,6 +647,8 @@ def w4_mm_grouped(W, stype: int, scale, zero, scale_cols: int, num_groups: int, 
         return
     fn = "w4_mm_grouped"
     ldx, ldy = cols if ldx is None else ldx, rows if ldy is None else ldy
+    if (stype | scale_cols | num_groups | xtype | ytype | rows | cols | n_rows | ldx | ldy) >> 31:
+        _fit(fn, (stype, scale_cols, num_groups, xtype, ytype), (rows, cols, n_rows, ldx, ldy))
     dev, st = _context(stream)
     n = num_groups * rows
     blocks = n * (cols // scale_cols) if scale_cols > 0 else 0
