@@ -16,13 +16,15 @@ import os
 import subprocess
 import sysconfig
 import threading
+import warnings
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
 LIB_PATH = os.path.join(_HERE, "libqmoe.so")
 HEADER = os.path.join(_ROOT, "include", "qmoe.h")
-CALLS_PATH = os.path.join(_HERE, "_calls.so")  # csrc/calls.c, the short way into the library
+# csrc/calls.c, the short way into the library, for this interpreter
+CALLS_PATH = os.path.join(_HERE, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 # qmoe_qtype
 F32, Q8_0, Q4_0, Q4_K, Q5_K, Q6_K = 0, 1, 2, 3, 4, 5
@@ -49,21 +51,35 @@ class QmoeError(RuntimeError):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
 
 
-def _sources():
-    return sorted(os.path.join(_CSRC, f) for f in os.listdir(_CSRC)
-                  if f.endswith((".cu", ".cuh", ".c")))
+def _sources(*endings):
+    return sorted(os.path.join(_CSRC, f) for f in os.listdir(_CSRC) if f.endswith(endings))
+
+
+def _stale(path: str, sources) -> bool:
+    return not os.path.exists(path) or os.path.getmtime(path) < max(
+        os.path.getmtime(s) for s in (*sources, HEADER))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libqmoe.so in-tree for sm_103a with nvcc."""
-    srcs = _sources() + [HEADER]
-    built = min((os.path.getmtime(f) if os.path.exists(f) else 0) for f in (LIB_PATH, CALLS_PATH))
-    if not force and built >= max(os.path.getmtime(s) for s in srcs):
-        return LIB_PATH
+    """Compile libqmoe.so in-tree for sm_103a with nvcc, and the binding's C module with
+    the C compiler.  Where the module does not compile (no headers of the interpreter)
+    the library is there all the same, and calls go through ctypes."""
+    calls = None
+    if force or _stale(CALLS_PATH, _sources(".c")):
+        calls = _start_calls(verbose)
+    try:
+        if force or _stale(LIB_PATH, _sources(".cu", ".cuh")):
+            _build_lib(verbose)
+    finally:
+        if calls is not None:
+            _finish_calls(*calls)
+    return LIB_PATH
+
+
+def _build_lib(verbose: bool) -> None:
     nvcc = os.environ.get("NVCC", "nvcc")
     if not os.path.exists(nvcc) and os.path.exists("/usr/local/cuda/bin/nvcc"):
         nvcc = "/usr/local/cuda/bin/nvcc"
-    tag = f".{os.getpid()}.tmp"
     objs = [os.path.join(_HERE, u.replace(".cu", f".{os.getpid()}.o")) for u in UNITS]
     procs = []
     for u, o in zip(UNITS, objs):
@@ -71,21 +87,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd))
         procs.append(subprocess.Popen(cmd))
-    calls = CALLS_PATH + tag
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC",
-           "-I" + sysconfig.get_paths()["include"], "-o", calls, os.path.join(_CSRC, "calls.c")]
-    if verbose:
-        print(" ".join(cmd))
-    procs.append(subprocess.Popen(cmd))
     codes = [p.wait() for p in procs]
     try:
-        if codes[-1]:
-            raise subprocess.CalledProcessError(codes[-1], "calls.c")
-        os.replace(calls, CALLS_PATH)
         for u, c in zip(UNITS, codes):
             if c:
                 raise subprocess.CalledProcessError(c, f"nvcc {u}")
-        tmp = LIB_PATH + tag
+        tmp = LIB_PATH + f".{os.getpid()}.tmp"
         cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-o", tmp, *objs]
         if verbose:
             print(" ".join(cmd))
@@ -95,7 +102,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for o in objs:
             if os.path.exists(o):
                 os.remove(o)
-    return LIB_PATH
+
+
+def _start_calls(verbose: bool):
+    """(the compiler's process or None, its output file)"""
+    tmp = CALLS_PATH + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC",
+           "-I" + sysconfig.get_paths()["include"], "-o", tmp, os.path.join(_CSRC, "calls.c")]
+    if verbose:
+        print(" ".join(cmd))
+    try:
+        return subprocess.Popen(cmd), tmp
+    except OSError:
+        return None, tmp
+
+
+def _finish_calls(proc, tmp: str) -> None:
+    global _calls
+    if proc is not None and proc.wait() == 0:
+        os.replace(tmp, CALLS_PATH)
+        if _calls is _LONG_WAY:
+            _calls = None
+        return
+    for f in (tmp, CALLS_PATH):  # (one of older sources would not fit the library)
+        if os.path.exists(f):
+            os.remove(f)
+    warnings.warn("csrc/calls.c could not be compiled: calls go through ctypes, which costs the "
+                  "host about 4 us more each", RuntimeWarning, stacklevel=3)
 
 
 class _Shape(ctypes.Structure):
@@ -464,7 +497,25 @@ def moe_experts_f8(gate_stack, gate_scale, up_stack, up_scale, down_stack, down_
 # ------------------- steps around the experts' products (include/qmoe.h)
 # These calls first go the short way of csrc/calls.c, which answers None for whatever it
 # leaves to the checks below.
+class _LongWay:
+    """In place of the module where it could not be built: leaves every call."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+_LONG_WAY = _LongWay()
 _calls = None
+
+
+def _short_way():
+    global _calls
+    if os.path.exists(CALLS_PATH):
+        return _bind_calls()
+    warnings.warn(f"{CALLS_PATH} is missing (build() compiles it): calls go through ctypes",
+                  RuntimeWarning, stacklevel=3)
+    _calls = _LONG_WAY
+    return _calls
 
 
 def _bind_calls():
@@ -473,7 +524,7 @@ def _bind_calls():
     import torch
     h = lib()
     with _lock:
-        if _calls is None:
+        if _calls is None or _calls is _LONG_WAY:
             if not os.path.exists(CALLS_PATH):
                 raise QmoeError(ERR_CUDA, f"{CALLS_PATH} is missing: run moe_ffn_gb300.build()")
             spec = importlib.util.spec_from_file_location("moe_ffn_gb300._calls", CALLS_PATH)
@@ -499,7 +550,7 @@ def moe_route(ltype: int, logits, n_tokens: int, num_experts: int, top_k: int, t
               renormalize: bool = True, ldl=None, stream=None) -> None:
     """topk_idx, topk_w = the top-k experts of each token's logits and their softmax
     weights (see include/qmoe.h)."""
-    if ldl is None and _answered((_calls or _bind_calls()).route(
+    if ldl is None and _answered((_calls or _short_way()).route(
             ltype, logits, n_tokens, num_experts, top_k, topk_idx, topk_w,
             0 if renormalize else ROUTE_NO_RENORM, stream)):
         return
@@ -518,7 +569,7 @@ def moe_route_backward(ltype: int, logits, n_tokens: int, num_experts: int, top_
                        topk_w, grad_w, grad_logits, renormalize: bool = True, ldl=None, ldg=None,
                        stream=None) -> None:
     """grad_logits from the gradient of moe_route's weights (see include/qmoe.h)."""
-    if ldl is None and ldg is None and _answered((_calls or _bind_calls()).route_backward(
+    if ldl is None and ldg is None and _answered((_calls or _short_way()).route_backward(
             ltype, logits, n_tokens, num_experts, top_k, topk_idx, topk_w, grad_w, grad_logits,
             0 if renormalize else ROUTE_NO_RENORM, stream)):
         return
@@ -548,7 +599,7 @@ def moe_permute_workspace_size(n_tokens: int, num_experts: int, top_k: int) -> i
 def moe_permute(xtype: int, x, n_tokens: int, cols: int, topk_idx, num_experts: int, top_k: int,
                 rows, offsets, pos, ws, ldx=None, ldr=None, ws_bytes=None, stream=None) -> None:
     """rows[pos[t][s]] = x[t], the rows sorted by expert (see include/qmoe.h)."""
-    if ldx is None and ldr is None and ws_bytes is None and _answered((_calls or _bind_calls()).permute(
+    if ldx is None and ldr is None and ws_bytes is None and _answered((_calls or _short_way()).permute(
             xtype, x, n_tokens, cols, topk_idx, num_experts, top_k, rows, offsets, pos, ws, stream)):
         return
     fn = "moe_permute"
@@ -573,7 +624,7 @@ def moe_permute(xtype: int, x, n_tokens: int, cols: int, topk_idx, num_experts: 
 def moe_combine(ytype: int, y, n_rows: int, cols: int, pos, topk_w, n_tokens: int, top_k: int,
                 otype: int, residual, out, ldy=None, ldo=None, stream=None) -> None:
     """out[t] = residual[t] + sum_s topk_w[t][s] y[pos[t][s]] (see include/qmoe.h)."""
-    if ldy is None and ldo is None and _answered((_calls or _bind_calls()).combine(
+    if ldy is None and ldo is None and _answered((_calls or _short_way()).combine(
             ytype, y, n_rows, cols, pos, topk_w, n_tokens, top_k, otype, residual, out, stream)):
         return
     fn = "moe_combine"
@@ -593,7 +644,7 @@ def moe_combine_backward(ytype: int, y, n_rows: int, cols: int, pos, topk_w, n_t
                          top_k: int, otype: int, grad_out, grad_y, grad_w, ldy=None, ldo=None,
                          ldg=None, stream=None) -> None:
     """grad_y and grad_w (either may be None) of moe_combine (see include/qmoe.h)."""
-    if ldy is None and ldo is None and ldg is None and _answered((_calls or _bind_calls()).combine_backward(
+    if ldy is None and ldo is None and ldg is None and _answered((_calls or _short_way()).combine_backward(
             ytype, y, n_rows, cols, pos, topk_w, n_tokens, top_k, otype, grad_out, grad_y, grad_w,
             stream)):
         return
@@ -618,7 +669,7 @@ def w4_mm(W, stype: int, scale, zero, scale_cols: int, rows: int, cols: int, xty
           n_tokens: int, ytype: int, y, ldx=None, ldy=None, stream=None) -> None:
     """y = x W^T with 4-bit weights, a scale and zero point per scale_cols columns (see
     include/qmoe.h)."""
-    if ldx is None and ldy is None and _answered((_calls or _bind_calls()).w4(
+    if ldx is None and ldy is None and _answered((_calls or _short_way()).w4(
             W, stype, scale, zero, scale_cols, -1, rows, cols, xtype, x, n_tokens, None, ytype, y,
             stream)):
         return
@@ -641,7 +692,7 @@ def w4_mm_grouped(W, stype: int, scale, zero, scale_cols: int, num_groups: int, 
                   ldy=None, stream=None) -> None:
     """y[r] = W_g x[r] for the rows of every group, with 4-bit weights (see
     include/qmoe.h)."""
-    if ldx is None and ldy is None and _answered((_calls or _bind_calls()).w4(
+    if ldx is None and ldy is None and _answered((_calls or _short_way()).w4(
             W, stype, scale, zero, scale_cols, num_groups, rows, cols, xtype, x, n_rows, offsets,
             ytype, y, stream)):
         return
