@@ -516,13 +516,15 @@ qmoe_status moe_combine_backward(int ytype, const void* y, int64_t n_rows, int64
  *   ytype, y    as f8_mm
  * Products of (code - zero) and x are exact, sums and scales f32, and y is
  * rounded once.  The sum of |code - zero| |x| over the columns of one scale has to
- * stay below 2^128, whatever the scale makes of it, and an x below 2^-100 may lose
- * bits to f32's subnormal range.  A NaN or infinite x or scale makes its own row or
- * column of y what the formula gives.  Few tokens run a kernel that decodes the
- * weights in registers, many one on the tensor cores with tiles of 64 tokens, which
- * reads the weights again for every 64.  Same inputs, same bits; the bits of a token
- * may differ between calls of other sizes.  Errors as f8_quantize; QMOE_ERR_TIMEOUT
- * from qmoe_device_status as f8_mm. */
+ * stay below 2^128, whatever the scale makes of it; an x below 2^-100, and a product
+ * of a scale and its columns' sum below 2^-110, may lose bits to f32's subnormal
+ * range.  A NaN or infinite x or scale makes its own row or column of y what the
+ * formula gives, but an infinite scale counts as NaN (which the formula gives too,
+ * unless all of that scale's terms are of one sign and not 0).  Few tokens run a
+ * kernel that decodes the weights in registers, many one on the tensor cores with
+ * tiles of 64 tokens, which reads the weights again for every 64.  Same inputs, same
+ * bits; the bits of a token may differ between calls of other sizes.  Errors as
+ * f8_quantize; QMOE_ERR_TIMEOUT from qmoe_device_status as f8_mm. */
 qmoe_status w4_mm(const void* W, int stype, const void* scale, const uint8_t* zero,
                   int32_t scale_cols, int64_t rows, int64_t cols, int xtype, const void* x,
                   int64_t n_tokens, int64_t ldx, int ytype, void* y, int64_t ldy, void* stream);

@@ -55,10 +55,14 @@ __device__ __forceinline__ void cluster_st_f32(float* p, uint32_t rank, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ float typed(uint32_t raw, int type) {
-    return type == QMOE_F32    ? __uint_as_float(raw)
-           : type == QMOE_BF16 ? __uint_as_float(raw << 16)
-                               : __half2float(__ushort_as_half(static_cast<unsigned short>(raw)));
+// A scale as f32.  The formula multiplies every weight by it, so an infinite one makes
+// infinities of both signs or NaN (a code at its zero point) of them, and NaN of their sum;
+// here it meets the sum (for an f32 x those of its three parts), so it is taken as NaN.
+__device__ __forceinline__ float scale_value(uint32_t raw, int type) {
+    const float s = type == QMOE_F32    ? __uint_as_float(raw)
+                    : type == QMOE_BF16 ? __uint_as_float(raw << 16)
+                                        : __half2float(__ushort_as_half(static_cast<unsigned short>(raw)));
+    return fmaf(s, 0.f, s);
 }
 __device__ __forceinline__ uint32_t load_raw(const void* p, int64_t i, int type) {
     return type == QMOE_F32 ? __ldcg(static_cast<const unsigned*>(p) + i)
@@ -492,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < NS; ++j) {
-                    sc[h][j] = typed(s_raw[h][j], p.stype);
+                    sc[h][j] = scale_value(s_raw[h][j], p.stype);
                     zb[h][j] = Magic<H>::bias(z_raw[h][j]);
                 }
             const bool last = round + 1 == rounds;

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
                             const int at = (s * 4 + g) * MANY_ROWS + r0 + j * n;
-                            sc_s[at] = typed(v[g], p.stype);
+                            sc_s[at] = scale_value(v[g], p.stype);
                             sc_z[at] = static_cast<uint16_t>(Magic<H>::bias(zero[j] >> (8 * g)));
                         }
                     }

@@ -37,3 +37,36 @@ def test_f32_rows_keep_every_bit(qm, m, n, k, S):
     assert qm.device_status() == qm.OK
     factor = code[:, at].T.astype(np.float64) - zero[:, at // S].T
     assert np.array_equal(y.cpu().numpy(), (factor * value[:, None]).astype(np.float32))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(3, 40, 256), (16, 4096, 4096), (40, 4096, 4096),
+                                   (130, 5000, 1152)])
+def test_scales_do_what_the_formula_says(qm, m, n, k, kind):
+    """Small whole numbers, so that no sum rounds: powers of two down to 2^-100 scale exactly,
+    and infinite ones make their columns NaN, and no other (the formula's weights are then
+    infinities of both signs, and NaN where a code is at its zero point)."""
+    import torch
+    from tests.test_gpu_f8 import kinds
+    g = np.random.default_rng(m + k)
+    S = 64
+    q = g.integers(0, 256, (n, k // 2), dtype=np.uint8)
+    code = np.stack((q & 15, q >> 4), -1).reshape(n, k).astype(np.float64) - 8
+    x = g.integers(-2, 3, (m, k)).astype(np.float64)
+    x[1, :S] = 0
+    scale = np.full((n, k // S), 2.0 ** -100)
+    scale[7, 0], scale[20, 1], scale[30, :2] = np.inf, -np.inf, np.inf
+    s = torch.from_numpy(scale.astype(np.float32)).cuda()
+    got_dt, dt = kinds(qm)[kind]
+    y = torch.full((m, n), 55.0, device="cuda")
+    qm.w4_mm(torch.from_numpy(q).cuda(), qm.F32, s, None, S, n, k, got_dt,
+             torch.from_numpy(x.astype(np.float32)).to(dt).cuda(), m, qm.F32, y)
+    assert qm.device_status() == qm.OK
+    with np.errstate(invalid="ignore"):
+        w = np.repeat(scale, S, 1) * code
+        want = x @ np.delete(w, [7, 20, 30], 0).T
+        for row in (7, 20, 30):
+            assert np.isnan(x @ w[row]).all()
+            want = np.insert(want, row, np.nan, 1)
+    got = y.cpu().numpy().astype(np.float64)
+    assert np.array_equal(got, want, equal_nan=True)
