@@ -12,6 +12,7 @@
 #include "host.cuh"
 #include "w4.cuh"
 #include "w4_many.cuh"
+#include "w4_rule.cuh"
 
 namespace qmoe {
 
@@ -180,30 +181,11 @@ static qmoe_status launch_many(w4::Params p, const DevInfo& d, cudaStream_t st) 
     return QMOE_OK;
 }
 
-// Whether the kernel for many rows takes a call.  It reads each weight once for 64 rows
-// and starts slowly, about 10 us; the other reads it again for every 16 (5 of f32) and
-// starts in 4, but its time grows with the rows: by 0.33 us for each row of a group per
-// 2^24 weights, 0.2 where all rows share one matrix, against 2.2 and 1.7 for the weights
-// themselves (2.7 in the kernel for many).  So it depends on the weights that have rows
-// and on the rows per group.  us, few / many: one matrix, 4096 x 4096, 16 / 32 / 64 rows
-// 11.8 / 15.9 / 23.8 against 14.0 / 15.2 / 17.9; 14336 x 4096, 8 / 16 / 32 rows 15.0 / 20.5 /
-// 33.0 against 20.4 / 21.3 / 23.5; 768 x 2048, 64 rows 8.0 against 12.6; 64 groups, 1024 x
-// 2048, 2 / 4 / 8 / 16 rows each 26.8 / 31.3 / 42.2 / 65.1 against 31.8 / 31.8 / 32.1 / 32.3;
-// 8 groups, 16 / 32 rows each 11.0 / 19.7 against 12.0 / 16.2.  f32: 14336 x 4096, 8 / 16 rows
-// 27.3 / 50.6 against 32.6 / 35.9; 64 groups, 4 / 8 rows each 41.5 / 79.1 against 55.8 / 56.3.
-static bool many_rows(const w4::Params& p, bool f32) {
-    const double groups = std::min(p.M, p.E);
-    const double rows = p.M / groups;
-    const double weights = groups * p.N * p.K / 16777216.0;
-    if (p.E > 1) return (rows - 2) * weights > 18;
-    return (rows * (f32 ? 1.25 : 1.0) - 5) * weights > 30;
-}
-
 template <class X, int S>
 static qmoe_status launch_rows(const w4::Params& p, const DevInfo& d, cudaStream_t st) {
     constexpr int one = std::is_same<X, float>::value ? 2 : 8;  // tokens of one column block
     const int64_t groups = std::min(p.M, p.E);
-    if (many_rows(p, std::is_same<X, float>::value)) {
+    if (w4::many_rows(p.M, p.E, p.N, p.K, std::is_same<X, float>::value)) {
         if constexpr (!std::is_same<X, float>::value)
             if (p.vec_x) return launch_many<w4::Many<X, S, true>>(p, d, st);
         return launch_many<w4::Many<X, S, false>>(p, d, st);
