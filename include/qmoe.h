@@ -409,10 +409,12 @@ qmoe_status moe_experts_f8(const void* gate_stack, const float* gate_scale, cons
  * The steps of an MoE layer around its experts' products, with their gradients,
  * and products with 4-bit weights.  The pages have no counterpart of these
  * calls; the conventions are those of the section above.  With them
- *   moe_route -> moe_permute -> mm_grouped or w4_mm_grouped (gate, up; down)
- *   -> moe_combine
- * is a layer for weights that moe_ffn does not take; moe_route also makes the
- * routes that moe_experts_f8 asks for.  Limits common to the steps: num_experts
+ *   moe_route -> moe_permute -> mm_grouped or w4_mm_grouped (gate, up) -> the
+ *   caller's activation -> the same product (down) -> moe_combine
+ * a caller makes a layer for weights that moe_ffn does not take; moe_route also
+ * makes the routes that moe_experts_f8 asks for.  The products are forward only:
+ * the gradient of x of mm_grouped is mm_grouped with a transposed copy of the
+ * stack, that of w4_mm and w4_mm_grouped cannot be had from these calls.  Limits common to the steps: num_experts
  * <= 1024, top_k <= 16, n_tokens * top_k <= 2^25, cols <= 2^20. */
 
 /* Routes from the router's logits, by moe_ffn's rule (see there for ties and
@@ -436,7 +438,8 @@ qmoe_status moe_route(int ltype, const void* logits, int64_t n_tokens, int32_t n
  * moe_route wrote them.  With c = sum_s w_s grad_w_s over the token's slots:
  *   renormalised   grad_logits[e_s] = w_s (grad_w_s - c), 0 elsewhere
  *   NO_RENORM      grad_logits[e] = p_e (grad_w_s [e = e_s] - c), p formed again
- *                  from the logits (which the renormalised form does not read)
+ *                  from the logits (which the renormalised form does not read,
+ *                  but they may not be null there either)
  * in f32, rounded once to ltype.  Every element of the [n_tokens][num_experts]
  * gradient (rows ldg apart) is written.  A slot whose expert lies outside
  * [0, num_experts) adds nothing; an expert that two slots name takes both. */
