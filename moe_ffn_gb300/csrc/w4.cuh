@@ -42,8 +42,7 @@ struct Params {
     DevCtl* err;
 };
 
-// A barrier over the cluster's threads in two steps that orders no memory: once it is
-// passed every CTA of the cluster has started, so its shared memory may be written.
+// A barrier over the cluster's threads, in two steps, that orders no memory.
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
@@ -282,8 +281,6 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     const int lg = 31 - __clz(ranks);
     const int cluster = blockIdx.x >> lg, clusters = gridDim.x >> lg;
     const int kw = warp >> p.rts_log, rts = 1 << p.rts_log, rt = warp & (rts - 1);
-    // (waited for before the first store to another CTA, when all have long started)
-    if (ranks > 1) cluster_arrive();
     int* t_lo = reinterpret_cast<int*>(smem);
     int* t_hi = t_lo + p.E;
     int* t_pre = t_hi + p.E;
@@ -323,15 +320,20 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
     };
     // (what does not depend on earlier launches comes before the wait for them)
     if (!p.offsets) look_up(cluster);
+    // All CTAs of the cluster run from here on, so that their shared memory may be written.
+    // (In this place it costs a call at most 1%; split in two, or in the tiles' loop before
+    // the first store, it cost calls without clusters too 1 to 6%, by another allocation of
+    // registers.)
+    if (ranks > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
     pdl_wait();
     pdl_trigger();
     if (p.offsets) {
         gmm::build_tables(p, p.nt, p.nb, t_lo, t_hi, t_pre);
         tiles = t_pre[p.E];
-        if (cluster >= tiles) {
-            if (ranks > 1) cluster_wait();
-            return;
-        }
+        if (cluster >= tiles) return;
     }
     // the first unit of this warp's block of a round, and whether the block is whole
     auto block_at = [&](int round) { return ub + (round << kw_shift) + kw * BLOCK; };
@@ -526,7 +528,6 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Params p) {
         }
         __syncthreads();
         const int shift = 4 + p.rts_log, rows16 = 16 << p.rts_log;
-        if (ranks > 1 && tile == cluster) cluster_wait();
         for (int i = tid; i < rows16 * c.nv; i += THREADS) {
             const int row = i & (rows16 - 1), tok = i >> shift;
             const float* at = red + ((buf * WARPS + (row >> 4)) * 8 * NB + tok * PARTS) * RED_LD + (row & 15);

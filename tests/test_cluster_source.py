@@ -32,17 +32,10 @@ def test_no_cta_touches_another_before_it_is_known_to_run():
     assert found == {"f8moe.cuh", "gmm.cuh", "gmm_pair.cuh", "w4.cuh", "w4_many.cuh"}
 
 
-def test_split_barriers_are_paired_on_every_way_out():
-    """Whoever arrives at a split cluster barrier also waits for it, before an early return
-    too, and under the same condition."""
+def test_barriers_in_two_steps_are_paired():
+    """Whoever arrives also waits, at once and under the same condition."""
     for name, k in kernels():
-        if "cluster_arrive();" not in k:
-            continue
-        assert k.count("cluster_arrive();") == 1 == k.count("if (ranks > 1) cluster_arrive();")
-        body = k[k.index("cluster_arrive();"):]
-        for way_out in re.findall(r"\{([^{}]*)return; \}", body):
-            assert "if (ranks > 1) cluster_wait();" in way_out, (name, way_out)
-        assert not re.search(r"\) return;", body), name
-        # the first tile, which every cluster that stays has, waits before its first store
-        assert "if (ranks > 1 && tile == cluster) cluster_wait();" in k, name
-        assert k.index("tile == cluster) cluster_wait();") < re.search(REMOTE, k).start()
+        if "cluster_arrive();" in k or "cluster_wait();" in k:
+            for half in ("cluster_arrive();", "cluster_wait();"):
+                assert k.count(half) == 1, name
+            assert "if (ranks > 1) { cluster_arrive(); cluster_wait(); }" in k, name
