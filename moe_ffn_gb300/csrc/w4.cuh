@@ -222,10 +222,11 @@ __device__ __forceinline__ void pack_x(const Raw8<X>& v,
 // 128 the four lanes of a row hold 32 columns each; for 64 and 32 they first exchange
 // words.
 //
-// Bound by instructions, not by HBM, once the loads run: a unit (32 codes a lane, 8 MMAs)
-// takes a scheduler 158 clocks in a probe of the loop alone, which makes about half of a
-// call; the rest goes to starts, tile changes and sums.  Measured: 14336 x 4096, one row
-// 10.7 us (2.9 TB/s), five rows 12.6; 4096 x 4096, one row 5.5 us cold (by clock stamps
+// No pipe is full (14336 x 4096, five rows: issue 54%, ALU 44%, tensor 11%, DRAM 23%).  A unit
+// (32 codes a lane, 8 MMAs) takes a scheduler 158 clocks in a probe of the loop alone, which
+// makes about half of a call; the other half, starts, tile changes and sums, was not
+// measured apart.  Measured: 14336 x 4096, one row
+// 10.9 us (2.8 TB/s), five rows 12.7; 4096 x 4096, one row 5.5 us cold (by clock stamps
 // about 2 us before the first product, 1.3 for the products, 0.4 for the sum); eight
 // groups of one row, 768 x 2048 5.6 us.  With three shifts and four subtractions a word
 // of codes, and a table of groups where there are none, 14336 x 4096 took one row 13.4 us.

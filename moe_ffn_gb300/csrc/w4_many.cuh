@@ -16,8 +16,9 @@
 // Bound by the steps between the roles and by instruction issue (67%), not by the tensor
 // cores (19% busy) or HBM: a k-block takes about 1,100 clocks of handing over with no
 // work in it, 1,450 with.  Measured: 64 groups of 64 rows, 1024 x 2048, 37.5 us (460
-// TFLOP/s, 1.9 TB/s), of 16 rows 32.8; 4096 rows in 64 uneven groups 49 us (370 tiles on
-// 152 SMs are three rounds, the last of them 43% full); 14336 x 4096, 64 rows 27.7 us.
+// TFLOP/s, 1.9 TB/s), of 16 rows 32.8; 4096 rows in 64 uneven groups 50 us (370 tiles on
+// 152 SMs are three rounds, the last of them 43% full); 14336 x 4096, 64 rows 27.8 us, 4096
+// rows 665 us (723 TFLOP/s: every weight is decoded again for each 64 rows; f32 rows 2.2 ms).
 // Without the products of one part (timing only, 38.3 us whole): MMAs 37.8, sums 30.3,
 // codes 35.4, all three 26.4, the copies too 22.7.
 #pragma once
