@@ -414,8 +414,9 @@ qmoe_status moe_experts_f8(const void* gate_stack, const float* gate_scale, cons
  * a caller makes a layer for weights that moe_ffn does not take; moe_route also
  * makes the routes that moe_experts_f8 asks for.  The products are forward only:
  * the gradient of x of mm_grouped is mm_grouped with a transposed copy of the
- * stack, that of w4_mm and w4_mm_grouped cannot be had from these calls.  Limits common to the steps: num_experts
- * <= 1024, top_k <= 16, n_tokens * top_k <= 2^25, cols <= 2^20. */
+ * stack, that of w4_mm and w4_mm_grouped cannot be had from these calls.  Limits
+ * common to the steps: num_experts <= 1024, top_k <= 16, n_tokens * top_k <= 2^25,
+ * cols <= 2^20. */
 
 /* Routes from the router's logits, by moe_ffn's rule (see there for ties and
  * logits that are not finite): p = softmax over the experts, the top_k largest,

@@ -15,9 +15,9 @@ namespace w4 {
 // the rows of a matrix count times N (K + 768)^1.5, over the matrices that have rows; how
 // the rows spread over them is known on the device only, so the average stands for it.
 //
-// The constants are those that lose least over 882 cases timed with both kernels
-// (profiles/w4_kernel_times.json): 1.0% a case with one matrix (f32 0.4%), 1.2% with
-// groups (f32 2.4%).  us, few / many: one matrix, 4096 x 4096, 16 / 24 / 48 rows 11.1 / 14.0 /
+// The constants are fitted to 882 cases timed with both kernels
+// (profiles/w4_kernel_times.json), over which the choice loses 1.0% a case with one matrix
+// (f32 0.4%), 1.2% with groups (f32 2.4%).  us, few / many: one matrix, 4096 x 4096, 16 / 24 / 48 rows 11.1 / 14.0 /
 // 28.1 against 14.2 / 15.2 / 16.5; 14336 x 4096, 8 / 12 / 24 rows 14.6 / 18.2 / 30.5 against
 // 21.1 / 21.9 / 23.0; 768 x 2048, 128 / 384 rows 9.2 / 17.1 against 12.8 / 13.7; 16384 x 128, 32 / 64
 // rows 4.7 / 8.3 against 6.9 / 7.2; 64 groups, 1024 x 2048, 2 / 8 rows each 27.7 / 39.5 against

@@ -57,3 +57,20 @@ def test_more_rows_never_go_back(many, kind):
         for n, k in ((300, 640), (4096, 4096), (14336, 4096), (1024, 128), (1 << 20, 32)):
             picks = [many(m * e, e, n, k, kind) for m in range(1, 600)]
             assert picks == sorted(picks)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_gpu_tests_reach_the_kernel_they_are_for(many, kind):
+    """The shapes by which tests/test_gpu_w4*.py mean one kernel or the other."""
+    from tests.test_gpu_w4 import MANY
+    for m, n, k, _ in MANY + [(500, 1280, 1024, 64), (500, 2048, 1024, 128), (64, 4096, 4096, 128),
+                              (600, 8000, 1024, 128), (300, 9000, 1024, 128)]:
+        assert many(m, 1, n, k, kind), (m, n, k)
+    uneven = 3 + sum([150, 1, 64, 65, 129, 7, 300, 63, 2, 200]) + 5
+    assert many(uneven, 14, 520, 1024, kind) and many(uneven, 14, 768, 672, kind)
+    for m, n, k in ((1, 4096, 4096), (5, 48, 14336), (64, 16, 4096),
+                    (4 if kind == "f32" else 8, 4096, 14336), (16, 4096, 4096), (13, 1000, 5120),
+                    (70, 200, 512)):
+        assert not many(m, 1, n, k, kind), (m, n, k)
+    for m, e, n, k in ((8, 128, 768, 2048), (12, 4, 200, 6144), (9, 9, 100, 256)):
+        assert not many(m, e, n, k, kind), (m, e, n, k)
