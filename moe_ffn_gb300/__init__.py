@@ -725,8 +725,8 @@ def set_exec_mode(mode: int) -> None:
 def set_fault_injection(wait_limit_ns: int = 0, skip_arrive_cta: int = -1) -> None:
     """Failure-path tests only: shorten every bounded device wait and make one
     CTA of the cooperative kernels skip its grid-barrier arrivals, or one of the
-    e4m3, bf16 and f16 products load nothing; (0, -1) restores normal operation
-    (see include/qmoe.h)."""
+    e4m3, bf16 and f16 products, or of the 4-bit products for many rows, load
+    nothing; (0, -1) restores normal operation (see include/qmoe.h)."""
     _check(lib().qmoe_set_fault_injection(wait_limit_ns, skip_arrive_cta))
 
 
